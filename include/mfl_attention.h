@@ -1,0 +1,143 @@
+/*
+ * mfl_attention.h — C ABI of attention: the back-to-back GEMM of
+ * mfl_chain.h with the softmax between its products, for packed sequences
+ * with grouped heads, its gradients, and its form for decoding behind a
+ * shared prefix.
+ *
+ * For query token t and query head h of a sequence with lq query tokens and
+ * lk keys, kv head g = h / (heads_q / heads_kv):
+ *
+ *   s_j   = scale * sum_d q(t, h, d) k(j, g, d)        over the visible keys j
+ *   lse   = log sum_j exp(s_j)
+ *   out_d = sum_j exp(s_j - lse) v(j, g, d)
+ *
+ * causal: t sees keys j <= t + lk - lq (both counted from 0 in the sequence:
+ * the last query token sees every key); otherwise every key of the sequence.
+ * A query that sees no key has out = 0 and lse = -infinity.
+ *
+ * Types.  Inputs, out and gradients are all MFL_F16 or all MFL_BF16.  Scores,
+ * maxima, sums and accumulators are fp32; the weights are rounded once (to
+ * nearest even) to the input type as the second product's operand, results
+ * once at the end.  lse is fp32.
+ *
+ * Addressing (elements): x(t, h, d) = X[t * x_token + h * x_head + d].  Every
+ * pointer is 16-byte aligned and every stride a multiple of 8 (else
+ * MFL_E_MISALIGNED); strides are not negative, 0 lets an input be shared.
+ * head_dim is a multiple of 8 up to 256 (else MFL_E_UNSUPPORTED).
+ *
+ * Packed sequences.  seq_q and seq_k hold batch + 1 offsets each in device
+ * memory, the first of them 0, growing: sequence s owns query tokens
+ * seq_q[s] .. seq_q[s+1] - 1 and keys seq_k[s] .. seq_k[s+1] - 1; lengths of
+ * 0 are allowed.  Both NULL: one sequence.  The offsets are read by the
+ * kernels and held inside [0, total_q] and [0, total_k] whatever they are.
+ * Query tokens behind the last sequence are no rows: their out and lse stay
+ * as they were, their gradients are set to 0.
+ *
+ * Values of keys outside a sequence never reach it, whatever they are.  A
+ * key inside it whose v holds infinities or NaNs can make NaN of out in the
+ * rows the causal mask hides it from: a weight of 0 times NaN.
+ *
+ * Ownership and execution are gemm_tn's (mfl_gemm.h): nothing is allocated,
+ * kept or synchronised; work runs on `stream`.  A workspace belongs to one
+ * call until that call's work is done; its size comes from the *_plan
+ * function, which makes the same checks without touching the GPU.  Outputs
+ * must not overlap inputs or the workspace.  Results are the same bits for
+ * the same arguments: no sum depends on the order workgroups run in.
+ */
+#ifndef MFL_ATTENTION_H
+#define MFL_ATTENTION_H
+
+#include <stdint.h>
+
+#include "mfl_gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MFL_BF16 3            /* mfl_dtype of these functions, beside MFL_F16 */
+#define MFL_E_WORKSPACE (-10) /* workspace NULL, misaligned or too small */
+
+/* Kernel of the forward functions: AUTO chooses by sizes.  TALL: 8 or 4
+ * waves of 32 rows (a row is a token of one query head) share each chunk of
+ * keys; FLAT: 32 rows per workgroup, whose waves take turns over the keys. */
+#define MFL_ATTENTION_AUTO 0
+#define MFL_ATTENTION_TALL 1
+#define MFL_ATTENTION_TALL_4 2
+#define MFL_ATTENTION_FLAT 3
+
+typedef struct {
+  int32_t dtype;                /* MFL_F16 or MFL_BF16 */
+  int32_t causal;               /* 0 or 1 */
+  int64_t batch;                /* sequences, >= 1 */
+  int64_t total_q, total_k;     /* tokens of q and out, of k and v */
+  int64_t heads_q, heads_kv;    /* heads_q a multiple of heads_kv */
+  int64_t head_dim;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
+  float scale;                  /* > 0, finite */
+  int32_t algo;                 /* MFL_ATTENTION_* */
+  int32_t splits;               /* parts the keys are split into, 0: by sizes */
+} mfl_attention_t;
+
+/* out, and lse (total_q x heads_q, contiguous) unless NULL. */
+int attention_packed(const mfl_attention_t* a, const void* q, const void* k, const void* v,
+                     const int32_t* seq_q, const int32_t* seq_k, void* out, float* lse,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+/* the same checks; on success the kernel, the splits and the workspace's size
+ * (0: none needed).  Any out pointer may be NULL. */
+int attention_packed_plan(const mfl_attention_t* a, const void* q, const void* k, const void* v,
+                          const int32_t* seq_q, const int32_t* seq_k, const void* out,
+                          const float* lse, int32_t* algo, int32_t* splits,
+                          int64_t* workspace_bytes);
+
+/* Gradients of sum(out * dout) with respect to q, k and v, from the forward
+ * call's out and lse; `f` as in that call (algo and splits are not read). */
+typedef struct {
+  mfl_attention_t f;
+  int64_t dout_token, dout_head, dq_token, dq_head, dk_token, dk_head, dv_token, dv_head;
+} mfl_attention_grad_t;
+
+int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, const void* q,
+                              const void* k, const void* v, const void* out, const float* lse,
+                              const int32_t* seq_q, const int32_t* seq_k, void* dq, void* dk,
+                              void* dv, void* workspace, int64_t workspace_bytes, void* stream);
+int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* dout,
+                                   const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const int32_t* seq_q, const int32_t* seq_k,
+                                   const void* dq, const void* dk, const void* dv,
+                                   int64_t* workspace_bytes);
+
+/* Decoding behind a shared prefix: `batch` sequences of q_tokens query
+ * tokens each.  Every query sees all `prefix` keys of prefix_k / prefix_v;
+ * query token t of sequence b also sees the keys j <= lengths[b] - q_tokens + t
+ * of its own cache k(b, j, g, d) = K[b * k_batch + j * k_token + g * k_head + d],
+ * which holds lengths[b] keys (device memory, held inside [0, capacity]), the
+ * new tokens' among them.  Prefix keys are read once for all sequences. */
+typedef struct {
+  int32_t dtype;
+  int32_t algo;                 /* of the prefix's part; the own keys' is FLAT */
+  int64_t batch, q_tokens;
+  int64_t prefix, capacity;
+  int64_t heads_q, heads_kv, head_dim;
+  int64_t q_batch, q_token, q_head, prefix_k_token, prefix_k_head, prefix_v_token,
+      prefix_v_head;
+  int64_t k_batch, k_token, k_head, v_batch, v_token, v_head, out_batch, out_token, out_head;
+  float scale;
+  int32_t splits_prefix, splits_own;   /* 0: by sizes */
+} mfl_attention_prefix_t;
+
+/* lse: batch x q_tokens x heads_q, contiguous, or NULL */
+int attention_prefix(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,
+                     const void* prefix_v, const void* k, const void* v, const int32_t* lengths,
+                     void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+int attention_prefix_plan(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,
+                          const void* prefix_v, const void* k, const void* v,
+                          const int32_t* lengths, const void* out, const float* lse,
+                          int32_t* algo, int32_t* splits_prefix, int32_t* splits_own,
+                          int64_t* workspace_bytes);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* MFL_ATTENTION_H */

@@ -1,8 +1,8 @@
 """Python binding of the MI355X fp16 TN GEMM library (libmfl_gemm.so).
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels
-behind the C ABI declared in include/mfl_gemm.h, include/mfl_layout.h and
-include/mfl_probe.h.  PyTorch provides device memory and the current stream.
+behind the C ABI declared in include/mfl_gemm.h, include/mfl_chain.h,
+include/mfl_attention.h, include/mfl_layout.h and include/mfl_probe.h.  PyTorch provides device memory and the current stream.
 There is no fallback: if the library is missing, importing this package
 raises.
 
@@ -19,6 +19,10 @@ from typing import Optional, Tuple
 # library binds to, so device pointers and streams are shared.
 import torch  # noqa: E402
 import numpy as np
+
+from . import _attention
+from ._attention import (ATTENTION_ALGOS, BF16, AttentionArgs, AttentionGradArgs,  # noqa: F401
+                         AttentionPrefixArgs)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmfl_gemm.so")
@@ -48,6 +52,7 @@ ERRORS = {
     0: "MFL_OK", -1: "MFL_E_NEGATIVE_DIM", -2: "MFL_E_LEADING_DIM", -3: "MFL_E_NULL_POINTER",
     -4: "MFL_E_UNSUPPORTED", -5: "MFL_E_LAUNCH", -6: "MFL_E_ALGO_CASE",
     -7: "MFL_E_MISALIGNED", -8: "MFL_E_ALIAS", -9: "MFL_E_TOO_LARGE",
+    -10: "MFL_E_WORKSPACE",
 }
 ERR = {v.replace("MFL_E_", "").replace("MFL_", ""): k for k, v in ERRORS.items()}
 
@@ -143,6 +148,7 @@ def _load() -> ctypes.CDLL:
     lib.mfl_bench_lds_read.restype = ctypes.c_int
     lib.mfl_wall_clock_khz.argtypes = [P(i32)]
     lib.mfl_wall_clock_khz.restype = ctypes.c_int
+    _attention.declare(lib)
     return lib
 
 
@@ -250,6 +256,10 @@ def gemm_tn(A: torch.Tensor, B: torch.Tensor, C: Optional[torch.Tensor] = None,
                      None if C is None else C.data_ptr(), ldc, D.data_ptr(), ldd, dt, stream)
     _check(rc)
     return D
+
+
+# ------------------------------------------------------------ attention
+attention, attention_plan, attention_backward, attention_prefix = _attention.bind(_lib, _check)
 
 
 # ------------------------------------------------------- back-to-back GEMM

@@ -1,0 +1,512 @@
+// C ABI of attention (mfl_attention.h): argument checks, choice of kernel and
+// splits, launches.
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/mfl_attention.h"
+#include "attention.hpp"
+#include "attention_bwd.hpp"
+#include "attention_launch.hpp"
+
+namespace {
+
+using namespace mfl::att;
+
+constexpr int64_t kMaxCount = (int64_t)INT_MAX - (1 << 16);
+constexpr int64_t kMaxStride = (int64_t)1 << 40;   // elements; products with a count fit int64
+
+bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
+
+int check_strides(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides) {
+    if (s < 0) return MFL_E_LEADING_DIM;
+    if (s > kMaxStride) return MFL_E_TOO_LARGE;
+    if (s % 8) return MFL_E_MISALIGNED;
+  }
+  return MFL_OK;
+}
+
+// no two elements of an output share an address: sorted by stride, each
+// extent must reach past everything the smaller ones cover
+struct Axis {
+  int64_t count, stride;
+};
+int check_output(int64_t dim, Axis a, Axis b, Axis c) {
+  Axis x[3] = {a, b, c};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (x[j].stride < x[i].stride) {
+        const Axis t = x[i];
+        x[i] = x[j];
+        x[j] = t;
+      }
+  __int128 span = dim;
+  for (const Axis& y : x) {
+    if (y.count <= 1) continue;
+    if (y.stride < span) return MFL_E_ALIAS;
+    span += (__int128)(y.count - 1) * y.stride;
+  }
+  return MFL_OK;
+}
+
+int check_heads(int32_t dtype, int64_t batch, int64_t heads_q, int64_t heads_kv, int64_t dim,
+                float scale) {
+  if (heads_q < 0 || heads_kv < 0 || dim < 0 || batch < 0) return MFL_E_NEGATIVE_DIM;
+  if (dtype != MFL_F16 && dtype != MFL_BF16) return MFL_E_UNSUPPORTED;
+  if (batch == 0 || heads_kv == 0 || heads_q == 0 || heads_q % heads_kv) return MFL_E_UNSUPPORTED;
+  if (dim == 0 || dim % 8 || dim > 256) return MFL_E_UNSUPPORTED;
+  if (!(scale > 0.0f) || !isfinite(scale)) return MFL_E_UNSUPPORTED;
+  if (heads_q > (1 << 16) || batch > (1 << 24)) return MFL_E_TOO_LARGE;
+  return MFL_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t clamp(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
+
+// slots of `bm`-row tiles over the sequences (find_sequence)
+int64_t tile_slots(int64_t rows, int64_t batch, int64_t bm, bool packed) {
+  return packed ? rows / bm + batch : ceil_div(rows, bm);
+}
+
+struct Choice {
+  int algo;
+  int64_t splits, slots;
+};
+
+// Workgroups that fill the chip once: 256 CUs, one of the large-LDS kernels
+// each.
+constexpr int64_t kFill = 256;
+
+Choice choose(int64_t rows, int64_t batch, bool packed, int64_t keys, int64_t heads_kv, int dc,
+              int algo, int64_t splits) {
+  Choice c;
+  const int64_t mean_rows = ceil_div(rows, batch);
+  if (algo == MFL_ATTENTION_AUTO) {
+    if (mean_rows <= 32)
+      algo = MFL_ATTENTION_FLAT;
+    else if (dc == 256 || mean_rows <= 128 ||
+             tile_slots(rows, batch, 256, packed) * heads_kv < kFill)
+      algo = MFL_ATTENTION_TALL_4;
+    else
+      algo = MFL_ATTENTION_TALL;
+  }
+  c.algo = algo;
+  c.slots = tile_slots(rows, batch, tile_rows(algo), packed);
+  const int64_t units = ceil_div(ceil_div(keys, batch), algo == MFL_ATTENTION_FLAT ? 256 : 128);
+  if (splits == 0)
+    splits = clamp(kFill / (c.slots * heads_kv > 0 ? c.slots * heads_kv : 1), 1, clamp(units, 1, 64));
+  c.splits = splits;
+  return c;
+}
+
+int64_t partial_bytes(int64_t rows, int64_t splits, int dc) {
+  return splits > 1 ? splits * rows * (4 * (int64_t)dc + 8) : 0;
+}
+
+bool grid_fits(const Choice& c, int64_t heads_kv) {
+  return (__int128)c.slots * heads_kv * c.splits < INT_MAX;
+}
+
+int run(KernelRef k, int64_t blocks, void* params, void* stream) {
+  if (!k.fn) return MFL_E_UNSUPPORTED;
+  if (blocks == 0) return MFL_OK;
+  void* args[] = {params};
+  const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
+                                       (hipStream_t)stream);
+  return e == hipSuccess ? MFL_OK : MFL_E_LAUNCH;
+}
+
+int run_forward(FwdParams& p, const Choice& c, bool bf16, int dc, void* stream) {
+  p.splits = (int)c.splits;
+  p.slots = (int)c.slots;
+  return run(fwd_kernel(bf16, dc, c.algo), c.slots * p.heads_kv * c.splits, &p, stream);
+}
+
+int run_join(const FwdParams& p, int splits, bool bf16, int dc, void* stream) {
+  CombineParams j{};
+  j.part_o = p.part_o;
+  j.part_ml = p.part_ml;
+  j.o = p.o;
+  j.lse = p.lse;
+  j.rows = p.rows;
+  j.splits = splits;
+  j.dim = p.dim;
+  j.heads = p.heads_kv * p.group;
+  j.q_inner = p.q_inner;
+  j.o_batch = p.o_batch;
+  j.o_tok = p.o_tok;
+  j.o_head = p.o_head;
+  return run(join_kernel(bf16, dc), ceil_div(p.rows, 4), &j, stream);
+}
+
+int check_packed(const mfl_attention_t& a, const void* q, const void* k, const void* v,
+                 const int32_t* seq_q, const int32_t* seq_k, const void* out, const float* lse) {
+  if (a.total_q < 0 || a.total_k < 0) return MFL_E_NEGATIVE_DIM;
+  int rc = check_heads(a.dtype, a.batch, a.heads_q, a.heads_kv, a.head_dim, a.scale);
+  if (rc) return rc;
+  if ((a.causal != 0 && a.causal != 1) || a.algo < 0 || a.algo > MFL_ATTENTION_FLAT ||
+      a.splits < 0 || a.splits > 1024)
+    return MFL_E_UNSUPPORTED;
+  if (!seq_q != !seq_k) return MFL_E_NULL_POINTER;
+  if (!seq_q && a.batch != 1) return MFL_E_NULL_POINTER;
+  if (a.total_q > kMaxCount || a.total_k > kMaxCount || a.total_q * a.heads_q > kMaxCount)
+    return MFL_E_TOO_LARGE;
+  if (a.total_q > 0 && (!q || !out)) return MFL_E_NULL_POINTER;
+  if (a.total_q > 0 && a.total_k > 0 && (!k || !v)) return MFL_E_NULL_POINTER;
+  rc = check_strides({a.q_token, a.q_head, a.k_token, a.k_head, a.v_token, a.v_head, a.out_token,
+                      a.out_head});
+  if (rc) return rc;
+  if (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(out) || (uintptr_t)lse % 4 ||
+      (uintptr_t)seq_q % 4 || (uintptr_t)seq_k % 4)
+    return MFL_E_MISALIGNED;
+  if (out && (out == q || out == k || out == v)) return MFL_E_ALIAS;
+  return check_output(a.head_dim, {a.total_q, a.out_token}, {a.heads_q, a.out_head}, {1, 0});
+}
+
+int plan_packed(const mfl_attention_t& a, bool packed, Choice& c, int64_t& bytes) {
+  const int dc = dim_class(a.head_dim);
+  if (dc == 256 && a.algo == MFL_ATTENTION_TALL) return MFL_E_ALGO_CASE;
+  c = choose(a.total_q * (a.heads_q / a.heads_kv), a.batch, packed, a.total_k, a.heads_kv, dc,
+             a.algo, a.splits);
+  if (!grid_fits(c, a.heads_kv)) return MFL_E_TOO_LARGE;
+  bytes = partial_bytes(a.total_q * a.heads_q, c.splits, dc);
+  return MFL_OK;
+}
+
+int check_workspace(const void* workspace, int64_t have, int64_t need) {
+  if (need == 0) return MFL_OK;
+  return !workspace || !aligned(workspace) || have < need ? MFL_E_WORKSPACE : MFL_OK;
+}
+
+// the partial rows, then the (maximum, sum) pairs
+void place_partials(FwdParams& p, void* workspace, int64_t splits, int dc) {
+  p.part_o = (float*)workspace;
+  p.part_ml = (float2*)((char*)workspace + 4 * splits * p.rows * dc);
+}
+
+int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* q, const void* k,
+                   const void* v, const void* out, const float* lse, const int32_t* seq_q,
+                   const int32_t* seq_k, const void* dq, const void* dk, const void* dv) {
+  mfl_attention_t f = a.f;
+  f.algo = MFL_ATTENTION_AUTO;
+  f.splits = 0;
+  int rc = check_packed(f, q, k, v, seq_q, seq_k, out, lse);
+  if (rc) return rc;
+  if (f.total_q > 0 && (!dout || !lse || !dq)) return MFL_E_NULL_POINTER;
+  if (f.total_k > 0 && (!dk || !dv)) return MFL_E_NULL_POINTER;
+  rc = check_strides({a.dout_token, a.dout_head, a.dq_token, a.dq_head, a.dk_token, a.dk_head,
+                      a.dv_token, a.dv_head});
+  if (rc) return rc;
+  const void* grads[3] = {dq, dk, dv};
+  const void* inputs[6] = {dout, q, k, v, out, lse};
+  if (!aligned(dout)) return MFL_E_MISALIGNED;
+  for (int i = 0; i < 3; ++i) {
+    if (!aligned(grads[i])) return MFL_E_MISALIGNED;
+    for (const void* x : inputs)
+      if (grads[i] && grads[i] == x) return MFL_E_ALIAS;
+    for (int j = 0; j < i; ++j)
+      if (grads[i] && grads[i] == grads[j]) return MFL_E_ALIAS;
+  }
+  rc = check_output(f.head_dim, {f.total_q, a.dq_token}, {f.heads_q, a.dq_head}, {1, 0});
+  if (rc) return rc;
+  rc = check_output(f.head_dim, {f.total_k, a.dk_token}, {f.heads_kv, a.dk_head}, {1, 0});
+  if (rc) return rc;
+  rc = check_output(f.head_dim, {f.total_k, a.dv_token}, {f.heads_kv, a.dv_head}, {1, 0});
+  if (rc) return rc;
+  const int dc = dim_class(f.head_dim);
+  const int64_t rows = f.total_q * (f.heads_q / f.heads_kv);
+  if ((rows / dq_rows(dc) + f.batch + 1) * f.heads_kv >= INT_MAX ||
+      (f.total_k / dkv_keys(dc) + f.batch + 1) * f.heads_kv >= INT_MAX)
+    return MFL_E_TOO_LARGE;
+  return MFL_OK;
+}
+
+int64_t backward_bytes(const mfl_attention_t& f) { return 8 * f.heads_q * f.total_q; }
+
+int check_prefix(const mfl_attention_prefix_t& a, const void* q, const void* prefix_k,
+                 const void* prefix_v, const void* k, const void* v, const int32_t* lengths,
+                 const void* out, const float* lse) {
+  if (a.q_tokens < 0 || a.prefix < 0 || a.capacity < 0) return MFL_E_NEGATIVE_DIM;
+  int rc = check_heads(a.dtype, a.batch, a.heads_q, a.heads_kv, a.head_dim, a.scale);
+  if (rc) return rc;
+  if (a.algo < 0 || a.algo > MFL_ATTENTION_FLAT || a.splits_prefix < 0 ||
+      a.splits_prefix > 1024 || a.splits_own < 0 || a.splits_own > 1024)
+    return MFL_E_UNSUPPORTED;
+  if (a.q_tokens > kMaxCount || a.prefix > kMaxCount || a.capacity > kMaxCount)
+    return MFL_E_TOO_LARGE;
+  if ((__int128)a.batch * a.q_tokens * a.heads_q > kMaxCount) return MFL_E_TOO_LARGE;
+  if (a.q_tokens > 0) {
+    if (!q || !out) return MFL_E_NULL_POINTER;
+    if (a.prefix > 0 && (!prefix_k || !prefix_v)) return MFL_E_NULL_POINTER;
+    if (a.capacity > 0 && (!k || !v || !lengths)) return MFL_E_NULL_POINTER;
+  }
+  rc = check_strides({a.q_batch, a.q_token, a.q_head, a.prefix_k_token, a.prefix_k_head,
+                      a.prefix_v_token, a.prefix_v_head, a.k_batch, a.k_token, a.k_head,
+                      a.v_batch, a.v_token, a.v_head, a.out_batch, a.out_token, a.out_head});
+  if (rc) return rc;
+  if (!aligned(q) || !aligned(prefix_k) || !aligned(prefix_v) || !aligned(k) || !aligned(v) ||
+      !aligned(out) || (uintptr_t)lse % 4 || (uintptr_t)lengths % 4)
+    return MFL_E_MISALIGNED;
+  if (out && (out == q || out == prefix_k || out == prefix_v || out == k || out == v))
+    return MFL_E_ALIAS;
+  return check_output(a.head_dim, {a.batch, a.out_batch}, {a.q_tokens, a.out_token},
+                      {a.heads_q, a.out_head});
+}
+
+struct PrefixPlan {
+  Choice prefix, own;      // splits 0: the part has no launch
+  int64_t bytes;
+};
+
+int plan_prefix(const mfl_attention_prefix_t& a, PrefixPlan& r) {
+  const int dc = dim_class(a.head_dim);
+  if (dc == 256 && a.algo == MFL_ATTENTION_TALL) return MFL_E_ALGO_CASE;
+  const int64_t group = a.heads_q / a.heads_kv, rows = a.batch * a.q_tokens * group;
+  r.prefix = choose(rows, 1, false, a.prefix, a.heads_kv, dc, a.algo, a.splits_prefix);
+  if (a.prefix == 0) r.prefix.splits = 0;
+  // tiles of one sequence's rows
+  r.own.algo = MFL_ATTENTION_FLAT;
+  r.own.slots = a.batch * ceil_div(a.q_tokens * group, tile_rows(MFL_ATTENTION_FLAT));
+  const int64_t wgs = r.own.slots * a.heads_kv;
+  r.own.splits = a.splits_own ? a.splits_own
+                              : clamp(wgs ? kFill / wgs : 1, 1, clamp(a.capacity / 256, 1, 64));
+  if (a.capacity == 0) r.own.splits = a.prefix == 0 ? 1 : 0;
+  if (!grid_fits(r.prefix, a.heads_kv) || !grid_fits(r.own, a.heads_kv)) return MFL_E_TOO_LARGE;
+  r.bytes = partial_bytes(a.batch * a.q_tokens * a.heads_q, r.prefix.splits + r.own.splits, dc);
+  return MFL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attention_packed_plan(const mfl_attention_t* a, const void* q, const void* k, const void* v,
+                          const int32_t* seq_q, const int32_t* seq_k, const void* out,
+                          const float* lse, int32_t* algo, int32_t* splits,
+                          int64_t* workspace_bytes) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_packed(*a, q, k, v, seq_q, seq_k, out, lse);
+  if (rc) return rc;
+  Choice c;
+  int64_t bytes;
+  rc = plan_packed(*a, seq_q != nullptr, c, bytes);
+  if (rc) return rc;
+  if (algo) *algo = c.algo;
+  if (splits) *splits = (int32_t)c.splits;
+  if (workspace_bytes) *workspace_bytes = bytes;
+  return MFL_OK;
+}
+
+int attention_packed(const mfl_attention_t* a, const void* q, const void* k, const void* v,
+                     const int32_t* seq_q, const int32_t* seq_k, void* out, float* lse,
+                     void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_packed(*a, q, k, v, seq_q, seq_k, out, lse);
+  if (rc) return rc;
+  Choice c;
+  int64_t bytes;
+  rc = plan_packed(*a, seq_q != nullptr, c, bytes);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, bytes);
+  if (rc) return rc;
+  if (a->total_q == 0) return MFL_OK;
+  const int dc = dim_class(a->head_dim);
+  FwdParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = out;
+  p.lse = lse;
+  p.seq_q = seq_q;
+  p.seq_k = seq_k;
+  p.batch = (int)a->batch;
+  p.q_len = (int)a->total_q;
+  p.total_q = (int)a->total_q;
+  p.total_k = (int)a->total_k;
+  p.q_inner = INT_MAX;
+  p.heads_kv = (int)a->heads_kv;
+  p.group = (int)(a->heads_q / a->heads_kv);
+  p.dim = (int)a->head_dim;
+  p.causal = a->causal;
+  p.rows = a->total_q * a->heads_q;
+  p.q_tok = a->q_token;
+  p.q_head = a->q_head;
+  p.k_tok = a->k_token;
+  p.k_head = a->k_head;
+  p.v_tok = a->v_token;
+  p.v_head = a->v_head;
+  p.o_tok = a->out_token;
+  p.o_head = a->out_head;
+  p.scale_log2 = a->scale * kLog2e;
+  const bool bf16 = a->dtype == MFL_BF16;
+  if (c.splits > 1) place_partials(p, workspace, c.splits, dc);
+  rc = run_forward(p, c, bf16, dc, stream);
+  if (rc || c.splits == 1) return rc;
+  return run_join(p, (int)c.splits, bf16, dc, stream);
+}
+
+int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* dout,
+                                   const void* q, const void* k, const void* v, const void* out,
+                                   const float* lse, const int32_t* seq_q, const int32_t* seq_k,
+                                   const void* dq, const void* dk, const void* dv,
+                                   int64_t* workspace_bytes) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_backward(*a, dout, q, k, v, out, lse, seq_q, seq_k, dq, dk, dv);
+  if (rc) return rc;
+  if (workspace_bytes) *workspace_bytes = backward_bytes(a->f);
+  return MFL_OK;
+}
+
+int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, const void* q,
+                              const void* k, const void* v, const void* out, const float* lse,
+                              const int32_t* seq_q, const int32_t* seq_k, void* dq, void* dk,
+                              void* dv, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_backward(*a, dout, q, k, v, out, lse, seq_q, seq_k, dq, dk, dv);
+  if (rc) return rc;
+  const mfl_attention_t& f = a->f;
+  rc = check_workspace(workspace, workspace_bytes, backward_bytes(f));
+  if (rc) return rc;
+  const int dc = dim_class(f.head_dim);
+  const bool bf16 = f.dtype == MFL_BF16, packed = seq_q != nullptr;
+  BwdParams p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = out;
+  p.dout = dout;
+  p.lse = lse;
+  p.stats = (float*)workspace;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.seq_q = seq_q;
+  p.seq_k = seq_k;
+  p.batch = (int)f.batch;
+  p.total_q = (int)f.total_q;
+  p.total_k = (int)f.total_k;
+  p.heads_kv = (int)f.heads_kv;
+  p.group = (int)(f.heads_q / f.heads_kv);
+  p.dim = (int)f.head_dim;
+  p.causal = f.causal;
+  p.q_tok = f.q_token;
+  p.q_head = f.q_head;
+  p.k_tok = f.k_token;
+  p.k_head = f.k_head;
+  p.v_tok = f.v_token;
+  p.v_head = f.v_head;
+  p.o_tok = f.out_token;
+  p.o_head = f.out_head;
+  p.do_tok = a->dout_token;
+  p.do_head = a->dout_head;
+  p.dq_tok = a->dq_token;
+  p.dq_head = a->dq_head;
+  p.dk_tok = a->dk_token;
+  p.dk_head = a->dk_head;
+  p.dv_tok = a->dv_token;
+  p.dv_head = a->dv_head;
+  p.scale = f.scale;
+  p.scale_log2 = f.scale * kLog2e;
+  // one slot more than tiles can need: the tokens behind the last sequence
+  const int64_t rows = f.total_q * p.group;
+  p.slots_q = (int)(tile_slots(rows, f.batch, dq_rows(dc), packed) + (packed ? 1 : 0));
+  p.slots_k = (int)(tile_slots(f.total_k, f.batch, dkv_keys(dc), packed) + (packed ? 1 : 0));
+  if (f.total_q > 0) {
+    rc = run(dq_kernel(bf16, dc), (int64_t)p.slots_q * p.heads_kv, &p, stream);
+    if (rc) return rc;
+  }
+  if (f.total_k == 0) return MFL_OK;
+  return run(dkv_kernel(bf16, dc), (int64_t)p.slots_k * p.heads_kv, &p, stream);
+}
+
+int attention_prefix_plan(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,
+                          const void* prefix_v, const void* k, const void* v,
+                          const int32_t* lengths, const void* out, const float* lse,
+                          int32_t* algo, int32_t* splits_prefix, int32_t* splits_own,
+                          int64_t* workspace_bytes) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_prefix(*a, q, prefix_k, prefix_v, k, v, lengths, out, lse);
+  if (rc) return rc;
+  PrefixPlan r;
+  rc = plan_prefix(*a, r);
+  if (rc) return rc;
+  if (algo) *algo = r.prefix.algo;
+  if (splits_prefix) *splits_prefix = (int32_t)r.prefix.splits;
+  if (splits_own) *splits_own = (int32_t)r.own.splits;
+  if (workspace_bytes) *workspace_bytes = r.bytes;
+  return MFL_OK;
+}
+
+int attention_prefix(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,
+                     const void* prefix_v, const void* k, const void* v, const int32_t* lengths,
+                     void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_prefix(*a, q, prefix_k, prefix_v, k, v, lengths, out, lse);
+  if (rc) return rc;
+  PrefixPlan r;
+  rc = plan_prefix(*a, r);
+  if (rc) return rc;
+  rc = check_workspace(workspace, workspace_bytes, r.bytes);
+  if (rc) return rc;
+  if (a->q_tokens == 0) return MFL_OK;
+  const int dc = dim_class(a->head_dim);
+  const bool bf16 = a->dtype == MFL_BF16;
+  const int splits = (int)(r.prefix.splits + r.own.splits);
+  FwdParams p{};
+  p.q = q;
+  p.o = out;
+  p.lse = lse;
+  p.q_inner = (int)a->q_tokens;
+  p.heads_kv = (int)a->heads_kv;
+  p.group = (int)(a->heads_q / a->heads_kv);
+  p.dim = (int)a->head_dim;
+  p.rows = a->batch * a->q_tokens * a->heads_q;
+  p.total_q = (int)(a->batch * a->q_tokens);
+  p.q_batch = a->q_batch;
+  p.q_tok = a->q_token;
+  p.q_head = a->q_head;
+  p.o_batch = a->out_batch;
+  p.o_tok = a->out_token;
+  p.o_head = a->out_head;
+  p.scale_log2 = a->scale * kLog2e;
+  if (splits > 1) place_partials(p, workspace, splits, dc);
+  if (r.prefix.splits > 0) {     // one sequence of all rows against the prefix
+    FwdParams s = p;
+    s.k = prefix_k;
+    s.v = prefix_v;
+    s.batch = 1;
+    s.q_len = p.total_q;
+    s.total_k = (int)a->prefix;
+    s.k_tok = a->prefix_k_token;
+    s.k_head = a->prefix_k_head;
+    s.v_tok = a->prefix_v_token;
+    s.v_head = a->prefix_v_head;
+    rc = run_forward(s, r.prefix, bf16, dc, stream);
+    if (rc) return rc;
+  }
+  if (r.own.splits > 0) {        // each sequence's rows against its own keys
+    FwdParams s = p;
+    s.k = k;
+    s.v = v;
+    s.lengths = lengths;
+    s.batch = (int)a->batch;
+    s.q_len = (int)a->q_tokens;
+    s.total_k = (int)a->capacity;
+    s.causal = 1;
+    s.k_batch = a->k_batch;
+    s.k_tok = a->k_token;
+    s.k_head = a->k_head;
+    s.v_batch = a->v_batch;
+    s.v_tok = a->v_token;
+    s.v_head = a->v_head;
+    s.split0 = (int)r.prefix.splits;
+    rc = run_forward(s, r.own, bf16, dc, stream);
+    if (rc) return rc;
+  }
+  return splits > 1 ? run_join(p, splits, bf16, dc, stream) : MFL_OK;
+}
+
+}  // extern "C"

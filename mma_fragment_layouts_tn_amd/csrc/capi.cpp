@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "../../include/mfl_gemm.h"
+#include "../../include/mfl_attention.h"
 #include "../../include/mfl_chain.h"
 #include "../../include/mfl_layout.h"
 #include "../../include/mfl_probe.h"
@@ -749,6 +750,7 @@ const char* gemm_strerror(int code) {
     case MFL_E_MISALIGNED: return "pointer not aligned to its element size";
     case MFL_E_ALIAS: return "D aliases C with a different leading dimension or dtype";
     case MFL_E_TOO_LARGE: return "size beyond the supported index range";
+    case MFL_E_WORKSPACE: return "workspace missing, misaligned or too small";
     default: return "unknown error code";
   }
 }
