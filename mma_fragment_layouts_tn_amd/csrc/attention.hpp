@@ -111,6 +111,10 @@ struct BwdParams {
   int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head, do_tok, do_head;
   int64_t dq_tok, dq_head, dk_tok, dk_head, dv_tok, dv_head;
   float scale, scale_log2;
+  // dK, dV: a tile's steps go to one workgroup per part_steps of them, at
+  // most max_parts; the parts' sums are dK then dV of part 0, 1, ...
+  int part_steps, max_parts;
+  float* partials;
 };
 
 // ------------------------------------------------------------- LDS tiles
@@ -152,11 +156,6 @@ constexpr bool swizzle_spreads() {
 static_assert(swizzle_spreads<64>() && swizzle_spreads<128>() && swizzle_spreads<256>(),
               "both kinds of LDS reads must touch every bank group once");
 
-// Where no key or column is, the direct-to-LDS loads read zeros (for a
-// query's log-sum-exp: infinity, which makes its weights zero).
-static __device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
-static __device__ const float kInfinity = INFINITY;
-
 template <class T>
 __device__ __forceinline__ Vec8<T> load8(const T* p) {
   Vec8<T> v;
@@ -164,23 +163,81 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
   return v;
 }
 
-// The operand fragment of rows r..r+31 (lane: row l % 32, d = d0 + 8 (l / 32))
+// A lane's place in a stage for both kinds of fragment reads, as LDS byte
+// addresses.  Tiles start at multiples of 4 KiB, so the address of another
+// chunk is the address of the first one XOR a constant, and other rows (32
+// and 16 further, where the swizzle is the same) are constant offsets: two
+// registers serve every read of a stage.
+//
+// The compiler lets an LDS read wait for every direct-to-LDS load in
+// flight unless it can tell them apart, which would take away the loads'
+// lead.  The kernels' steps are therefore functions of two restricted
+// pointers, to the stage they read (`stage` here) and to the ring they fill,
+// and every read is addressed from the first.  What orders a read behind the
+// loads it needs is its address, which at() forms behind the wait.
+using lds_c = __attribute__((address_space(3))) char*;
 template <class T, int DC>
-__device__ __forceinline__ Vec8<T> frag(const T* tile, int r, int d) {
-  return *(const Vec8<T>*)&tile[tile_off<DC>(r, d)];
+struct Reader {
+  unsigned s, t;
+  lds_c stage;
+  // straight: row l % 32, d = 8 (l / 32)
+  // transposed: of each 16 lanes, lane i supplies 4 elements of key i / 4
+  static __device__ __forceinline__ Reader of(int lane) {
+    const int i = lane & 15, blk = lane >> 4;
+    return Reader{2u * tile_off<DC>(lane & 31, 8 * (lane >> 5)),
+                  2u * tile_off<DC>(4 * (blk >> 1) + (i >> 2), 16 * (blk & 1) + 4 * (i & 3)),
+                  nullptr};
+  }
+  // in the stage at `base`, `more` bytes on; opaque, so that the addresses
+  // below are formed where they are used instead of held in registers
+  __device__ __forceinline__ Reader at(lds_c base, unsigned more = 0) const {
+    const unsigned b = (unsigned)(uintptr_t)base + more;
+    Reader r{s + b, t + b, base};
+    asm volatile("" : "+v"(r.s), "+v"(r.t));
+    return r;
+  }
+  // operand fragment of rows 32 b .. 32 b + 31, K chunk kk, `more` bytes on
+  __device__ __forceinline__ Vec8<T> straight(int b, int kk, int more = 0) const {
+    using ptr = const __attribute__((address_space(3))) Vec8<T>*;
+    return *(ptr)in_stage((s ^ (32u * kk)) + 64 * b * DC + more);
+  }
+  // transposed: rows d = 32 db + l % 32; values the keys
+  // 16 kc + 4 (l / 32) + 0..3 and 8 further
+  __device__ __forceinline__ Vec8<T> transposed(int kc, int db, int more = 0) const {
+    const unsigned x = t ^ (64u * db);
+    const shortx4 lo = read_tr(x + 32 * kc * DC + more);
+    const shortx4 hi = read_tr((x ^ 32u) + 32 * kc * DC + 16 * DC + more);
+    return __builtin_bit_cast(Vec8<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+  __device__ __forceinline__ shortx4 read_tr(unsigned address) const {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)in_stage(address));
+  }
+  __device__ __forceinline__ lds_c in_stage(unsigned address) const {
+    return stage + (int)(address - (unsigned)(uintptr_t)stage);
+  }
+};
+// what Reader takes for granted of the tile's layout
+template <int DC>
+constexpr bool reader_addresses_hold() {
+  for (int r = 0; r < 32; ++r)
+    for (int kk = 0; kk < DC / 16; ++kk)
+      for (int h = 0; h < 2; ++h)
+        if (tile_off<DC>(r + 32, 16 * kk + 8 * h) !=
+            (tile_off<DC>(r, 8 * h) ^ (16 * kk)) + 32 * DC)
+          return false;
+  for (int r = 0; r < 8; ++r)
+    for (int d = 0; d < 32; d += 4)
+      for (int db = 0; db < DC / 32; ++db) {
+        const int x = tile_off<DC>(r, d) ^ (32 * db);
+        if (tile_off<DC>(16 + r, 32 * db + d) != x + 16 * DC ||
+            tile_off<DC>(16 + r + 8, 32 * db + d) != (x ^ 16) + 24 * DC)
+          return false;
+      }
+  return true;
 }
-
-// Transposed: lane (row d0 + l % 32, values: the keys k0 + 4 (l / 32) + 0..3
-// and 8 further) of a tile stored key by key
-template <class T, int DC>
-__device__ __forceinline__ Vec8<T> frag_tr(const T* tile, int k0, int d0, int lane) {
-  const int s = lane & 15, blk = lane >> 4;
-  const int r = k0 + 4 * (blk >> 1) + (s >> 2), d = d0 + 16 * (blk & 1) + 4 * (s & 3);
-  const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(&tile[tile_off<DC>(r, d)]));
-  const shortx4 hi =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(&tile[tile_off<DC>(r + 8, d)]));
-  return __builtin_bit_cast(Vec8<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
+static_assert(reader_addresses_hold<64>() && reader_addresses_hold<128>() &&
+                  reader_addresses_hold<256>(),
+              "chunks by XOR, rows by offset");
 
 // LDS reads of this wave done, then the workgroup barrier
 __device__ __forceinline__ void barrier() {
@@ -217,6 +274,13 @@ __device__ __forceinline__ float both_max(float x) {
 __device__ __forceinline__ float both_sum(float x) {
   const Halves h = halves(x);
   return h.lower + h.upper;
+}
+// x, but not for the optimiser: a first step told apart by it stays a branch
+// in the loop's body (a copy of the body for it would hide from the compiler
+// that its loads and the other steps' reads are apart)
+__device__ __forceinline__ int hidden(int x) {
+  asm volatile("" : "+s"(x));
+  return x;
 }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -291,21 +355,51 @@ __device__ __forceinline__ Place place_of(const FwdParams& p, int slot, int bm) 
 
 // ------------------------------------------------ direct-to-LDS staging
 // One wave instruction fills 1024 consecutive LDS bytes; each lane fetches
-// the 16 bytes its place stands for.
+// the 16 bytes its place stands for.  Buffer loads: a tile's rows past the
+// sequence's end and columns past the head dimension are out of the buffer's
+// range, and the hardware stores zeros for them, so every load of every tile
+// is one instruction on a descriptor made once per tile and a 32-bit offset
+// per lane that never changes.  (Addresses formed per lane, with a choice
+// between the tensor and a block of zeros, cost a fifth of the gradients'
+// step in vector instructions.)  Loads move at most 64 bytes a clock into
+// LDS, and a wave that issues several in a row stands still meanwhile: the
+// kernels issue them one by one between matrix instructions.
+constexpr int kMaxTokenStride = 1 << 23;   // elements: 64 rows stay within 2^30 bytes
+
 template <class T, int DC>
 struct Fetch {
   static constexpr int ROWS = 512 / DC;   // tile rows per instruction
-  // instruction i of a tile whose row 0 is key `key0`: rows with key >= end
-  // and columns past `dim` are zeros
-  static __device__ __forceinline__ void issue(const T* base, int64_t stride, int key0, int end,
-                                               int dim, T* tile, int i, int lane) {
-    const int r = i * ROWS + (8 * lane) / DC, c = ((8 * lane) % DC) / 8;
-    const int col = 8 * (c ^ swz_row<DC>(r)), key = key0 + r;
-    const void* g = base + (int64_t)key * stride + col;
-    if (key >= end || col >= dim) g = &kZeros;
-    __builtin_amdgcn_global_load_lds(g, (lds_t)(tile + i * 512), 16, 0, 0);
+  __amdgpu_buffer_rsrc_t r;
+  // the tile's rows `row0` .. of `end` rows at `base`
+  static __device__ __forceinline__ Fetch of(const T* base, int64_t stride, int row0, int end,
+                                             int dim) {
+    const int rows = min(end - row0, 64);
+    const int bytes = rows > 0 ? 2 * ((rows - 1) * (int)stride + dim) : 0;
+    return Fetch{__builtin_amdgcn_make_buffer_rsrc((void*)(base + (int64_t)row0 * stride), 0, bytes,
+                                                   0x00027000)};
+  }
+  // instruction i of the tile
+  __device__ __forceinline__ void issue(int64_t stride, int dim, lds_c tile, int i,
+                                        int lane) const {
+    const int row = (8 * lane) / DC, c = ((8 * lane) % DC) / 8;
+    const int col = 8 * (c ^ swz_row<DC>(row) ^ swz_row<DC>(i * ROWS));
+    const unsigned off = col < dim ? 2u * (row * (int)stride + col) : 0x80000000u;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t)(tile + i * 1024), 16, off,
+                                             2 * i * ROWS * (int)stride, 0, 0);
   }
 };
+// the swizzle of a sum of rows without common bits
+template <int DC>
+constexpr bool swizzle_is_linear() {
+  for (int r = 0; r < 64; ++r)
+    for (int i = 512 / DC; i < 64; i += 512 / DC)
+      if (r < 512 / DC && swz_row<DC>(i + r) != (swz_row<DC>(i) ^ swz_row<DC>(r))) return false;
+  return true;
+}
+static_assert(swizzle_is_linear<64>() && swizzle_is_linear<128>() && swizzle_is_linear<256>(),
+              "a lane's column of another instruction by XOR");
+// memory loads stay on their side, everything else may pass
+__device__ __forceinline__ void pin_loads() { __builtin_amdgcn_sched_barrier(0x38f); }
 
 // 8 values of a row from the two halves of the wave: value i of block x is
 // d = 8 (i / 4) + 4 (l / 32) + i % 4; after the exchange lane l holds
@@ -412,15 +506,27 @@ __device__ __forceinline__ void softmax_step(floatx16 (&st)[NB], floatx16 (&acc)
   l += sum;
 }
 
+// bits 0 .. n - 1 (none for n <= 0, all for n > 31)
+__device__ __forceinline__ unsigned low_bits(int n) {
+  return n > 31 ? ~0u : n > 0 ? (1u << n) - 1u : 0u;
+}
+// all bits of x where bit r of the mask is set, else those of y
+__device__ __forceinline__ float select_bit(unsigned mask, int r, float x, float y) {
+  const unsigned m = (unsigned)__builtin_amdgcn_sbfe((int)mask, r, 1);
+  return __builtin_bit_cast(float, (m & __builtin_bit_cast(unsigned, x)) |
+                                       (~m & __builtin_bit_cast(unsigned, y)));
+}
 // keys past the row's limit get -inf
 template <int NB>
 __device__ __forceinline__ void mask_keys(floatx16 (&st)[NB], int key0, int limit, int lane) {
   const int room = limit - key0 - 4 * (lane >> 5);
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int b = 0; b < NB; ++b) {
+    const unsigned seen = low_bits(room + 1 - 32 * b);
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (32 * b + 8 * (i / 4) + i % 4 > room) st[b][i] = -INFINITY;
+      st[b][i] = select_bit(seen, 8 * (i / 4) + i % 4, st[b][i], -INFINITY);
+  }
 }
 
 // ------------------------------------------------------ forward, tall
@@ -449,9 +555,6 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
   const int r0 = at.tile * BM + 32 * w;
   const RowOf row = row_of(r0 + (lane & 31), at.lq, at.lk, p.group, kvh, at.q0, p.causal);
   const int first_row_limit = uniform(row.limit);
-  // no work for a wave whose rows are all past the last one
-  const int wave_limit =
-      r0 < at.lq * p.group ? __builtin_amdgcn_readlane(row.limit, 31) : -1;
   // keys of this workgroup: to its last row's limit, its share of them
   const int last_t = min((int)(((int64_t)at.tile * BM + BM - 1) / p.group), at.lq - 1);
   const int seen = max(p.causal ? min(last_t + at.lk - at.lq, at.lk - 1) + 1 : at.lk, 0);
@@ -461,15 +564,22 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
 
   const T* K = (const T*)p.k + at.k_off + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + at.v_off + (int64_t)kvh * p.v_head;
-  auto issue = [&](int c) {
-    if (c >= c1) return;
-    T* st = smem + ((c - c0) % NST) * 2 * TILE;
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-      Fetch<T, DC>::issue(K, p.k_tok, c * CK, at.lk, p.dim, st, w * NI + j, lane);
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-      Fetch<T, DC>::issue(V, p.v_tok, c * CK, at.lk, p.dim, st + TILE, w * NI + j, lane);
+  const lds_c ring = (lds_c)smem;
+  auto stage_of = [&](int c) { return (c - c0) % NST * 4 * TILE; };
+  // load j of chunk c: K, then V
+  struct Next {
+    Fetch<T, DC> k, v;
+  };
+  auto next_chunk = [&](int c) {
+    const int end = c < c1 ? at.lk : 0;
+    return Next{Fetch<T, DC>::of(K, p.k_tok, c * CK, end, p.dim),
+                Fetch<T, DC>::of(V, p.v_tok, c * CK, end, p.dim)};
+  };
+  auto issue = [&](const Next& n, lds_c to, int j) {
+    if (j < NI)
+      n.k.issue(p.k_tok, p.dim, to, w * NI + j, lane);
+    else
+      n.v.issue(p.v_tok, p.dim, to + 2 * TILE, w * NI + j - NI, lane);
   };
 
   const int64_t qn = (int64_t)(row.n / p.q_inner) * p.q_batch + (row.n % p.q_inner) * p.q_tok;
@@ -487,40 +597,62 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
   floatx16 acc[ND];
   zero(acc);
   float m = -INFINITY, l = 0.0f;
-
+  const Reader<T, DC> reader = Reader<T, DC>::of(lane);
+  // chunk c, while chunk c + NST - 1 is fetched; `to` is the whole ring.
+  // Every step issues 2 NI loads (of nothing past the last chunk), so what is
+  // in flight is known by count.
+  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to) {
+    if (c == hidden(c0)) {
 #pragma unroll
-  for (int s = 0; s < NST - 1; ++s) issue(c0 + s);
-  for (int c = c0; c < c1; ++c) {
+      for (int s = 0; s < NST - 1; ++s) {
+        const Next nx = next_chunk(c0 + s);
+#pragma unroll
+        for (int j = 0; j < 2 * NI; ++j) issue(nx, to + 4 * s * TILE, j);
+      }
+    }
     // chunk c has landed here, and after the barrier everywhere; its
     // predecessor's stage is free
-    const int ahead = min(c1 - 1 - c, NST - 2);
-    if (ahead >= 2) wait_vm<(NST > 3 ? 2 : 0) * 2 * NI>();
-    else if (ahead == 1) wait_vm<(NST > 2 ? 1 : 0) * 2 * NI>();
-    else wait_vm<0>();
+    wait_vm<(NST - 2) * 2 * NI>();
     barrier();
-    issue(c + NST - 1);
+    const Next nx = next_chunk(c + NST - 1);
+    const lds_c fill = to + stage_of(c + NST - 1);
     const int key0 = c * CK;
-    if (key0 > wave_limit) continue;
-    const T* sk = smem + ((c - c0) % NST) * 2 * TILE;
-    const T* sv = sk + TILE;
+    const Reader<T, DC> rd = reader.at(from);
     floatx16 st[2];
     zero(st);
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk)
-        st[b] = Elem<T>::mma(
-            frag<T, DC>(sk, 32 * b + (lane & 31), 16 * kk + 8 * (lane >> 5)), qf[kk], st[b]);
+      for (int kk = 0; kk < KS; ++kk) {
+        st[b] = Elem<T>::mma(rd.straight(b, kk), qf[kk], st[b]);
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          if ((2 * j + 1) * 2 * KS / (2 * NI) == b * KS + kk) {
+            pin_loads();
+            issue(nx, fill, j);
+            pin_loads();
+          }
+      }
     if (key0 + CK - 1 > first_row_limit) mask_keys(st, key0, row.limit, lane);
     softmax_step(st, acc, m, l, p.scale_log2);
 #pragma unroll
     for (int kc = 0; kc < 4; ++kc) {
       const Vec8<T> pf = pack8<T>(st[kc / 2], kc % 2);
 #pragma unroll
-      for (int db = 0; db < ND; ++db)
-        acc[db] = Elem<T>::mma(frag_tr<T, DC>(sv, 16 * kc, 32 * db, lane), pf, acc[db]);
+      for (int db = 0; db < ND; ++db) {
+        acc[db] = Elem<T>::mma(rd.transposed(kc, db, 2 * TILE), pf, acc[db]);
+#pragma unroll
+        for (int j = 0; j < NI; ++j)
+          if ((2 * j + 1) * 4 * ND / (2 * NI) == kc * ND + db) {
+            pin_loads();
+            issue(nx, fill, NI + j);
+            pin_loads();
+          }
+      }
     }
-  }
+  };
+  for (int c = c0; c < c1; ++c) step(c, ring + stage_of(c), ring);
+  wait_vm<0>();
 
   l = both_sum(l);
   const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
@@ -560,8 +692,10 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
                 ND = DC / 32, TILE = CK * DC, NI = TILE / 512, BM = 32;
   static_assert(2 * (NST - 1) * NI < 64, "loads in flight");
   constexpr int RING = NST * 2 * TILE;                   // elements per wave
-  __shared__ __attribute__((aligned(1024))) T smem[W * RING];
-  __shared__ float2 ml[W][32];
+  // one object: with a second one the compiler's bookkeeping of direct-to-LDS
+  // loads makes every read wait for all of them
+  __shared__ __attribute__((aligned(1024))) T smem[W * RING + W * 32 * 4];
+  float2(*ml)[32] = (float2(*)[32])(smem + W * RING);
   static_assert(2 * W * RING >= 4 * W * 32 * DC, "the partial rows fit in the rings");
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   int bid = blockIdx.x;
@@ -580,17 +714,16 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
   const int c1 = (int)((int64_t)chunks * (split + 1) / p.splits);
   const T* K = (const T*)p.k + at.k_off + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + at.v_off + (int64_t)kvh * p.v_head;
-  T* ring = smem + w * RING;
+  const lds_c ring = (lds_c)smem + 2 * w * RING;
   const int mine = max((c1 - c0 - w + W - 1) / W, 0);    // chunks c0 + w, + W, ...
-  auto issue = [&](int i) {
-    if (i >= mine) return;
-    T* st = ring + (i % NST) * 2 * TILE;
-    const int key0 = (c0 + w + i * W) * CK;
+  auto issue = [&](int i, lds_c to) {
+    const int key0 = (c0 + w + i * W) * CK, end = i < mine ? at.lk : 0;
+    const Fetch<T, DC> k = Fetch<T, DC>::of(K, p.k_tok, key0, end, p.dim);
+    const Fetch<T, DC> v = Fetch<T, DC>::of(V, p.v_tok, key0, end, p.dim);
 #pragma unroll
-    for (int j = 0; j < NI; ++j) Fetch<T, DC>::issue(K, p.k_tok, key0, at.lk, p.dim, st, j, lane);
+    for (int j = 0; j < NI; ++j) k.issue(p.k_tok, p.dim, to, j, lane);
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-      Fetch<T, DC>::issue(V, p.v_tok, key0, at.lk, p.dim, st + TILE, j, lane);
+    for (int j = 0; j < NI; ++j) v.issue(p.v_tok, p.dim, to + 2 * TILE, j, lane);
   };
   const int64_t qn = (int64_t)(row.n / p.q_inner) * p.q_batch + (row.n % p.q_inner) * p.q_tok;
   const T* Q = (const T*)p.q + qn + row.head * p.q_head;
@@ -607,27 +740,24 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
   floatx16 acc[ND];
   zero(acc);
   float m = -INFINITY, l = 0.0f;
+  const Reader<T, DC> reader = Reader<T, DC>::of(lane);
+  // chunk i of this wave, while chunk i + NST - 1 is fetched
+  auto step = [&](int i, lds_c __restrict__ from, lds_c __restrict__ to) {
+    if (i == hidden(0))
 #pragma unroll
-  for (int s = 0; s < NST - 1; ++s) issue(s);
-  for (int i = 0; i < mine; ++i) {
+      for (int s = 0; s < NST - 1; ++s) issue(s, to + 4 * s * TILE);
     // this wave's reads of the stage of chunk i - 1 are done: refill it
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    issue(i + NST - 1);
-    const int ahead = min(mine - 1 - i, NST - 1);
-    if (ahead >= 3) wait_vm<(NST > 3 ? 3 : 0) * 2 * NI>();
-    else if (ahead == 2) wait_vm<(NST > 2 ? 2 : 0) * 2 * NI>();
-    else if (ahead == 1) wait_vm<2 * NI>();
-    else wait_vm<0>();
+    issue(i + NST - 1, to + (i + NST - 1) % NST * 4 * TILE);
+    wait_vm<(NST - 1) * 2 * NI>();   // chunk i has landed
     __builtin_amdgcn_sched_barrier(0);
-    const T* sk = ring + (i % NST) * 2 * TILE;
-    const T* sv = sk + TILE;
+    const Reader<T, DC> rd = reader.at(from);
     const int key0 = (c0 + w + i * W) * CK;
     floatx16 st[1];
     zero(st);
 #pragma unroll
-    for (int kk = 0; kk < KS; ++kk)
-      st[0] = Elem<T>::mma(frag<T, DC>(sk, lane & 31, 16 * kk + 8 * (lane >> 5)), qf[kk], st[0]);
+    for (int kk = 0; kk < KS; ++kk) st[0] = Elem<T>::mma(rd.straight(0, kk), qf[kk], st[0]);
     if (key0 + CK - 1 > first_row_limit) mask_keys(st, key0, row.limit, lane);
     softmax_step(st, acc, m, l, p.scale_log2);
 #pragma unroll
@@ -635,9 +765,11 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
       const Vec8<T> pf = pack8<T>(st[0], kc);
 #pragma unroll
       for (int db = 0; db < ND; ++db)
-        acc[db] = Elem<T>::mma(frag_tr<T, DC>(sv, 16 * kc, 32 * db, lane), pf, acc[db]);
+        acc[db] = Elem<T>::mma(rd.transposed(kc, db, 2 * TILE), pf, acc[db]);
     }
-  }
+  };
+  for (int i = 0; i < mine; ++i) step(i, ring + i % NST * 4 * TILE, ring);
+  wait_vm<0>();
   // join: every wave scales its rows to the common maximum and leaves them in
   // LDS (16-byte group g of row r at g ^ (r & 15))
   l = both_sum(l);

@@ -9,6 +9,12 @@
 #include "attention.hpp"
 #include "attention_bwd.hpp"
 #include "attention_launch.hpp"
+#ifndef FDIV
+#define FDIV 1
+#endif
+#ifndef PMIN
+#define PMIN 8
+#endif
 
 namespace {
 
@@ -16,6 +22,13 @@ using namespace mfl::att;
 
 constexpr int64_t kMaxCount = (int64_t)INT_MAX - (1 << 16);
 constexpr int64_t kMaxStride = (int64_t)1 << 40;   // elements; products with a count fit int64
+
+// between tokens: tiles of tokens are addressed with 32-bit offsets
+int check_token_strides(std::initializer_list<int64_t> strides) {
+  for (int64_t s : strides)
+    if (s > kMaxTokenStride) return MFL_E_TOO_LARGE;
+  return MFL_OK;
+}
 
 bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
 
@@ -109,10 +122,10 @@ bool grid_fits(const Choice& c, int64_t heads_kv) {
   return (__int128)c.slots * heads_kv * c.splits < INT_MAX;
 }
 
-int run(KernelRef k, int64_t blocks, void* params, void* stream) {
+int run(KernelRef k, int64_t blocks, void* params, void* stream, int a = 0, int b = 0) {
   if (!k.fn) return MFL_E_UNSUPPORTED;
   if (blocks == 0) return MFL_OK;
-  void* args[] = {params};
+  void* args[] = {params, &a, &b};   // (a kernel takes as many as it has)
   const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
                                        (hipStream_t)stream);
   return e == hipSuccess ? MFL_OK : MFL_E_LAUNCH;
@@ -157,6 +170,7 @@ int check_packed(const mfl_attention_t& a, const void* q, const void* k, const v
   if (a.total_q > 0 && a.total_k > 0 && (!k || !v)) return MFL_E_NULL_POINTER;
   rc = check_strides({a.q_token, a.q_head, a.k_token, a.k_head, a.v_token, a.v_head, a.out_token,
                       a.out_head});
+  if (!rc) rc = check_token_strides({a.q_token, a.k_token, a.v_token});
   if (rc) return rc;
   if (!aligned(q) || !aligned(k) || !aligned(v) || !aligned(out) || (uintptr_t)lse % 4 ||
       (uintptr_t)seq_q % 4 || (uintptr_t)seq_k % 4)
@@ -186,6 +200,38 @@ void place_partials(FwdParams& p, void* workspace, int64_t splits, int dc) {
   p.part_ml = (float2*)((char*)workspace + 4 * splits * p.rows * dc);
 }
 
+// How dK and dV are shared out: the steps of a tile (chunks of query tokens of
+// every head of the group) per workgroup, and the workspace.
+struct BackwardPlan {
+  int64_t slots_q, slots_k, bytes, stats_bytes;
+  int part_steps, max_parts;
+};
+
+BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
+  const int dc = dim_class(f.head_dim);
+  const int64_t group = f.heads_q / f.heads_kv;
+  BackwardPlan r;
+  // one slot more than tiles can need: the tokens behind the last sequence
+  r.slots_q = tile_slots(f.total_q * group, f.batch, dq_rows(dc), packed) + (packed ? 1 : 0);
+  r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed) + (packed ? 1 : 0);
+  r.stats_bytes = 8 * f.heads_q * f.total_q;
+  r.part_steps = INT_MAX / 2;
+  r.max_parts = 1;
+  const int64_t tiles = ceil_div(f.total_k, dkv_keys(dc)) * f.heads_kv;
+  if (tiles > 0 && tiles < 4 * kFill) {
+    const int64_t steps = group * ceil_div(ceil_div(f.total_q, f.batch), dkv_chunk(dc));
+    const int64_t fair = tiles * steps / (f.causal ? 2 : 1) / kFill / FDIV;
+    r.part_steps = (int)clamp(fair, PMIN, INT_MAX / 2);
+    r.max_parts = (int)clamp(ceil_div(2 * steps, r.part_steps), 1, 8);
+  }
+  r.bytes = r.stats_bytes;
+  if (r.max_parts > 1) {
+    r.stats_bytes = ceil_div(r.stats_bytes, 16) * 16;
+    r.bytes = r.stats_bytes + r.max_parts * 8 * f.total_k * f.heads_kv * dc;
+  }
+  return r;
+}
+
 int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* q, const void* k,
                    const void* v, const void* out, const float* lse, const int32_t* seq_q,
                    const int32_t* seq_k, const void* dq, const void* dk, const void* dv) {
@@ -198,6 +244,7 @@ int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* 
   if (f.total_k > 0 && (!dk || !dv)) return MFL_E_NULL_POINTER;
   rc = check_strides({a.dout_token, a.dout_head, a.dq_token, a.dq_head, a.dk_token, a.dk_head,
                       a.dv_token, a.dv_head});
+  if (!rc) rc = check_token_strides({a.dout_token});
   if (rc) return rc;
   const void* grads[3] = {dq, dk, dv};
   const void* inputs[6] = {dout, q, k, v, out, lse};
@@ -215,15 +262,11 @@ int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* 
   if (rc) return rc;
   rc = check_output(f.head_dim, {f.total_k, a.dv_token}, {f.heads_kv, a.dv_head}, {1, 0});
   if (rc) return rc;
-  const int dc = dim_class(f.head_dim);
-  const int64_t rows = f.total_q * (f.heads_q / f.heads_kv);
-  if ((rows / dq_rows(dc) + f.batch + 1) * f.heads_kv >= INT_MAX ||
-      (f.total_k / dkv_keys(dc) + f.batch + 1) * f.heads_kv >= INT_MAX)
+  const BackwardPlan r = plan_backward(f, seq_q != nullptr);
+  if (r.slots_q * f.heads_kv >= INT_MAX || r.slots_k * 8 * f.heads_kv >= INT_MAX)
     return MFL_E_TOO_LARGE;
   return MFL_OK;
 }
-
-int64_t backward_bytes(const mfl_attention_t& f) { return 8 * f.heads_q * f.total_q; }
 
 int check_prefix(const mfl_attention_prefix_t& a, const void* q, const void* prefix_k,
                  const void* prefix_v, const void* k, const void* v, const int32_t* lengths,
@@ -245,6 +288,7 @@ int check_prefix(const mfl_attention_prefix_t& a, const void* q, const void* pre
   rc = check_strides({a.q_batch, a.q_token, a.q_head, a.prefix_k_token, a.prefix_k_head,
                       a.prefix_v_token, a.prefix_v_head, a.k_batch, a.k_token, a.k_head,
                       a.v_batch, a.v_token, a.v_head, a.out_batch, a.out_token, a.out_head});
+  if (!rc) rc = check_token_strides({a.prefix_k_token, a.prefix_v_token, a.k_token, a.v_token});
   if (rc) return rc;
   if (!aligned(q) || !aligned(prefix_k) || !aligned(prefix_v) || !aligned(k) || !aligned(v) ||
       !aligned(out) || (uintptr_t)lse % 4 || (uintptr_t)lengths % 4)
@@ -355,7 +399,7 @@ int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* do
   if (!a) return MFL_E_NULL_POINTER;
   const int rc = check_backward(*a, dout, q, k, v, out, lse, seq_q, seq_k, dq, dk, dv);
   if (rc) return rc;
-  if (workspace_bytes) *workspace_bytes = backward_bytes(a->f);
+  if (workspace_bytes) *workspace_bytes = plan_backward(a->f, seq_q != nullptr).bytes;
   return MFL_OK;
 }
 
@@ -367,10 +411,11 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   int rc = check_backward(*a, dout, q, k, v, out, lse, seq_q, seq_k, dq, dk, dv);
   if (rc) return rc;
   const mfl_attention_t& f = a->f;
-  rc = check_workspace(workspace, workspace_bytes, backward_bytes(f));
+  const BackwardPlan plan = plan_backward(f, seq_q != nullptr);
+  rc = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (rc) return rc;
   const int dc = dim_class(f.head_dim);
-  const bool bf16 = f.dtype == MFL_BF16, packed = seq_q != nullptr;
+  const bool bf16 = f.dtype == MFL_BF16;
   BwdParams p{};
   p.q = q;
   p.k = k;
@@ -409,16 +454,20 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.dv_head = a->dv_head;
   p.scale = f.scale;
   p.scale_log2 = f.scale * kLog2e;
-  // one slot more than tiles can need: the tokens behind the last sequence
-  const int64_t rows = f.total_q * p.group;
-  p.slots_q = (int)(tile_slots(rows, f.batch, dq_rows(dc), packed) + (packed ? 1 : 0));
-  p.slots_k = (int)(tile_slots(f.total_k, f.batch, dkv_keys(dc), packed) + (packed ? 1 : 0));
+  p.slots_q = (int)plan.slots_q;
+  p.slots_k = (int)plan.slots_k;
+  p.part_steps = plan.part_steps;
+  p.max_parts = plan.max_parts;
+  p.partials = (float*)((char*)workspace + plan.stats_bytes);
   if (f.total_q > 0) {
-    rc = run(dq_kernel(bf16, dc), (int64_t)p.slots_q * p.heads_kv, &p, stream);
+    rc = run(dq_kernel(bf16, dc), plan.slots_q * p.heads_kv, &p, stream);
     if (rc) return rc;
   }
   if (f.total_k == 0) return MFL_OK;
-  return run(dkv_kernel(bf16, dc), (int64_t)p.slots_k * p.heads_kv, &p, stream);
+  rc = run(dkv_kernel(bf16, dc), plan.slots_k * p.max_parts * p.heads_kv, &p, stream);
+  if (rc || p.max_parts == 1) return rc;
+  return run(dkv_join_kernel(bf16, dc), plan.slots_k * (dkv_keys(dc) / 32) * p.heads_kv, &p, stream,
+             dkv_keys(dc), dkv_chunk(dc));
 }
 
 int attention_prefix_plan(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,

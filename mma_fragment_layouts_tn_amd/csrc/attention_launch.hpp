@@ -21,6 +21,7 @@ KernelRef fwd_kernel(bool bf16, int dc, int algo);   // algo: MFL_ATTENTION_TALL
 KernelRef join_kernel(bool bf16, int dc);
 KernelRef dq_kernel(bool bf16, int dc);
 KernelRef dkv_kernel(bool bf16, int dc);
+KernelRef dkv_join_kernel(bool bf16, int dc);
 
 // columns of the accumulators for a head dimension
 constexpr int dim_class(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -28,6 +29,7 @@ constexpr int dim_class(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 
 constexpr int tile_rows(int algo) { return algo == 3 ? 32 : algo == 2 ? 128 : 256; }
 constexpr int dq_rows(int dc) { return dc == 256 ? 128 : 256; }
 constexpr int dkv_keys(int) { return 128; }
+constexpr int dkv_chunk(int dc) { return dc == 256 ? 32 : 64; }
 
 }  // namespace att
 }  // namespace mfl
