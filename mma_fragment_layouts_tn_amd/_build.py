@@ -24,7 +24,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["gemm_inst_256.hip", "gemm_inst_256w4.hip", "gemm_inst_128.hip",
            "gemm_inst_128w1.hip", "gemm_inst_splitk.hip", "gemm_inst_256w4x16.hip",
            "gemm_inst_256x16.hip", "gemm_inst_128x16.hip", "gemm_inst_splitk16.hip", "chain_inst.hip", "attention_fwd.hip",
-           "attention_bwd.hip", "attention_capi.hip", "gemm_dispatch.hip", "probe_kernels.hip", "microbench.hip", "probe_dump.hip", "capi.cpp"]
+           "attention_bwd.hip", "attention_dkv.hip", "attention_capi.hip", "gemm_dispatch.hip", "probe_kernels.hip", "microbench.hip", "probe_dump.hip", "capi.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-mcode-object-version=5",
@@ -102,7 +102,12 @@ def _blocks(lines):
     return blocks, succ
 
 
-def check_mfma_fences(asm_text: str, where: str, tied=None) -> int:
+# sources whose kernels tie accumulators to other instructions by hand: every
+# matrix instruction is taken for one of them
+TIED_SOURCES = {"attention_dkv.hip"}
+
+
+def check_mfma_fences(asm_text: str, where: str, tied=None, prefix=None) -> int:
     """Walk each kernel's control-flow graph with the fact "a matrix
     instruction may have run since the last drain" (the drain: three s_nop 7
     in a row, 24 wait states), and reject an accumulator access (v_accvgpr_*)
@@ -114,13 +119,14 @@ def check_mfma_fences(asm_text: str, where: str, tied=None) -> int:
         inside a block and along single paths): an access in a block with
         two or more predecessors before any instruction of its own, the
         case in which this compiler was seen to omit the wait states.
+    `prefix`: the instructions meant, for kernels that tie others by hand.
     Also requires wait states (an s_nop) between the last accumulator write
     and the first instruction on the straight-line prologue.  Returns the
     number of kernels checked; raises RuntimeError naming each violation."""
     bad, checked = [], 0
     for name, lines in _kernels(asm_text).items():
         k_tied = any(t.startswith(TIED_MFMA) for t in lines) if tied is None else tied
-        mfma = TIED_MFMA if k_tied else "v_mfma_"
+        mfma = prefix or (TIED_MFMA if k_tied else "v_mfma_")
         idx = [i for i, t in enumerate(lines) if t.startswith(mfma)]
         if not idx:
             continue
@@ -171,7 +177,7 @@ def check_mfma_fences(asm_text: str, where: str, tied=None) -> int:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-    checked = src in CHECKED_SOURCES
+    checked = src in CHECKED_SOURCES | TIED_SOURCES
     extra = ["-save-temps=obj"] if checked else []   # keeps the device assembly in OBJDIR
     cmd = [HIPCC, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -182,7 +188,8 @@ def _compile(src: str) -> str:
         asm = os.path.join(OBJDIR, f"{stem}-hip-amdgcn-amd-amdhsa-gfx950.s")
         with open(asm) as f:
             text = f.read()
-        if check_mfma_fences(text, src) == 0:
+        how = dict(tied=True, prefix="v_mfma_") if src in TIED_SOURCES else {}
+        if check_mfma_fences(text, src, **how) == 0:
             raise RuntimeError(f"{src}: no kernel issues a matrix instruction")
     return obj
 

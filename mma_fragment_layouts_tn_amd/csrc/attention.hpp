@@ -46,6 +46,22 @@ struct Elem<_Float16> {
   static __device__ __forceinline__ floatx16 mma(vec8 a, vec8 b, floatx16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
+  // The sum tied to accumulation registers (mma_tied) or to ordinary ones
+  // (mma_begin from zero, mma_add): the compiler keeps the results of its own
+  // matrix instructions all in the one kind or all in the other.  It does not
+  // see these instructions' wait states; the kernels that use them say how
+  // they are kept.
+  static __device__ __forceinline__ void mma_begin(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ void mma_add(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ void mma_tied(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0"
+                 : "+a"(c)
+                 : "v"(a), "v"(b));
+  }
 };
 template <>
 struct Elem<__bf16> {
@@ -53,9 +69,34 @@ struct Elem<__bf16> {
   static __device__ __forceinline__ floatx16 mma(vec8 a, vec8 b, floatx16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
+  // The sum tied to accumulation registers (mma_tied) or to ordinary ones
+  // (mma_begin from zero, mma_add): the compiler keeps the results of its own
+  // matrix instructions all in the one kind or all in the other.  It does not
+  // see these instructions' wait states; the kernels that use them say how
+  // they are kept.
+  static __device__ __forceinline__ void mma_begin(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ void mma_add(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+  }
+  static __device__ __forceinline__ void mma_tied(vec8 a, vec8 b, floatx16& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+                 : "+a"(c)
+                 : "v"(a), "v"(b));
+  }
 };
 template <class T>
 using Vec8 = typename Elem<T>::vec8;
+
+// Between the last matrix instruction of a loop and the first use of its
+// sums: the wait states that the compiler does not see for tied sums, nor
+// always across blocks for others.
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
 
 // One launch of the forward kernels.  Sequence s of `batch` owns query tokens
 // [seq_q[s], seq_q[s+1]) (or q_len tokens each, from s * q_len, when seq_q is
@@ -169,11 +210,11 @@ __device__ __forceinline__ Vec8<T> load8(const T* p) {
 // and 16 further, where the swizzle is the same) are constant offsets: two
 // registers serve every read of a stage.
 //
-// The compiler lets an LDS read wait for every direct-to-LDS load in
+// The compiler lets a transposing read wait for every direct-to-LDS load in
 // flight unless it can tell them apart, which would take away the loads'
 // lead.  The kernels' steps are therefore functions of two restricted
 // pointers, to the stage they read (`stage` here) and to the ring they fill,
-// and every read is addressed from the first.  What orders a read behind the
+// and every such read is addressed from the first.  What orders a read behind the
 // loads it needs is its address, which at() forms behind the wait.
 using lds_c = __attribute__((address_space(3))) char*;
 template <class T, int DC>
@@ -199,7 +240,7 @@ struct Reader {
   // operand fragment of rows 32 b .. 32 b + 31, K chunk kk, `more` bytes on
   __device__ __forceinline__ Vec8<T> straight(int b, int kk, int more = 0) const {
     using ptr = const __attribute__((address_space(3))) Vec8<T>*;
-    return *(ptr)in_stage((s ^ (32u * kk)) + 64 * b * DC + more);
+    return *(ptr)((s ^ (32u * kk)) + 64 * b * DC + more);
   }
   // transposed: rows d = 32 db + l % 32; values the keys
   // 16 kc + 4 (l / 32) + 0..3 and 8 further
@@ -373,10 +414,12 @@ struct Fetch {
   // the tile's rows `row0` .. of `end` rows at `base`
   static __device__ __forceinline__ Fetch of(const T* base, int64_t stride, int row0, int end,
                                              int dim) {
-    const int rows = min(end - row0, 64);
-    const int bytes = rows > 0 ? 2 * ((rows - 1) * (int)stride + dim) : 0;
-    return Fetch{__builtin_amdgcn_make_buffer_rsrc((void*)(base + (int64_t)row0 * stride), 0, bytes,
-                                                   0x00027000)};
+    return at(base + (int64_t)row0 * stride, stride, end - row0, dim);
+  }
+  // `rows` rows (any number) from `row` on
+  static __device__ __forceinline__ Fetch at(const T* row, int64_t stride, int rows, int dim) {
+    const int bytes = rows > 0 ? 2 * ((min(rows, 64) - 1) * (int)stride + dim) : 0;
+    return Fetch{__builtin_amdgcn_make_buffer_rsrc((void*)row, 0, bytes, 0x00027000)};
   }
   // instruction i of the tile
   __device__ __forceinline__ void issue(int64_t stride, int dim, lds_c tile, int i,
@@ -512,7 +555,8 @@ __device__ __forceinline__ unsigned low_bits(int n) {
 }
 // all bits of x where bit r of the mask is set, else those of y
 __device__ __forceinline__ float select_bit(unsigned mask, int r, float x, float y) {
-  const unsigned m = (unsigned)__builtin_amdgcn_sbfe((int)mask, r, 1);
+  unsigned m = (unsigned)__builtin_amdgcn_sbfe((int)mask, r, 1);
+  asm("" : "+v"(m));   // two instructions, not a test and a choice
   return __builtin_bit_cast(float, (m & __builtin_bit_cast(unsigned, x)) |
                                        (~m & __builtin_bit_cast(unsigned, y)));
 }
@@ -653,6 +697,7 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
   };
   for (int c = c0; c < c1; ++c) step(c, ring + stage_of(c), ring);
   wait_vm<0>();
+  settle();
 
   l = both_sum(l);
   const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
@@ -770,6 +815,7 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
   };
   for (int i = 0; i < mine; ++i) step(i, ring + i % NST * 4 * TILE, ring);
   wait_vm<0>();
+  settle();
   // join: every wave scales its rows to the common maximum and leaves them in
   // LDS (16-byte group g of row r at g ^ (r & 15))
   l = both_sum(l);

@@ -17,17 +17,6 @@ KernelRef dq(int dc) {
          : dc == 128 ? KernelRef{(const void*)attention_dq<T, 128>, 64 * dq_waves<128>()}
                      : KernelRef{(const void*)attention_dq<T, 256>, 64 * dq_waves<256>()};
 }
-template <class T, int DC, int KW, int RW>
-KernelRef dkv_ref() {
-  static_assert(dkv_keys(DC) == 32 * KW && dkv_chunk(DC) == dkv_rows<DC>(), "tile");
-  return {(const void*)attention_dkv<T, DC, KW, RW>, 64 * KW * RW};
-}
-template <class T>
-KernelRef dkv(int dc) {
-  return dc == 64    ? dkv_ref<T, 64, 4, 2>()
-         : dc == 128 ? dkv_ref<T, 128, 4, 2>()
-                     : dkv_ref<T, 256, 4, 1>();
-}
 template <class T>
 KernelRef join(int dc) {
   return {dc == 64    ? (const void*)attention_dkv_join<T, 64>
@@ -38,7 +27,6 @@ KernelRef join(int dc) {
 }  // namespace
 
 KernelRef dq_kernel(bool bf16, int dc) { return bf16 ? dq<__bf16>(dc) : dq<_Float16>(dc); }
-KernelRef dkv_kernel(bool bf16, int dc) { return bf16 ? dkv<__bf16>(dc) : dkv<_Float16>(dc); }
 KernelRef dkv_join_kernel(bool bf16, int dc) {
   return bf16 ? join<__bf16>(dc) : join<_Float16>(dc);
 }

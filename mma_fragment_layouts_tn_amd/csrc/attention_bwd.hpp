@@ -190,51 +190,76 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
   };
   for (int c = 0; c < chunks; ++c) step(c, ring + c % NST * 4 * TILE, ring);
   wait_vm<0>();
+  settle();
   store_row<T, DC>((T*)p.dq + row.n * p.dq_tok + row.head * p.dq_head, acc, p.scale, p.dim, lane,
                    row.valid);
 }
 
 // ------------------------------------------------------------- dK and dV
-// KW x RW waves: wave w holds the 32 keys of key group w % KW and takes block
-// w / KW of each chunk's 32-row blocks; the row groups' sums are added in LDS
-// at the end.  Chunks of RC query tokens of one head at a time,
-// over the heads of the group.  Scores come with the rows in the registers
-// and the key in the lane (S = Q K^T, A operand from LDS), so P and dS are
-// the B operands of dV^T = dO^T P and dK^T = Q^T dS as they are.
+// KW x RW waves: wave w holds the 32 KB keys of key group w % KW and takes
+// block w / KW of each chunk's 32-row blocks; the row groups' sums are added
+// in LDS at the end.  Chunks of RC query tokens of one head at a time, over
+// the heads of the group.  Scores come with the rows in the registers and the
+// key in the lane (S = Q K^T, A operand from LDS), so P and dS are the B
+// operands of dV^T = dO^T P and dK^T = Q^T dS as they are, and every fragment
+// read from LDS serves the KB key blocks of the wave.
+//
+// With KB = 2 a wave's sums take all 256 accumulation registers, one wave per
+// SIMD, and K and V of the tile stay in LDS.  Two waves of 32 keys each instead issue twice the LDS
+// reads, waits and scalar instructions per matrix instruction, and those, not
+// the matrix pipe, set their pace: 4,600 cycles for 2,048 of matrix work.
 //
 // A tile's steps (chunks of all heads) are shared out over as many workgroups
-// as dkv_parts() says, in order; with more than one, their sums go to the
-// workspace and attention_dkv_join adds them in order.
+// as dkv_steps() says, in order; with more than one, their sums go to the
+// workspace and attention_dkv_join adds them in order.  The chunks that the
+// causal mask cuts come first, in a loop of their own: the mask as a branch
+// inside one loop made the compiler spill accumulators.
 template <int DC>
 MFL_HD constexpr int dkv_rows() { return DC == 256 ? 32 : 64; }
 
 struct DkvSteps {
-  int t0, per_head, steps, parts;
+  int first, cut, last;     // chunks: first that sees the tile, first without
+                            // hidden keys, last of the sequence
+  int steps, parts;
 };
-// first token that sees the tile's first key, chunks per head, chunks in all,
-// workgroups they are shared out over
 __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, const BwdPlace& at, int bn,
                                               int rc) {
   DkvSteps r;
-  r.t0 = p.causal ? max(at.tile * bn - (at.lk - at.lq), 0) / rc * rc : 0;
-  r.per_head = r.t0 < at.lq ? (at.lq - r.t0 + rc - 1) / rc : 0;
-  r.steps = r.per_head * p.group;
+  const int off = at.lk - at.lq, j0 = at.tile * bn;
+  r.last = (at.lq + rc - 1) / rc - 1;
+  r.first = r.cut = 0;
+  if (p.causal) {           // token t sees the keys up to t + off
+    r.first = max(j0 - off, 0) / rc;
+    r.cut = max((max(j0 + bn - 1 - off, 0) + rc - 1) / rc, r.first);
+    r.first = min(r.first, r.last + 1);
+    r.cut = min(r.cut, r.last + 1);
+  }
+  r.steps = (r.last + 1 - r.first) * p.group;
   r.parts = min(max((r.steps + p.part_steps - 1) / p.part_steps, 1), p.max_parts);
   return r;
 }
 
-template <class T, int DC, int KW, int RW>
+template <bool B>
+struct BoolC {
+  static constexpr bool value = B;
+};
+
+template <class T, int DC, int KW, int RW, int KB>
 __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p) {
-  constexpr int W = KW * RW, NST = DC == 64 ? 4 : DC == 128 ? 3 : 2, BN = 32 * KW,
+  // K of the tile in registers (else in LDS beside V)
+  constexpr bool KREG = DC == 256;
+  constexpr int W = KW * RW, NST = DC == 64 ? 4 : 2, BN = 32 * KW * KB,
                 RC = dkv_rows<DC>(), KS = DC / 16, ND = DC / 32, TILE = RC * DC,
                 NI = TILE / 512 / W, PER = 2 * NI + 1;   // loads per wave and stage
+  static_assert(KB <= 2, "key blocks");
   static_assert(RC == 32 * RW, "every row group has a block of each chunk");
-  static_assert(RW == 1 || (RW - 1) * KW * 32 * DC * 4 <= NST * 4 * TILE, "sums fit in the stages");
+  static_assert((RW - 1) * KW * 32 * DC * 4 <= NST * 4 * TILE, "sums fit in the stages");
   // one object: with a second one the compiler's bookkeeping of direct-to-LDS
   // loads makes every read wait for all of them
-  __shared__ __attribute__((aligned(4096))) T smem[NST * 2 * TILE + BN * DC + NST * 256];
-  float(*sstat)[2][64] = (float(*)[2][64])(smem + NST * 2 * TILE + BN * DC);
-  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE;   // sv: the tile's V, for all steps
+  constexpr int HELD = KREG ? 1 : 2;                     // the tile's V, and K
+  __shared__ __attribute__((aligned(4096))) T smem[NST * 2 * TILE + HELD * BN * DC + NST * 256];
+  float(*sstat)[2][64] = (float(*)[2][64])(smem + NST * 2 * TILE + HELD * BN * DC);
+  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE, sk = sv + 2 * BN * DC;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), kw = w % KW, rw = w / KW;
   int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv, heads = p.heads_kv * p.group;
@@ -254,110 +279,130 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   }
   const DkvSteps all = dkv_steps(p, at, BN, RC);
   if (part >= all.parts) return;
-  const int first = (int)((int64_t)all.steps * part / all.parts);
-  const int steps = (int)((int64_t)all.steps * (part + 1) / all.parts) - first;
-  const int j0 = at.tile * BN + 32 * kw, off = at.lk - at.lq, t0 = all.t0;
-  // The step fetched next.  Chunks start at multiples of RC and are walked
-  // from the sequence's end, so the workgroups of one head, whose first tokens
-  // differ, fetch the same chunks at the same time.
-  const int t_last = (at.lq - 1) / RC * RC;
-  int next = 0, next_head = kvh * p.group, next_t = t_last;
-  if (all.per_head > 0) {
-    next_head += first / all.per_head;
-    next_t -= first % all.per_head * RC;
-  }
-  int t = next_t;
+  const int first = uniform((int)((int64_t)all.steps * part / all.parts));
+  const int steps = uniform((int)((int64_t)all.steps * (part + 1) / all.parts)) - first;
+  const int j0 = at.tile * BN + 32 * KB * kw, off = at.lk - at.lq;
+
+  // Steps in order: the cut chunks of every head, then the others, each from
+  // the last chunk down, so that the workgroups of one kv head, whose first
+  // chunks differ, fetch the same chunks at about the same time.
+  struct Cursor {
+    int head, c, lo, hi;
+  };
+  auto cursor_at = [&](int s) {
+    const int cut_steps = (all.cut - all.first) * p.group;
+    Cursor u;
+    const bool cut = s < cut_steps;
+    u.lo = cut ? all.first : all.cut;
+    u.hi = cut ? all.cut - 1 : all.last;
+    if (!cut) s -= cut_steps;
+    const int n = max(u.hi + 1 - u.lo, 1);
+    u.head = uniform(s / n);
+    u.c = u.hi - uniform(s % n);
+    return u;
+  };
+  auto move = [&](Cursor& u) {
+    if (--u.c >= u.lo) return;
+    if (++u.head == p.group) {     // the cut chunks are done
+      u.head = 0;
+      u.lo = all.cut;
+      u.hi = all.last;
+    }
+    u.c = u.hi;
+  };
+  const int cut_here =
+      min(max((all.cut - all.first) * p.group - first, 0), steps);   // steps of the first loop
+  int left = steps;                                                  // steps to fetch
+  Cursor ahead = cursor_at(first), now = ahead;
+
+  // the loads of a step, one by one
   struct Next {
     Fetch<T, DC> q, g;
     __amdgpu_buffer_rsrc_t stat;
-    int stage;
   };
   auto advance = [&]() {
-    const int end = next < steps ? at.lq : 0;
-    Next n;
-    n.stage = next % NST;
-    n.q = Fetch<T, DC>::of((const T*)p.q + (int64_t)at.q0 * p.q_tok + next_head * p.q_head, p.q_tok,
-                           next_t, end, p.dim);
-    n.g = Fetch<T, DC>::of((const T*)p.dout + (int64_t)at.q0 * p.do_tok + next_head * p.do_head,
-                           p.do_tok, next_t, end, p.dim);
+    const int t = ahead.c * RC, head = kvh * p.group + ahead.head;
+    const int rows = left > 0 ? at.lq - t : 0;
+    const int64_t n = (int64_t)at.q0 + t;
+    Next x;
+    x.q = Fetch<T, DC>::at((const T*)p.q + n * p.q_tok + head * p.q_head, p.q_tok, rows, p.dim);
+    x.g =
+        Fetch<T, DC>::at((const T*)p.dout + n * p.do_tok + head * p.do_head, p.do_tok, rows, p.dim);
     // even waves fetch the log-sum-exps, odd waves the deltas, 64 at a time
     // (several waves the same: every wave has as many loads in flight)
-    n.stat = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(p.stats + ((int64_t)(w & 1) * heads + next_head) * p.total_q + at.q0 + next_t), 0,
-        4 * max(min(end - next_t, 64), 0), 0x00027000);
-    ++next;
-    next_t -= RC;
-    if (next_t < t0) {
-      next_t = t_last;
-      ++next_head;
-    }
-    return n;
+    x.stat = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(p.stats + ((int64_t)(w & 1) * heads + head) * p.total_q + n), 0,
+        uniform(rows > 64 ? 256 : rows > 0 ? 4 * rows : 0), 0x00027000);
+    --left;
+    move(ahead);
+    return x;
   };
-  auto issue = [&](const Next& n, lds_c to, int j) {
+  auto issue = [&](const Next& n, lds_c to, int stage, int j) {
     if (j < NI)
       n.q.issue(p.q_tok, p.dim, to, w * NI + j, lane);
     else if (j < 2 * NI)
       n.g.issue(p.do_tok, p.dim, to + 2 * TILE, w * NI + j - NI, lane);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(n.stat, (lds_t)(&sstat[n.stage][w & 1][0]), 4,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(n.stat, (lds_t)(&sstat[stage][w & 1][0]), 4,
                                                4u * lane, 0, 0, 0);
   };
-  const int key = j0 + (lane & 31);
-  const int64_t n = (int64_t)at.k0 + min(key, at.lk - 1);
-  const T* K = (const T*)p.k + n * p.k_tok + (int64_t)kvh * p.k_head;
-  Vec8<T> kf[KS];
-#pragma unroll
-  for (int kk = 0; kk < KS; ++kk) {
-    const int d = 16 * kk + 8 * (lane >> 5);
-    if (d < p.dim)
-      kf[kk] = load8(K + d);
-    else
-#pragma unroll
-      for (int e = 0; e < 8; ++e) kf[kk][e] = (T)0.0f;
-  }
+  const T* K = (const T*)p.k + (int64_t)at.k0 * p.k_tok + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + (int64_t)at.k0 * p.v_tok + (int64_t)kvh * p.v_head;
+  Vec8<T> kf[KREG ? KB : 1][KREG ? KS : 1];
+  if constexpr (KREG) {
+#pragma unroll
+    for (int x = 0; x < KB; ++x)
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        const int d = 16 * kk + 8 * (lane >> 5);
+        if (d < p.dim)
+          kf[x][kk] = load8(K + min(j0 + 32 * x + (lane & 31), at.lk - 1) * p.k_tok + d);
+        else
+#pragma unroll
+          for (int e = 0; e < 8; ++e) kf[x][kk][e] = (T)0.0f;
+      }
+  }
   // (64 rows at a time: what a descriptor covers)
   constexpr int NV = 64 * DC / 512 / W;
 #pragma unroll
   for (int b = 0; b < BN / 64; ++b) {
     const Fetch<T, DC> f = Fetch<T, DC>::of(V, p.v_tok, at.tile * BN + 64 * b, at.lk, p.dim);
+    const Fetch<T, DC> g = Fetch<T, DC>::of(K, p.k_tok, at.tile * BN + 64 * b, at.lk, p.dim);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
       f.issue(p.v_tok, p.dim, sv + 128 * b * DC, w * NV + j, lane);
+      if (!KREG) g.issue(p.k_tok, p.dim, sk + 128 * b * DC, w * NV + j, lane);
+    }
   }
-  floatx16 dk[ND], dv[ND];
-  zero(dk);
-  zero(dv);
+  floatx16 dk[KB][ND], dv[KB][ND];
+#pragma unroll
+  for (int x = 0; x < KB; ++x) {
+    zero(dk[x]);
+    zero(dv[x]);
+  }
 
-  // 32 rows of a stage, the tokens from tb on, in 4 KS slots of one matrix
-  // instruction each, pinned in this order: S; dP, under which P is formed;
-  // dV, under which dS is formed; dK.  Fragments are read RA slots ahead; the
-  // next stage's loads are spread over the slots.
+  // 32 rows of a stage in 4 KS KB slots of one matrix instruction each,
+  // pinned in this order: S; dP, under which P is formed; dV, under which dS
+  // is formed; dK.  Fragments are read RA fragments ahead; the next stage's
+  // loads are spread over the slots.
 #ifndef RAV
 #define RAV 2
 #endif
   constexpr int RA = RAV;
   auto block = [&](const Reader<T, DC>& rd, const Reader<T, DC>& rv, const float* stat, int tb,
-                   const Next& nx, lds_c to) {
-    auto load_at = [&](int n) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if ((2 * j + 1) * 4 * KS / (2 * PER) == n) issue(nx, to, j);
-    };
-    floatx16 st, dp;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) st[i] = dp[i] = 0.0f;
+                   const Next& nx, lds_c to, int stage, auto masked) {
+    floatx16 st[KB], dp[KB];
     const float* ps = stat + 4 * (lane >> 5);
-    Vec8<T> fr[RA + 1], fv[RA + 1], pf[2], df[2];
+    Vec8<T> fr[RA + 1], fv[RA + 1][KB], pf[KB][2], df[KB][2];
+    // bit r: row r of the 32 (+ 4 in the upper half of the wave) sees the
+    // lane's key
+    unsigned rows[KB];
+    if constexpr (decltype(masked)::value)
+#pragma unroll
+      for (int x = 0; x < KB; ++x)
+        rows[x] = ~low_bits(j0 + 32 * x + (lane & 31) - off - tb - 4 * (lane >> 5));
     // values formed per slot of dP and dV, in groups of four with one read of
     // their rows' log-sum-exps and deltas
-    // Bit r: row r of the 32 (+ 4 in the upper half of the wave) exists and
-    // sees the lane's key.  Two instructions per weight in every block; as a
-    // branch taken by the few blocks that need it, it made the compiler spill
-    // accumulators.
-    const int from = max((p.causal ? key - off - tb : 0) - 4 * (lane >> 5), 0);
-    const int to_ = at.lq - tb - 4 * (lane >> 5);
-    const unsigned rows = low_bits(to_) & ~low_bits(from);
     constexpr int E = 16 / KS, NQ = (RA * E + 3) / 4 + 1;
     floatx4 stats[NQ];
     auto read = [&](int n) {
@@ -368,83 +413,143 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
             *(const floatx4*)(ps + (ph - 1) * 64 + 8 * (kk * E / 4));
       Vec8<T>& f = fr[n % (RA + 1)];
       if (ph == 0) f = rd.straight(0, kk);
-      if (ph == 1) {
-        f = rd.straight(0, kk, 2 * TILE);
-        fv[n % (RA + 1)] = rv.straight(0, kk);
-      }
+      if (ph == 1) f = rd.straight(0, kk, 2 * TILE);
+      if (ph == 1 || (ph == 0 && !KREG))
+#pragma unroll
+        for (int x = 0; x < KB; ++x)
+          fv[n % (RA + 1)][x] = rv.straight(x, kk, ph == 0 ? 2 * BN * DC : 0);
       if (ph == 2) f = rd.transposed(kk / ND, kk % ND, 2 * TILE);
       if (ph == 3) f = rd.transposed(kk / ND, kk % ND);
     };
+    auto load_at = [&](int n) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if ((2 * j + 1) * 4 * KS / (2 * PER) == n) issue(nx, to, stage, j);
+    };
 #pragma unroll
     for (int n = 0; n < RA; ++n) read(n);
-#pragma unroll
-    for (int n = 0; n < KS; ++n) {
-      read(n + RA);
-      st = Elem<T>::mma(fr[n % (RA + 1)], kf[n], st);
-      load_at(n);
+    // Before the first use of st (dp): its last instruction has run for the
+    // 8 passes that the first of the next product waited for the matrix pipe,
+    // and for 16 more here, with KB = 2 for 8 passes of the other key block's
+    // too (19 are asked for).
+    auto scores_done = [&](floatx16(&z)[KB]) {
       __builtin_amdgcn_sched_barrier(0);
+      if constexpr (KB == 1)
+        asm volatile("s_nop 7\n\ts_nop 7" : "+v"(z[0]));
+      else
+        asm volatile("s_nop 7\n\ts_nop 7" : "+v"(z[0]), "+v"(z[KB - 1]));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto slot_done = [&](int n, int x) {
+      if (x == 0) load_at(n);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int m = 0; m < KS; ++m) {
+      read(m + RA);
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        const Vec8<T>& kx = KREG ? kf[KREG ? x : 0][KREG ? m : 0] : fv[m % (RA + 1)][x];
+        if (m == 0)
+          Elem<T>::mma_begin(fr[0], kx, st[x]);
+        else
+          Elem<T>::mma_add(fr[m % (RA + 1)], kx, st[x]);
+        slot_done(m, x);
+      }
     }
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       const int n = KS + m;
       read(n + RA);
-      dp = Elem<T>::mma(fr[n % (RA + 1)], fv[n % (RA + 1)], dp);
-      load_at(n);
 #pragma unroll
-      for (int i = m * E; i < m * E + E; ++i)
-        st[i] = select_bit(rows, 8 * (i / 4) + i % 4,
-                           __builtin_amdgcn_exp2f(__builtin_fmaf(
-                               st[i], p.scale_log2, -stats[i / 4 % NQ][i % 4])),
-                           0.0f);
-      if (m * E + E == 8) pf[0] = pack8<T>(st, 0);
-      if (m * E + E == 16) pf[1] = pack8<T>(st, 1);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int x = 0; x < KB; ++x) {
+        if (m == 0)
+          Elem<T>::mma_begin(fr[n % (RA + 1)], fv[n % (RA + 1)][x], dp[x]);
+        else
+          Elem<T>::mma_add(fr[n % (RA + 1)], fv[n % (RA + 1)][x], dp[x]);
+        if (m == 0 && x == 0) scores_done(st);
+#pragma unroll
+        for (int i = m * E; i < m * E + E; ++i) {
+          float v = __builtin_amdgcn_exp2f(
+              __builtin_fmaf(st[x][i], p.scale_log2, -stats[i / 4 % NQ][i % 4]));
+          if constexpr (decltype(masked)::value)
+            v = select_bit(rows[x], 8 * (i / 4) + i % 4, v, 0.0f);
+          st[x][i] = v;
+        }
+        if (m * E + E == 8) pf[x][0] = pack8<T>(st[x], 0);
+        if (m * E + E == 16) pf[x][1] = pack8<T>(st[x], 1);
+        slot_done(n, x);
+      }
     }
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       const int n = 2 * KS + m;
       read(n + RA);
-      dv[m % ND] = Elem<T>::mma(fr[n % (RA + 1)], pf[m / ND], dv[m % ND]);
-      load_at(n);
 #pragma unroll
-      for (int i = m * E; i < m * E + E; ++i)
-        dp[i] = st[i] * (dp[i] - stats[(4 + i / 4) % NQ][i % 4]);
-      if (m * E + E == 8) df[0] = pack8<T>(dp, 0);
-      if (m * E + E == 16) df[1] = pack8<T>(dp, 1);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int x = 0; x < KB; ++x) {
+        Elem<T>::mma_tied(fr[n % (RA + 1)], pf[x][m / ND], dv[x][m % ND]);
+        if (m == 0 && x == 0) scores_done(dp);
+#pragma unroll
+        for (int i = m * E; i < m * E + E; ++i)
+          dp[x][i] = st[x][i] * (dp[x][i] - stats[(4 + i / 4) % NQ][i % 4]);
+        if (m * E + E == 8) df[x][0] = pack8<T>(dp[x], 0);
+        if (m * E + E == 16) df[x][1] = pack8<T>(dp[x], 1);
+        slot_done(n, x);
+      }
     }
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       const int n = 3 * KS + m;
       read(n + RA);
-      dk[m % ND] = Elem<T>::mma(fr[n % (RA + 1)], df[m / ND], dk[m % ND]);
-      load_at(n);
-      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < KB; ++x) {
+        Elem<T>::mma_tied(fr[n % (RA + 1)], df[x][m / ND], dk[x][m % ND]);
+        slot_done(n, x);
+      }
     }
   };
 
   const Reader<T, DC> reader = Reader<T, DC>::of(lane);
-  // step it on the tokens from t on, while step it + NST - 1 is fetched; every
-  // step issues PER loads
-  auto step = [&](int it, lds_c __restrict__ from, lds_c __restrict__ to,
-                  lds_c __restrict__ values) {
+  // step it, while step it + NST - 1 is fetched; every step issues PER loads
+  auto step = [&](int it, lds_c __restrict__ from, lds_c __restrict__ to, auto masked) {
     if (it == hidden(0)) {
 #pragma unroll
       for (int s = 0; s < NST - 1; ++s) {
         const Next nx = advance();
 #pragma unroll
-        for (int j = 0; j < PER; ++j) issue(nx, to + 4 * s * TILE, j);
+        for (int j = 0; j < PER; ++j) issue(nx, to + 4 * s * TILE, s, j);
       }
     }
     wait_vm<(NST - 2) * PER>();
     barrier();
     const Next nx = advance();
-    block(reader.at(from, 64 * DC * rw), reader.at(values, 64 * DC * kw), &sstat[it % NST][0][32 * rw],
-          t + 32 * rw, nx, to + (it + NST - 1) % NST * 4 * TILE);
+    const int stage = (it + NST - 1) % NST;
+    block(reader.at(from, 64 * DC * rw), reader.at(sv, 64 * DC * KB * kw),
+          &sstat[it % NST][0][32 * rw], now.c * RC + 32 * rw, nx, to + stage * 4 * TILE, stage,
+          masked);
   };
-  for (int it = 0; it < steps; ++it) {
-    step(it, ring + it % NST * 4 * TILE, ring, sv);
-    t = t - RC < t0 ? t_last : t - RC;
+  // the sums may be moved or read from here on
+  auto settled = [&]() {
+    settle();
+#pragma unroll
+    for (int x = 0; x < KB; ++x)
+#pragma unroll
+      for (int db = 0; db < ND; ++db) asm volatile("" : "+a"(dk[x][db]), "+a"(dv[x][db]));
+  };
+  // (settled inside the conditions: where the paths meet is too late)
+  int it = 0;
+  if (it < cut_here) {
+    do {
+      step(it, ring + it % NST * 4 * TILE, ring, BoolC<true>{});
+      move(now);
+    } while (++it < cut_here);
+    settled();
+  }
+  if (it < steps) {
+    do {
+      step(it, ring + it % NST * 4 * TILE, ring, BoolC<false>{});
+    } while (++it < steps);
+    settled();
   }
   wait_vm<0>();
   // the row groups' sums: group 0 adds the others', register by register
@@ -474,28 +579,39 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
             }
       }
     };
-    add(dk);
-    add(dv);
+#pragma unroll
+    for (int x = 0; x < KB; ++x) {
+      add(dk[x]);
+      add(dv[x]);
+    }
     if (rw > 0) return;
   }
-  const bool valid = key < at.lk;
-  if (all.parts > 1) {
-    const int64_t stride = (int64_t)p.total_k * p.heads_kv * DC;
-    float* o = p.partials + 2 * part * stride + (n * p.heads_kv + kvh) * DC + 4 * (lane >> 5);
-    if (valid)
 #pragma unroll
-      for (int db = 0; db < ND; ++db)
+  for (int x = 0; x < KB; ++x) {
+    const int key = j0 + 32 * x + (lane & 31);
+    const bool valid = key < at.lk;
+    const int64_t n = (int64_t)at.k0 + min(key, at.lk - 1);
+    if (all.parts > 1) {
+      const int64_t stride = (int64_t)p.total_k * p.heads_kv * DC;
+      float* o = p.partials + 2 * part * stride + (n * p.heads_kv + kvh) * DC + 4 * (lane >> 5);
+      if (valid)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          *(floatx4*)(o + 32 * db + 8 * q) = floatx4{dk[db][4 * q], dk[db][4 * q + 1],
-                                                     dk[db][4 * q + 2], dk[db][4 * q + 3]};
-          *(floatx4*)(o + stride + 32 * db + 8 * q) = floatx4{
-              dv[db][4 * q], dv[db][4 * q + 1], dv[db][4 * q + 2], dv[db][4 * q + 3]};
-        }
-    return;
+        for (int db = 0; db < ND; ++db)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            *(floatx4*)(o + 32 * db + 8 * q) =
+                floatx4{dk[x][db][4 * q], dk[x][db][4 * q + 1], dk[x][db][4 * q + 2],
+                        dk[x][db][4 * q + 3]};
+            *(floatx4*)(o + stride + 32 * db + 8 * q) =
+                floatx4{dv[x][db][4 * q], dv[x][db][4 * q + 1], dv[x][db][4 * q + 2],
+                        dv[x][db][4 * q + 3]};
+          }
+    } else {
+      store_row<T, DC>((T*)p.dk + n * p.dk_tok + kvh * p.dk_head, dk[x], p.scale, p.dim, lane,
+                       valid);
+      store_row<T, DC>((T*)p.dv + n * p.dv_tok + kvh * p.dv_head, dv[x], 1.0f, p.dim, lane, valid);
+    }
   }
-  store_row<T, DC>((T*)p.dk + n * p.dk_tok + kvh * p.dk_head, dk, p.scale, p.dim, lane, valid);
-  store_row<T, DC>((T*)p.dv + n * p.dv_tok + kvh * p.dv_head, dv, 1.0f, p.dim, lane, valid);
 }
 
 // The parts' sums of a tile whose steps were shared out, in part order; a

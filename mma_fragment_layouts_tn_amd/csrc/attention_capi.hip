@@ -246,6 +246,9 @@ int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* 
                       a.dv_token, a.dv_head});
   if (!rc) rc = check_token_strides({a.dout_token});
   if (rc) return rc;
+  // rows past a sequence's end must lie past its rows
+  if ((f.total_q > 1) && (f.q_token < f.head_dim || a.dout_token < f.head_dim))
+    return MFL_E_LEADING_DIM;
   const void* grads[3] = {dq, dk, dv};
   const void* inputs[6] = {dout, q, k, v, out, lse};
   if (!aligned(dout)) return MFL_E_MISALIGNED;
@@ -436,7 +439,8 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.group = (int)(f.heads_q / f.heads_kv);
   p.dim = (int)f.head_dim;
   p.causal = f.causal;
-  p.q_tok = f.q_token;
+  // (a single token's stride is not read, but must lead past its row)
+  p.q_tok = f.total_q > 1 ? f.q_token : f.head_dim;
   p.q_head = f.q_head;
   p.k_tok = f.k_token;
   p.k_head = f.k_head;
@@ -444,7 +448,7 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.v_head = f.v_head;
   p.o_tok = f.out_token;
   p.o_head = f.out_head;
-  p.do_tok = a->dout_token;
+  p.do_tok = f.total_q > 1 ? a->dout_token : f.head_dim;
   p.do_head = a->dout_head;
   p.dq_tok = a->dq_token;
   p.dq_head = a->dq_head;
