@@ -58,7 +58,7 @@ struct Elem<_Float16> {
     asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ void mma_tied(vec8 a, vec8 b, floatx16& c) {
-    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0"
+    asm volatile("v_mfma_f32_32x32x16_f16 %0, %1, %2, %0"
                  : "+a"(c)
                  : "v"(a), "v"(b));
   }
@@ -81,7 +81,7 @@ struct Elem<__bf16> {
     asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
   }
   static __device__ __forceinline__ void mma_tied(vec8 a, vec8 b, floatx16& c) {
-    asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
+    asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0"
                  : "+a"(c)
                  : "v"(a), "v"(b));
   }

@@ -214,9 +214,6 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
 // workspace and attention_dkv_join adds them in order.  The chunks that the
 // causal mask cuts come first, in a loop of their own: the mask as a branch
 // inside one loop made the compiler spill accumulators.
-template <int DC>
-MFL_HD constexpr int dkv_rows() { return DC == 256 ? 32 : 64; }
-
 struct DkvSteps {
   int first, cut, last;     // chunks: first that sees the tile, first without
                             // hidden keys, last of the sequence
@@ -246,20 +243,20 @@ struct BoolC {
 
 template <class T, int DC, int KW, int RW, int KB>
 __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p) {
-  // K of the tile in registers (else in LDS beside V)
-  constexpr bool KREG = DC == 256;
-  constexpr int W = KW * RW, NST = DC == 64 ? 4 : 2, BN = 32 * KW * KB,
-                RC = dkv_rows<DC>(), KS = DC / 16, ND = DC / 32, TILE = RC * DC,
-                NI = TILE / 512 / W, PER = 2 * NI + 1;   // loads per wave and stage
-  static_assert(KB <= 2, "key blocks");
-  static_assert(RC == 32 * RW, "every row group has a block of each chunk");
+  // the tile's K and V in registers (else in LDS for all steps)
+  constexpr bool KREG = true, VREG = DC == 64;
+  constexpr int W = KW * RW, NST = DC == 256 ? 2 : 4, BN = 32 * KW * KB, RC = 32 * RW,
+                KS = DC / 16, ND = DC / 32, TILE = RC * DC, NI = TILE / 512 / W,
+                PER = 2 * NI + 1;                        // loads per wave and stage
+  static_assert(KB <= 2 && NI >= 1, "key blocks, loads");
   static_assert((RW - 1) * KW * 32 * DC * 4 <= NST * 4 * TILE, "sums fit in the stages");
   // one object: with a second one the compiler's bookkeeping of direct-to-LDS
   // loads makes every read wait for all of them
-  constexpr int HELD = KREG ? 1 : 2;                     // the tile's V, and K
+  constexpr int HELD = (KREG ? 0 : 1) + (VREG ? 0 : 1);
   __shared__ __attribute__((aligned(4096))) T smem[NST * 2 * TILE + HELD * BN * DC + NST * 256];
   float(*sstat)[2][64] = (float(*)[2][64])(smem + NST * 2 * TILE + HELD * BN * DC);
-  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE, sk = sv + 2 * BN * DC;
+  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE,
+              sk = sv + (VREG ? 0 : 2 * BN * DC);
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), kw = w % KW, rw = w / KW;
   int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv, heads = p.heads_kv * p.group;
@@ -348,20 +345,19 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   };
   const T* K = (const T*)p.k + (int64_t)at.k0 * p.k_tok + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + (int64_t)at.k0 * p.v_tok + (int64_t)kvh * p.v_head;
-  Vec8<T> kf[KREG ? KB : 1][KREG ? KS : 1];
-  if constexpr (KREG) {
+  Vec8<T> kf[KREG ? KB : 1][KREG ? KS : 1], vf[VREG ? KB : 1][VREG ? KS : 1];
 #pragma unroll
-    for (int x = 0; x < KB; ++x)
+  for (int x = 0; x < KB; ++x)
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        const int d = 16 * kk + 8 * (lane >> 5);
-        if (d < p.dim)
-          kf[x][kk] = load8(K + min(j0 + 32 * x + (lane & 31), at.lk - 1) * p.k_tok + d);
-        else
+    for (int kk = 0; kk < KS; ++kk) {
+      const int d = 16 * kk + 8 * (lane >> 5);
+      const int64_t n = min(j0 + 32 * x + (lane & 31), at.lk - 1);
+      Vec8<T> none;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) kf[x][kk][e] = (T)0.0f;
-      }
-  }
+      for (int e = 0; e < 8; ++e) none[e] = (T)0.0f;
+      if constexpr (KREG) kf[x][kk] = d < p.dim ? load8(K + n * p.k_tok + d) : none;
+      if constexpr (VREG) vf[x][kk] = d < p.dim ? load8(V + n * p.v_tok + d) : none;
+    }
   // (64 rows at a time: what a descriptor covers)
   constexpr int NV = 64 * DC / 512 / W;
 #pragma unroll
@@ -370,7 +366,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
     const Fetch<T, DC> g = Fetch<T, DC>::of(K, p.k_tok, at.tile * BN + 64 * b, at.lk, p.dim);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      f.issue(p.v_tok, p.dim, sv + 128 * b * DC, w * NV + j, lane);
+      if (!VREG) f.issue(p.v_tok, p.dim, sv + 128 * b * DC, w * NV + j, lane);
       if (!KREG) g.issue(p.k_tok, p.dim, sk + 128 * b * DC, w * NV + j, lane);
     }
   }
@@ -382,13 +378,16 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   }
 
   // 32 rows of a stage in 4 KS KB slots of one matrix instruction each,
-  // pinned in this order: S; dP, under which P is formed; dV, under which dS
-  // is formed; dK.  Fragments are read RA fragments ahead; the next stage's
-  // loads are spread over the slots.
+  // pinned in this order: S, dP, dV, dK.  Weight i of a key block is formed
+  // under dP (i < 8) or the first half of dV, its score gradient under the
+  // second half of dV (i < 8) or the first half of dK: what an instruction
+  // takes is ready half a phase before, and the vector work is spread over
+  // three of the four phases.  Fragments are read RA fragments ahead; the next
+  // stage's loads are spread over the slots.
 #ifndef RAV
 #define RAV 2
 #endif
-  constexpr int RA = RAV;
+  constexpr int RA = RAV, H = KS / 2;
   auto block = [&](const Reader<T, DC>& rd, const Reader<T, DC>& rv, const float* stat, int tb,
                    const Next& nx, lds_c to, int stage, auto masked) {
     floatx16 st[KB], dp[KB];
@@ -401,33 +400,55 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
 #pragma unroll
       for (int x = 0; x < KB; ++x)
         rows[x] = ~low_bits(j0 + 32 * x + (lane & 31) - off - tb - 4 * (lane >> 5));
-    // values formed per slot of dP and dV, in groups of four with one read of
-    // their rows' log-sum-exps and deltas
-    constexpr int E = 16 / KS, NQ = (RA * E + 3) / 4 + 1;
-    floatx4 stats[NQ];
     auto read = [&](int n) {
       if (n >= 4 * KS) return;
       const int ph = n / KS, kk = n % KS;
-      if ((ph == 1 || ph == 2) && kk * E % 4 == 0)
-        stats[(4 * (ph - 1) + kk * E / 4) % NQ] =
-            *(const floatx4*)(ps + (ph - 1) * 64 + 8 * (kk * E / 4));
       Vec8<T>& f = fr[n % (RA + 1)];
       if (ph == 0) f = rd.straight(0, kk);
       if (ph == 1) f = rd.straight(0, kk, 2 * TILE);
-      if (ph == 1 || (ph == 0 && !KREG))
+      if ((ph == 0 && !KREG) || (ph == 1 && !VREG))
 #pragma unroll
         for (int x = 0; x < KB; ++x)
-          fv[n % (RA + 1)][x] = rv.straight(x, kk, ph == 0 ? 2 * BN * DC : 0);
+          fv[n % (RA + 1)][x] = rv.straight(x, kk, ph == 0 ? (int)(sk - sv) : 0);
       if (ph == 2) f = rd.transposed(kk / ND, kk % ND, 2 * TILE);
       if (ph == 3) f = rd.transposed(kk / ND, kk % ND);
+    };
+    // Vector work: unit u of 32 covers value u % 16; units 0 - 15 form the
+    // weights, 16 - 31 the score gradients.  Unit 0 starts with dP's slot 0,
+    // and a quarter of the units goes to each half phase (the first two
+    // quarters' first eight values to all of dP).  Rows' log-sum-exps and
+    // deltas come four at a time, read a group ahead.
+    floatx4 stats[2];
+    auto read_stats = [&](int g) {   // g 0 - 3: log-sum-exps, 4 - 7: deltas
+      if (g < 8) stats[g % 2] = *(const floatx4*)(ps + (g / 4) * 64 + 8 * (g % 4));
+    };
+    auto unit = [&](int x, int u) {
+      const int i = u % 16;
+      if (u < 16) {
+        float v = __builtin_amdgcn_exp2f(
+            __builtin_fmaf(st[x][i], p.scale_log2, -stats[u / 4 % 2][i % 4]));
+        if constexpr (decltype(masked)::value)
+          v = select_bit(rows[x], 8 * (i / 4) + i % 4, v, 0.0f);
+        st[x][i] = v;
+      } else {
+        dp[x][i] = st[x][i] * (dp[x][i] - stats[u / 4 % 2][i % 4]);
+      }
+      if (i % 8 == 7) {
+        Vec8<T>& f = u < 16 ? pf[x][i / 8] : df[x][i / 8];
+        f = pack8<T>(u < 16 ? st[x] : dp[x], i / 8);
+        asm volatile("" : "+v"(f));   // here, not where it is used
+      }
+    };
+    // units of slot n's frag: 8 over dP's KS, then 8 over each half phase
+    auto units_from = [&](int n) {
+      const int m = n - KS;
+      return m <= 0 ? 0 : m <= KS ? 8 * m / KS : m >= 2 * KS + H ? 32 : 8 + 8 * (m - KS) / H;
     };
     auto load_at = [&](int n) {
 #pragma unroll
       for (int j = 0; j < PER; ++j)
         if ((2 * j + 1) * 4 * KS / (2 * PER) == n) issue(nx, to, stage, j);
     };
-#pragma unroll
-    for (int n = 0; n < RA; ++n) read(n);
     // Before the first use of st (dp): its last instruction has run for the
     // 8 passes that the first of the next product waited for the matrix pipe,
     // and for 16 more here, with KB = 2 for 8 passes of the other key block's
@@ -440,10 +461,20 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
         asm volatile("s_nop 7\n\ts_nop 7" : "+v"(z[0]), "+v"(z[KB - 1]));
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto slot_done = [&](int n, int x) {
-      if (x == 0) load_at(n);
+    // after the matrix instruction of slot (n, x): its share of vector work
+    // and loads
+    auto fill = [&](int n, int x) {
+#pragma unroll
+      for (int u = units_from(n); u < units_from(n + 1); ++u) {
+        if (x == 0 && u % 4 == 0) read_stats(u / 4 + 1);
+        unit(x, u);
+      }
+      if (x == KB - 1) load_at(n);
       __builtin_amdgcn_sched_barrier(0);
     };
+    read_stats(0);
+#pragma unroll
+    for (int n = 0; n < RA; ++n) read(n);
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       read(m + RA);
@@ -454,7 +485,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
           Elem<T>::mma_begin(fr[0], kx, st[x]);
         else
           Elem<T>::mma_add(fr[m % (RA + 1)], kx, st[x]);
-        slot_done(m, x);
+        fill(m, x);
       }
     }
 #pragma unroll
@@ -463,48 +494,36 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       read(n + RA);
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
+        const Vec8<T>& vx = VREG ? vf[VREG ? x : 0][VREG ? m : 0] : fv[n % (RA + 1)][x];
         if (m == 0)
-          Elem<T>::mma_begin(fr[n % (RA + 1)], fv[n % (RA + 1)][x], dp[x]);
+          Elem<T>::mma_begin(fr[n % (RA + 1)], vx, dp[x]);
         else
-          Elem<T>::mma_add(fr[n % (RA + 1)], fv[n % (RA + 1)][x], dp[x]);
+          Elem<T>::mma_add(fr[n % (RA + 1)], vx, dp[x]);
         if (m == 0 && x == 0) scores_done(st);
-#pragma unroll
-        for (int i = m * E; i < m * E + E; ++i) {
-          float v = __builtin_amdgcn_exp2f(
-              __builtin_fmaf(st[x][i], p.scale_log2, -stats[i / 4 % NQ][i % 4]));
-          if constexpr (decltype(masked)::value)
-            v = select_bit(rows[x], 8 * (i / 4) + i % 4, v, 0.0f);
-          st[x][i] = v;
-        }
-        if (m * E + E == 8) pf[x][0] = pack8<T>(st[x], 0);
-        if (m * E + E == 16) pf[x][1] = pack8<T>(st[x], 1);
-        slot_done(n, x);
+        fill(n, x);
       }
     }
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       const int n = 2 * KS + m;
       read(n + RA);
+      if (KB == 1 && m == H) asm volatile("s_nop 1");   // pf[0][1] is a slot old
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
         Elem<T>::mma_tied(fr[n % (RA + 1)], pf[x][m / ND], dv[x][m % ND]);
-        if (m == 0 && x == 0) scores_done(dp);
-#pragma unroll
-        for (int i = m * E; i < m * E + E; ++i)
-          dp[x][i] = st[x][i] * (dp[x][i] - stats[(4 + i / 4) % NQ][i % 4]);
-        if (m * E + E == 8) df[x][0] = pack8<T>(dp[x], 0);
-        if (m * E + E == 16) df[x][1] = pack8<T>(dp[x], 1);
-        slot_done(n, x);
+        if (m == H && x == 0) scores_done(dp);
+        fill(n, x);
       }
     }
 #pragma unroll
     for (int m = 0; m < KS; ++m) {
       const int n = 3 * KS + m;
       read(n + RA);
+      if (KB == 1 && m % H == 0) asm volatile("s_nop 1");
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
         Elem<T>::mma_tied(fr[n % (RA + 1)], df[x][m / ND], dk[x][m % ND]);
-        slot_done(n, x);
+        fill(n, x);
       }
     }
   };

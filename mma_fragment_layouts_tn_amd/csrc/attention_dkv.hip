@@ -10,14 +10,14 @@ namespace mfl {
 namespace att {
 namespace {
 #ifndef V64
-#define V64 4,2,1
+#define V64 2,2,2
 #endif
 #ifndef V128
-#define V128 2,2,2
+#define V128 4,1,2
 #endif
 template <class T, int DC, int KW, int RW, int KB>
 KernelRef dkv_ref() {
-  static_assert(dkv_keys(DC) == 32 * KW * KB && dkv_chunk(DC) == dkv_rows<DC>(), "tile");
+  static_assert(dkv_keys(DC) == 32 * KW * KB && dkv_chunk(DC) == 32 * RW, "tile");
   return {(const void*)attention_dkv<T, DC, KW, RW, KB>, 64 * KW * RW};
 }
 template <class T>

@@ -28,8 +28,16 @@ constexpr int dim_class(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 
 // rows (forward, dQ) and keys (dK, dV) per workgroup
 constexpr int tile_rows(int algo) { return algo == 3 ? 32 : algo == 2 ? 128 : 256; }
 constexpr int dq_rows(int dc) { return dc == 256 ? 128 : 256; }
-constexpr int dkv_keys(int) { return 128; }
-constexpr int dkv_chunk(int dc) { return dc == 256 ? 32 : 64; }
+#ifndef K64
+#define K64 128
+#define C64 64
+#endif
+#ifndef K128
+#define K128 256
+#define C128 32
+#endif
+constexpr int dkv_keys(int dc) { return dc == 64 ? K64 : dc == 128 ? K128 : 128; }
+constexpr int dkv_chunk(int dc) { return dc == 256 ? 32 : dc == 64 ? C64 : C128; }
 
 }  // namespace att
 }  // namespace mfl
