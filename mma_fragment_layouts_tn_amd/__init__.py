@@ -22,7 +22,8 @@ import numpy as np
 
 from . import _attention
 from ._attention import (ATTENTION_ALGOS, BF16, AttentionArgs, AttentionGradArgs,  # noqa: F401
-                         AttentionPrefixArgs)
+                         AttentionPrefixArgs, attention, attention_backward, attention_plan,
+                         attention_prefix)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmfl_gemm.so")
@@ -148,7 +149,6 @@ def _load() -> ctypes.CDLL:
     lib.mfl_bench_lds_read.restype = ctypes.c_int
     lib.mfl_wall_clock_khz.argtypes = [P(i32)]
     lib.mfl_wall_clock_khz.restype = ctypes.c_int
-    _attention.declare(lib)
     return lib
 
 
@@ -259,7 +259,7 @@ def gemm_tn(A: torch.Tensor, B: torch.Tensor, C: Optional[torch.Tensor] = None,
 
 
 # ------------------------------------------------------------ attention
-attention, attention_plan, attention_backward, attention_prefix = _attention.bind(_lib, _check)
+_attention.bind(_lib, _check)   # attention, attention_backward, attention_prefix
 
 
 # ------------------------------------------------------- back-to-back GEMM

@@ -6,7 +6,6 @@ of the operators runs in the HIP kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 from typing import Optional, Tuple
@@ -65,22 +64,45 @@ def declare(lib: ctypes.CDLL) -> None:
 
 
 # ---------------------------------------------------------------- marshalling
+_lib = None        # the loaded library and the caller's check of its codes
+_check = None
+_E_WORKSPACE = -10
+
+
+def bind(lib: ctypes.CDLL, check) -> None:
+    """Give the functions below their library."""
+    global _lib, _check
+    declare(lib)
+    _lib, _check = lib, check
+
+
 class _Run:
     """Where a call runs: the tensors' device and the stream.  Outputs and
     workspaces are allocated for the stream that uses them; on a stream that
     is not the current one the caller's tensors are recorded there too."""
 
-    def __init__(self, device, stream, tensors):
-        self.device = device
-        cur = torch.cuda.current_stream(device)
-        self.handle = cur.cuda_stream if stream is None else int(stream)
-        self.cur = self.other = None
-        if self.handle != cur.cuda_stream:
-            self.cur = cur
-            self.other = torch.cuda.ExternalStream(self.handle, device=device)
+    __slots__ = ("device", "handle", "cur", "other")
+
+    def __init__(self, tensors, stream):
+        self.device = dev = tensors[0].device
+        for t in tensors:
+            if t.device != dev or not t.is_cuda:
+                raise ValueError("all tensors must be device tensors (no CPU path)"
+                                 if not t.is_cuda else "all tensors must be on one device")
+        self.handle = torch._C._cuda_getCurrentRawStream(dev.index)
+        self.other = None
+        if stream is not None and int(stream) != self.handle:
+            self.handle = int(stream)
+            self.cur = torch.cuda.current_stream(dev)
+            self.other = torch.cuda.ExternalStream(self.handle, device=dev)
             for t in tensors:
-                if t is not None:
-                    t.record_stream(self.other)
+                t.record_stream(self.other)
+
+    def like(self, t):
+        """A new contiguous tensor of t's shape and type."""
+        if self.other is None:
+            return torch.empty_like(t, memory_format=torch.contiguous_format)
+        return self.empty(t.shape, t.dtype)
 
     def empty(self, shape, dtype, result=True):
         if self.other is None:
@@ -91,257 +113,256 @@ class _Run:
             t.record_stream(self.cur)
         return t
 
-    def workspace(self, nbytes):
-        return self.empty((nbytes,), torch.uint8, result=False) if nbytes else None
+    def call(self, fn, args, ptrs, need):
+        """fn on the tensors' device.  `need` gives the workspace's size, asked
+        only when the call says that it wants one."""
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return self._call(fn, args, ptrs, need)
+        return self._call(fn, args, ptrs, need)
 
-    def on_device(self):
-        if torch.cuda.current_device() == self.device.index:
-            return contextlib.nullcontext()
-        return torch.cuda.device(self.device)
+    def _call(self, fn, args, ptrs, need):
+        rc = fn(args, *ptrs, None, 0, self.handle)
+        if rc == _E_WORKSPACE:
+            n = need()
+            ws = self.empty((n,), torch.uint8, result=False)
+            rc = fn(args, *ptrs, ws.data_ptr(), n, self.handle)
+        if rc:
+            _check(rc)
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+    return None if t is None else t.data_ptr()      # (no elements: NULL)
 
 
-def _check_type(tensors, names):
-    dt = tensors[0].dtype
-    if dt not in _DTYPES:
+def _dtype(names, first, *others):
+    dt = first.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
         raise TypeError(f"{names} must be float16 or bfloat16")
-    for t in tensors:
+    for t in others:
         if t.dtype != dt:
             raise TypeError(f"{names} must have one dtype")
-    return _DTYPES[dt]
+    return code
 
 
-def _check_device(tensors):
-    dev = tensors[0].device
-    for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("all tensors must be device tensors (no CPU path)")
-        if t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    return dev
-
-
-def _strides(t: torch.Tensor, name: str, dims: int):
-    """Element strides of all but the last dimension, which is contiguous; 0
+def _strides3(t: torch.Tensor, name: str):
+    """Token and head stride in elements; the last dimension is contiguous.  0
     for a dimension of one."""
-    if t.dim() != dims:
-        raise ValueError(f"{name} must be {dims}-D")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    n, h, d = t.shape
+    x, y, z = t.stride()
+    if z != 1 and d > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return [t.stride(i) if t.shape[i] > 1 else 0 for i in range(dims - 1)]
+    return x if n > 1 else 0, y if h > 1 else 0
+
+
+def _strides4(t: torch.Tensor, name: str):
+    """Batch, token and head stride, as _strides3."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be 4-D")
+    b, n, h, d = t.shape
+    w, x, y, z = t.stride()
+    if z != 1 and d > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return w if b > 1 else 0, x if n > 1 else 0, y if h > 1 else 0
 
 
 def _scale(scale, dim):
-    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
+    scale = 1.0 / math.sqrt(dim or 1) if scale is None else float(scale)
     if not (scale > 0.0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
     return scale
 
 
 def _offsets(seq_q, seq_k):
-    if seq_q is None and seq_k is None:
-        return 1
     if seq_q is None:
-        raise ValueError("seq_k without seq_q")
-    for t, n in ((seq_q, "seq_q"), (seq_k, "seq_k")):
+        if seq_k is not None:
+            raise ValueError("seq_k without seq_q")
+        return 1
+    for t, n in ((seq_q, "seq_q"),) if seq_k is seq_q else ((seq_q, "seq_q"), (seq_k, "seq_k")):
         if t.dtype != torch.int32:
             raise TypeError(f"{n} must be int32")
-        if t.dim() != 1 or t.shape[0] < 2 or (t.stride(0) != 1):
+        if t.dim() != 1 or t.shape[0] < 2 or t.stride(0) != 1:
             raise ValueError(f"{n} must hold sequences + 1 offsets, contiguous")
     if seq_q.shape != seq_k.shape:
         raise ValueError("seq_q and seq_k disagree on the number of sequences")
     return seq_q.shape[0] - 1
 
 
-def _packed_args(q, k, v, seq_q, seq_k, causal, scale, algo, splits):
-    a = AttentionArgs()
-    a.dtype = _check_type((q, k, v), "q, k and v")
-    a.q_token, a.q_head = _strides(q, "q", 3)
-    a.k_token, a.k_head = _strides(k, "k", 3)
-    a.v_token, a.v_head = _strides(v, "v", 3)
-    a.total_q, a.heads_q, a.head_dim = q.shape
-    a.total_k, a.heads_kv, dk = k.shape
-    if tuple(v.shape) != tuple(k.shape):
-        raise ValueError("k and v must have one shape")
-    if dk != a.head_dim:
-        raise ValueError("q and k disagree on the head dimension")
-    if a.heads_kv == 0 or a.heads_q == 0 or a.heads_q % a.heads_kv:
+def _heads(hq, hk):
+    if hk == 0 or hq == 0 or hq % hk:
         raise ValueError("the query heads must be a multiple of the key heads")
-    a.batch = _offsets(seq_q, seq_k)
-    a.causal = 1 if causal else 0
-    a.scale = _scale(scale, a.head_dim or 1)
-    a.algo = ATTENTION_ALGOS[algo]
-    a.splits = splits
-    return a
+
+
+def _packed_args(q, k, v, seq_q, seq_k, causal, scale, out_strides, algo, splits):
+    code = _dtype("q, k and v", q, k, v)
+    q0, q1 = _strides3(q, "q")
+    k0, k1 = _strides3(k, "k")
+    v0, v1 = _strides3(v, "v")
+    total_q, hq, d = q.shape
+    total_k, hk, dk = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    if dk != d:
+        raise ValueError("q and k disagree on the head dimension")
+    _heads(hq, hk)
+    return AttentionArgs(code, 1 if causal else 0, _offsets(seq_q, seq_k), total_q, total_k, hq,
+                         hk, d, q0, q1, k0, k1, v0, v1, out_strides[0], out_strides[1],
+                         _scale(scale, d), ATTENTION_ALGOS[algo], splits)
 
 
 def _like(t, ref, name):
     if t.dtype != ref.dtype:
         raise TypeError(f"{name} must have q's dtype")
-    if tuple(t.shape) != tuple(ref.shape):
+    if t.shape != ref.shape:
         raise ValueError(f"{name} must have shape {tuple(ref.shape)}")
 
 
-def _check_lse(lse, shape):
+def _fresh(shape):
+    """Strides of a new 3-D tensor, as _strides."""
+    return [shape[1] * shape[2] if shape[0] > 1 else 0, shape[2] if shape[1] > 1 else 0]
+
+
+# ------------------------------------------------------------------ functions
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
+              seq_q: Optional[torch.Tensor] = None, seq_k: Optional[torch.Tensor] = None,
+              causal: bool = True, scale: Optional[float] = None,
+              out: Optional[torch.Tensor] = None, return_lse: bool = False,
+              algo: str = "auto", splits: int = 0, stream=None):
+    """softmax(scale q k^T) v over packed sequences on the GPU.
+
+    q (tokens, heads, dim), k and v (tokens, kv heads, dim), float16 or
+    bfloat16, any 16-byte aligned token and head strides; heads is a multiple
+    of kv heads (grouped heads), dim a multiple of 8 up to 256.  seq_q, seq_k:
+    sequences + 1 int32 offsets on the device (one sequence without them;
+    seq_k defaults to seq_q).  causal: query token t of a sequence with lq
+    queries and lk keys sees the keys up to t + lk - lq.  scale defaults to
+    dim ** -0.5.  Returns out (tokens, heads, dim), with return_lse also the
+    log-sum-exp (tokens, heads) float32; a query without visible keys has out
+    0 and -inf.  Rows behind the last sequence are not written.  No autograd
+    graph is recorded: attention_backward gives the gradients.  algo and
+    splits choose the kernel and the parts its keys are split into."""
+    if seq_k is None:
+        seq_k = seq_q
+    if out is not None:
+        _like(out, q, "out")
+    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale,
+                     _strides3(out, "out") if out is not None else _fresh(q.shape), algo, splits)
+    run = _Run([t for t in (q, k, v, seq_q, seq_k, out) if t is not None], stream)
+    if out is None:
+        out = run.like(q)
+    lse = run.empty(q.shape[:2], torch.float32) if return_lse else None
+    ptrs = (_ptr(q), _ptr(k), _ptr(v), _ptr(seq_q), _ptr(seq_k), _ptr(out), _ptr(lse))
+
+    def need():
+        n = _i64(0)
+        _check(_lib.attention_packed_plan(a, *ptrs, None, None, n))
+        return n.value
+
+    run.call(_lib.attention_packed, a, ptrs, need)
+    return (out, lse) if return_lse else out
+
+
+def attention_plan(q, k, v, *, seq_q=None, seq_k=None, causal=True, scale=None, algo="auto",
+                   splits=0) -> Tuple[str, int, int]:
+    """(kernel, key splits, workspace bytes) attention() takes for these
+    tensors; their data is not read."""
+    if seq_k is None:
+        seq_k = seq_q
+    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, _fresh(q.shape), algo, splits)
+    al, sp, n = _i32(0), _i32(0), _i64(0)
+    _check(_lib.attention_packed_plan(a, _ptr(q), _ptr(k), _ptr(v), _ptr(seq_q), _ptr(seq_k),
+                                      1 << 40, None, al, sp, n))
+    return _NAMES[al.value], sp.value, n.value
+
+
+def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       out: torch.Tensor, lse: torch.Tensor, *,
+                       seq_q: Optional[torch.Tensor] = None,
+                       seq_k: Optional[torch.Tensor] = None, causal: bool = True,
+                       scale: Optional[float] = None, stream=None):
+    """(dq, dk, dv) of sum(out * dout) for attention()'s arguments and its out
+    and lse.  The gradients of a group's shared kv head are summed over its
+    query heads; tokens of no sequence have gradient 0.  The same arguments
+    give the same bits."""
+    if seq_k is None:
+        seq_k = seq_q
+    _like(dout, q, "dout")
+    _like(out, q, "out")
+    f = _packed_args(q, k, v, seq_q, seq_k, causal, scale, _strides3(out, "out"), "auto", 0)
     if lse.dtype != torch.float32:
         raise TypeError("lse must be float32")
-    if tuple(lse.shape) != tuple(shape) or not lse.is_contiguous():
-        raise ValueError(f"lse must be contiguous, of shape {tuple(shape)}")
+    if lse.shape != q.shape[:2] or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous, of shape {tuple(q.shape[:2])}")
+    g = AttentionGradArgs(f, *_strides3(dout, "dout"), *_fresh(q.shape), *_fresh(k.shape),
+                          *_fresh(v.shape))
+    run = _Run([t for t in (dout, q, k, v, out, lse, seq_q, seq_k) if t is not None], stream)
+    dq, dk, dv = run.like(q), run.like(k), run.like(v)
+    ptrs = tuple(_ptr(t) for t in (dout, q, k, v, out, lse, seq_q, seq_k, dq, dk, dv))
+
+    def need():
+        n = _i64(0)
+        _check(_lib.attention_packed_backward_plan(g, *ptrs, n))
+        return n.value
+
+    run.call(_lib.attention_packed_backward, g, ptrs, need)
+    return dq, dk, dv
 
 
-def bind(lib, check):
-    """The public functions over a loaded library."""
+def attention_prefix(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor,
+                     k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor, *,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     return_lse: bool = False, algo: str = "auto",
+                     splits: Tuple[int, int] = (0, 0), stream=None):
+    """Attention of a decoding batch whose sequences share a prefix.
 
-    def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
-                  seq_q: Optional[torch.Tensor] = None, seq_k: Optional[torch.Tensor] = None,
-                  causal: bool = True, scale: Optional[float] = None,
-                  out: Optional[torch.Tensor] = None, return_lse: bool = False,
-                  algo: str = "auto", splits: int = 0, stream=None):
-        """softmax(scale q k^T) v over packed sequences on the GPU.
-
-        q (tokens, heads, dim), k and v (tokens, kv heads, dim), float16 or
-        bfloat16, any 16-byte aligned token and head strides; heads is a
-        multiple of kv heads (grouped heads), dim a multiple of 8 up to 256.
-        seq_q, seq_k: sequences + 1 int32 offsets on the device (one sequence
-        without them; seq_k defaults to seq_q).  causal: query token t of a
-        sequence with lq queries and lk keys sees the keys up to t + lk - lq.
-        scale defaults to dim ** -0.5.  Returns out (tokens, heads, dim), with
-        return_lse also the log-sum-exp (tokens, heads) float32; a query
-        without visible keys has out 0 and -inf.  Rows behind the last
-        sequence are not written.  No autograd graph is recorded:
-        attention_backward gives the gradients."""
-        if seq_q is not None and seq_k is None:
-            seq_k = seq_q
-        a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, algo, splits)
-        if out is not None:
-            _like(out, q, "out")
-            a.out_token, a.out_head = _strides(out, "out", 3)
-        tensors = [t for t in (q, k, v, seq_q, seq_k, out) if t is not None]
-        run = _Run(_check_device(tensors), stream, tensors)
-        if out is None:
-            out = run.empty(q.shape, q.dtype)
-            a.out_token, a.out_head = _strides(out, "out", 3)
-        lse = run.empty(q.shape[:2], torch.float32) if return_lse else None
-        ptrs = [_ptr(t) for t in (q, k, v)] + \
-            [None if t is None else t.data_ptr() for t in (seq_q, seq_k)] + [_ptr(out), _ptr(lse)]
-        need = _i64(0)
-        check(lib.attention_packed_plan(a, *ptrs, None, None, need))
-        ws = run.workspace(need.value)
-        with run.on_device():
-            check(lib.attention_packed(a, *ptrs, _ptr(ws), need.value, run.handle))
-        return (out, lse) if return_lse else out
-
-    def attention_plan(q, k, v, *, seq_q=None, seq_k=None, causal=True, scale=None, algo="auto",
-                       splits=0) -> Tuple[str, int, int]:
-        """(kernel, key splits, workspace bytes) attention() takes for these
-        tensors; their data is not read."""
-        if seq_q is not None and seq_k is None:
-            seq_k = seq_q
-        a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, algo, splits)
-        a.out_token, a.out_head = a.heads_q * a.head_dim, a.head_dim
-        al, sp, need = _i32(0), _i32(0), _i64(0)
-        check(lib.attention_packed_plan(
-            a, *[_ptr(t) for t in (q, k, v)],
-            *[None if t is None else t.data_ptr() for t in (seq_q, seq_k)],
-            1 << 40, None, al, sp, need))
-        return _NAMES[al.value], sp.value, need.value
-
-    def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
-                           out: torch.Tensor, lse: torch.Tensor, *,
-                           seq_q: Optional[torch.Tensor] = None,
-                           seq_k: Optional[torch.Tensor] = None, causal: bool = True,
-                           scale: Optional[float] = None, stream=None):
-        """(dq, dk, dv) of sum(out * dout) for attention()'s arguments and
-        its out and lse.  The gradients of a group's shared kv head are summed
-        over its query heads; tokens of no sequence have gradient 0.  The same
-        arguments give the same bits."""
-        if seq_q is not None and seq_k is None:
-            seq_k = seq_q
-        g = AttentionGradArgs()
-        g.f = _packed_args(q, k, v, seq_q, seq_k, causal, scale, "auto", 0)
-        _like(dout, q, "dout")
+    q (batch, heads, dim) or (batch, new tokens, heads, dim); prefix_k,
+    prefix_v (prefix, kv heads, dim); k, v (batch, capacity, kv heads, dim):
+    each sequence's own cache, of which lengths[b] (int32, on the device) keys
+    are held, those of the new tokens last.  A new token sees the whole prefix
+    and its own sequence's keys up to itself.  The prefix is read once for the
+    whole batch.  Returns out of q's shape, with return_lse also the
+    log-sum-exp (float32, q's shape without dim).  algo and splits choose the
+    prefix's kernel and the parts the prefix and the caches are split into."""
+    code = _dtype("q, the prefix, k and v", q, prefix_k, prefix_v, k, v)
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be (batch, heads, dim) or (batch, tokens, heads, dim)")
+    x = q if q.dim() == 4 else q.unsqueeze(1)
+    batch, tokens, hq, d = x.shape
+    pks, pvs = _strides3(prefix_k, "prefix_k"), _strides3(prefix_v, "prefix_v")
+    ks, vs = _strides4(k, "k"), _strides4(v, "v")
+    prefix, hk, dim = prefix_k.shape
+    if prefix_v.shape != prefix_k.shape or v.shape != k.shape:
+        raise ValueError("keys and values must have one shape")
+    capacity = k.shape[1]
+    if dim != d or k.shape != (batch, capacity, hk, d):
+        raise ValueError("q, the prefix and the cache disagree on batch, heads or dim")
+    if batch == 0:
+        raise ValueError("the batch is empty")
+    _heads(hq, hk)
+    if lengths.dtype != torch.int32:
+        raise TypeError("lengths must be int32")
+    if lengths.shape != (batch,) or (batch > 1 and lengths.stride(0) != 1):
+        raise ValueError("lengths must hold one length per sequence, contiguous")
+    if out is not None:
         _like(out, q, "out")
-        _check_lse(lse, q.shape[:2])
-        g.f.out_token, g.f.out_head = _strides(out, "out", 3)
-        g.dout_token, g.dout_head = _strides(dout, "dout", 3)
-        tensors = [t for t in (dout, q, k, v, out, lse, seq_q, seq_k) if t is not None]
-        run = _Run(_check_device(tensors), stream, tensors)
-        dq, dk, dv = (run.empty(t.shape, t.dtype) for t in (q, k, v))
-        g.dq_token, g.dq_head = _strides(dq, "dq", 3)
-        g.dk_token, g.dk_head = _strides(dk, "dk", 3)
-        g.dv_token, g.dv_head = _strides(dv, "dv", 3)
-        ptrs = [_ptr(t) for t in (dout, q, k, v, out, lse)] + \
-            [None if t is None else t.data_ptr() for t in (seq_q, seq_k)] + \
-            [_ptr(t) for t in (dq, dk, dv)]
-        need = _i64(0)
-        check(lib.attention_packed_backward_plan(g, *ptrs, need))
-        ws = run.workspace(need.value)
-        with run.on_device():
-            check(lib.attention_packed_backward(g, *ptrs, _ptr(ws), need.value, run.handle))
-        return dq, dk, dv
+    run = _Run([t for t in (q, prefix_k, prefix_v, k, v, lengths, out) if t is not None], stream)
+    if out is None:
+        out = run.like(q)
+    os = _strides4(out if q.dim() == 4 else out.unsqueeze(1), "out")
+    a = AttentionPrefixArgs(code, ATTENTION_ALGOS[algo], batch, tokens, prefix, capacity, hq, hk,
+                            d, *_strides4(x, "q"), *pks, *pvs, *ks, *vs, *os, _scale(scale, d),
+                            *splits)
+    lse = run.empty(q.shape[:-1], torch.float32) if return_lse else None
+    ptrs = (_ptr(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(k), _ptr(v), _ptr(lengths), _ptr(out),
+            _ptr(lse))
 
-    def attention_prefix(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor,
-                         k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor, *,
-                         scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                         return_lse: bool = False, algo: str = "auto",
-                         splits: Tuple[int, int] = (0, 0), stream=None):
-        """Attention of a decoding batch whose sequences share a prefix.
+    def need():
+        n = _i64(0)
+        _check(_lib.attention_prefix_plan(a, *ptrs, None, None, None, n))
+        return n.value
 
-        q (batch, heads, dim) or (batch, new tokens, heads, dim); prefix_k,
-        prefix_v (prefix, kv heads, dim); k, v (batch, capacity, kv heads,
-        dim): each sequence's own cache, of which lengths[b] (int32, on the
-        device) keys are held, those of the new tokens last.  A new token sees
-        the whole prefix and its own sequence's keys up to itself.  The prefix
-        is read once for the whole batch.  Returns out of q's shape, with
-        return_lse also the log-sum-exp (float32, q's shape without dim)."""
-        a = AttentionPrefixArgs()
-        a.dtype = _check_type((q, prefix_k, prefix_v, k, v), "q, the prefix, k and v")
-        if q.dim() not in (3, 4):
-            raise ValueError("q must be (batch, heads, dim) or (batch, tokens, heads, dim)")
-        x = q if q.dim() == 4 else q.unsqueeze(1)
-        a.q_batch, a.q_token, a.q_head = _strides(x, "q", 4)
-        a.batch, a.q_tokens, a.heads_q, a.head_dim = x.shape
-        a.prefix_k_token, a.prefix_k_head = _strides(prefix_k, "prefix_k", 3)
-        a.prefix_v_token, a.prefix_v_head = _strides(prefix_v, "prefix_v", 3)
-        a.k_batch, a.k_token, a.k_head = _strides(k, "k", 4)
-        a.v_batch, a.v_token, a.v_head = _strides(v, "v", 4)
-        a.prefix, a.heads_kv, dim = prefix_k.shape
-        a.capacity = k.shape[1]
-        if prefix_v.shape != prefix_k.shape or v.shape != k.shape:
-            raise ValueError("keys and values must have one shape")
-        if dim != a.head_dim or k.shape[3] != dim or k.shape[2] != a.heads_kv or \
-                k.shape[0] != a.batch:
-            raise ValueError("q, the prefix and the cache disagree on batch, heads or dim")
-        if a.batch == 0:
-            raise ValueError("the batch is empty")
-        if a.heads_kv == 0 or a.heads_q == 0 or a.heads_q % a.heads_kv:
-            raise ValueError("the query heads must be a multiple of the key heads")
-        if lengths.dtype != torch.int32:
-            raise TypeError("lengths must be int32")
-        if tuple(lengths.shape) != (a.batch,) or (a.batch > 1 and lengths.stride(0) != 1):
-            raise ValueError("lengths must hold one length per sequence, contiguous")
-        a.scale = _scale(scale, a.head_dim or 1)
-        a.algo = ATTENTION_ALGOS[algo]
-        a.splits_prefix, a.splits_own = splits
-        if out is not None:
-            _like(out, q, "out")
-        tensors = [t for t in (q, prefix_k, prefix_v, k, v, lengths, out) if t is not None]
-        run = _Run(_check_device(tensors), stream, tensors)
-        if out is None:
-            out = run.empty(q.shape, q.dtype)
-        y = out if q.dim() == 4 else out.unsqueeze(1)
-        a.out_batch, a.out_token, a.out_head = _strides(y, "out", 4)
-        lse = run.empty(q.shape[:-1], torch.float32) if return_lse else None
-        ptrs = [_ptr(t) for t in (q, prefix_k, prefix_v, k, v)] + [lengths.data_ptr()] + \
-            [_ptr(out), _ptr(lse)]
-        need = _i64(0)
-        check(lib.attention_prefix_plan(a, *ptrs, None, None, None, need))
-        ws = run.workspace(need.value)
-        with run.on_device():
-            check(lib.attention_prefix(a, *ptrs, _ptr(ws), need.value, run.handle))
-        return (out, lse) if return_lse else out
-
-    return attention, attention_plan, attention_backward, attention_prefix
+    run.call(_lib.attention_prefix, a, ptrs, need)
+    return (out, lse) if return_lse else out
