@@ -58,13 +58,13 @@ extern "C" {
 #define MFL_BF16 3            /* mfl_dtype of these functions, beside MFL_F16 */
 #define MFL_E_WORKSPACE (-10) /* workspace NULL, misaligned or too small */
 
-/* Kernel of the forward functions: AUTO chooses by sizes.  TALL: 8 or 4
+/* Kernel of the forward functions: AUTO chooses by sizes.  TALL: four
  * waves of 32 rows (a row is a token of one query head) share each chunk of
- * keys; FLAT: 32 rows per workgroup, whose waves take turns over the keys. */
+ * keys; FLAT: 16 rows per workgroup, whose four waves take turns over the
+ * keys. */
 #define MFL_ATTENTION_AUTO 0
 #define MFL_ATTENTION_TALL 1
-#define MFL_ATTENTION_TALL_4 2
-#define MFL_ATTENTION_FLAT 3
+#define MFL_ATTENTION_FLAT 2
 
 typedef struct {
   int32_t dtype;                /* MFL_F16 or MFL_BF16 */
@@ -115,7 +115,7 @@ int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* do
  * new tokens' among them.  Prefix keys are read once for all sequences. */
 typedef struct {
   int32_t dtype;
-  int32_t algo;                 /* of the prefix's part; the own keys' is FLAT */
+  int32_t algo;                 /* of the prefix's part: AUTO, TALL or FLAT */
   int64_t batch, q_tokens;
   int64_t prefix, capacity;
   int64_t heads_q, heads_kv, head_dim;

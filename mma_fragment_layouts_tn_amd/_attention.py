@@ -13,7 +13,7 @@ from typing import Optional, Tuple
 import torch
 
 BF16 = 3
-ATTENTION_ALGOS = {"auto": 0, "tall": 1, "tall4": 2, "flat": 3}
+ATTENTION_ALGOS = {"auto": 0, "tall": 1, "flat": 2}
 _NAMES = {v: k for k, v in ATTENTION_ALGOS.items()}
 _DTYPES = {torch.float16: 1, torch.bfloat16: BF16}
 

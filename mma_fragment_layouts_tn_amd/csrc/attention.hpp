@@ -46,6 +46,9 @@ struct Elem<_Float16> {
   static __device__ __forceinline__ floatx16 mma(vec8 a, vec8 b, floatx16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
+  static __device__ __forceinline__ floatx4 mma16(vec8 a, vec8 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
   // The sum tied to accumulation registers (mma_tied) or to ordinary ones
   // (mma_begin from zero, mma_add): the compiler keeps the results of its own
   // matrix instructions all in the one kind or all in the other.  It does not
@@ -68,6 +71,9 @@ struct Elem<__bf16> {
   typedef __bf16 vec8 __attribute__((ext_vector_type(8)));
   static __device__ __forceinline__ floatx16 mma(vec8 a, vec8 b, floatx16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ floatx4 mma16(vec8 a, vec8 b, floatx4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
   // The sum tied to accumulation registers (mma_tied) or to ordinary ones
   // (mma_begin from zero, mma_add): the compiler keeps the results of its own
@@ -118,6 +124,7 @@ struct FwdParams {
   int q_inner;
   int heads_kv, group, dim, causal;
   int splits, split0, slots;  // key splits of this launch, index of the first
+  int part_keys;              // a tile takes a split per part_keys keys (0: all of them)
   int64_t rows;               // tokens * heads: the rows of one split
   int64_t q_batch, q_tok, q_head, k_batch, k_tok, k_head, v_batch, v_tok, v_head;
   int64_t o_batch, o_tok, o_head;
@@ -161,12 +168,13 @@ struct BwdParams {
 // ------------------------------------------------------------- LDS tiles
 // Rows of DC elements, 16-byte chunk c of row r stored at chunk c ^ swz(r).
 // Straight reads (one chunk of 16 consecutive rows) and transposing reads (4
-// consecutive chunks of 4 consecutive rows) both spread over the banks: swz
-// differs over 16 rows (DC = 64, two rows per pass of the banks: over 8 pairs
-// of rows), and over 4 rows (2 pairs) already in its upper bits.
+// consecutive chunks of 4 rows, or 2 chunks of 8 rows, consecutive ones) all
+// spread over the banks: swz differs over 16 rows (DC = 64, two rows per pass
+// of the banks: over 8 pairs of rows), over 4 rows already in its upper bits,
+// over 8 rows in all but the lowest.
 template <int DC>
 MFL_HD constexpr int swz_row(int r) {
-  return DC >= 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return (DC >= 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2) | ((r >> 2) & 1) << 1 | ((r >> 3) & 1);
 }
 template <int DC>
 MFL_HD constexpr int tile_off(int r, int d) {
@@ -192,10 +200,23 @@ constexpr bool swizzle_spreads() {
     }
     if (seen != 0xffffu) return false;
   }
+  for (int r0 = 0; r0 < 64; r0 += 8) {
+    unsigned seen = 0;
+    for (int i = 0; i < 16; ++i) {
+      const int r = r0 + i / 2;
+      seen |= 1u << (((r % per_pass) * row_groups + (((i % 2) ^ swz_row<DC>(r)) % row_groups)) & 15);
+    }
+    if (seen != 0xffffu) return false;
+  }
   return true;
 }
 static_assert(swizzle_spreads<64>() && swizzle_spreads<128>() && swizzle_spreads<256>(),
               "both kinds of LDS reads must touch every bank group once");
+
+template <bool B>
+struct BoolC {
+  static constexpr bool value = B;
+};
 
 template <class T>
 __device__ __forceinline__ Vec8<T> load8(const T* p) {
@@ -247,7 +268,7 @@ struct Reader {
   __device__ __forceinline__ Vec8<T> transposed(int kc, int db, int more = 0) const {
     const unsigned x = t ^ (64u * db);
     const shortx4 lo = read_tr(x + 32 * kc * DC + more);
-    const shortx4 hi = read_tr((x ^ 32u) + 32 * kc * DC + 16 * DC + more);
+    const shortx4 hi = read_tr((x ^ 16u) + 32 * kc * DC + 16 * DC + more);
     return __builtin_bit_cast(Vec8<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   __device__ __forceinline__ shortx4 read_tr(unsigned address) const {
@@ -271,7 +292,7 @@ constexpr bool reader_addresses_hold() {
       for (int db = 0; db < DC / 32; ++db) {
         const int x = tile_off<DC>(r, d) ^ (32 * db);
         if (tile_off<DC>(16 + r, 32 * db + d) != x + 16 * DC ||
-            tile_off<DC>(16 + r + 8, 32 * db + d) != (x ^ 16) + 24 * DC)
+            tile_off<DC>(16 + r + 8, 32 * db + d) != (x ^ 8) + 24 * DC)
           return false;
       }
   return true;
@@ -308,12 +329,27 @@ __device__ __forceinline__ Halves halves(float x) {
   const unsigned a = r[0], b = r[1];   // (a bit cast of r[i] itself reads element 0)
   return Halves{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
 }
+// the same over rows of 16 lanes: 0 and 1, 2 and 3
+__device__ __forceinline__ Halves quarters(float x) {
+  const unsigned u = __builtin_bit_cast(unsigned, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const unsigned a = r[0], b = r[1];
+  return Halves{__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)};
+}
 __device__ __forceinline__ float both_max(float x) {
   const Halves h = halves(x);
   return fmaxf(h.lower, h.upper);
 }
 __device__ __forceinline__ float both_sum(float x) {
   const Halves h = halves(x);
+  return h.lower + h.upper;
+}
+__device__ __forceinline__ float all4_max(float x) {   // lanes l, l ^ 16, l ^ 32, l ^ 48
+  const Halves h = quarters(both_max(x));
+  return fmaxf(h.lower, h.upper);
+}
+__device__ __forceinline__ float all4_sum(float x) {
+  const Halves h = quarters(both_sum(x));
   return h.lower + h.upper;
 }
 // x, but not for the optimiser: a first step told apart by it stays a branch
@@ -392,6 +428,20 @@ __device__ __forceinline__ Place place_of(const FwdParams& p, int slot, int bm) 
     r.v_off = (int64_t)s * p.v_batch;
   }
   return r;
+}
+
+// keys that the tile's last row sees; the splits they take; whether those go
+// to the workspace
+__device__ __forceinline__ int seen_of(const FwdParams& p, const Place& at, int bm) {
+  const int last = min((int)(((int64_t)at.tile * bm + bm - 1) / p.group), at.lq - 1);
+  return uniform(max(p.causal ? min(last + at.lk - at.lq, at.lk - 1) + 1 : at.lk, 0));
+}
+__device__ __forceinline__ int parts_of(const FwdParams& p, int seen) {
+  if (p.part_keys == 0) return p.splits;
+  return uniform(min(max((seen + p.part_keys - 1) / p.part_keys, 1), p.splits));
+}
+__device__ __forceinline__ bool to_parts(const FwdParams& p, int parts) {
+  return p.part_o && (p.part_keys == 0 || parts > 1);
 }
 
 // ------------------------------------------------ direct-to-LDS staging
@@ -574,37 +624,38 @@ __device__ __forceinline__ void mask_keys(floatx16 (&st)[NB], int key0, int limi
 }
 
 // ------------------------------------------------------ forward, tall
-// W waves of 32 rows each over chunks of 64 keys staged in a ring of NST LDS
-// stages (K and V of a chunk together), shared by the workgroup.
+// Four waves of 32 rows each over chunks of 64 keys staged in a ring of NST
+// LDS stages (K and V of a chunk together), shared by the workgroup: 64 KB, so
+// that two workgroups fit a CU up to 128 columns.
 template <int DC>
-MFL_HD constexpr int tall_stages(int waves) {
-  return DC == 256 ? 2 : waves == 8 ? 4 : DC == 64 ? 4 : 2;
+MFL_HD constexpr int tall_stages() {
+  return DC == 64 ? 4 : 2;
 }
 
-template <class T, int DC, int W>
-__global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
-  constexpr int BM = 32 * W, CK = 64, NST = tall_stages<DC>(W), KS = DC / 16, ND = DC / 32;
+template <class T, int DC>
+__device__ __forceinline__ void tall_rows(const FwdParams& p, T* smem, int bid) {
+  constexpr int W = 4, BM = 32 * W, CK = 64, NST = tall_stages<DC>(), KS = DC / 16, ND = DC / 32;
   constexpr int TILE = CK * DC, NI = CK * DC / 512 / W;   // elements, instructions per matrix and wave
-  static_assert(NI >= 1 && 4 * NST * TILE <= 160 * 1024, "staging");
-  __shared__ __attribute__((aligned(1024))) T smem[NST * 2 * TILE];
+  static_assert(NI >= 1, "loads");
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-  int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv;
   bid /= p.heads_kv;
-  const int split = bid % p.splits;
-  const int slot = p.slots - 1 - bid / p.splits;         // the longest rows first
+  // last splits first (only the longest tiles have them; between the others'
+  // workgroups the empty ones would leave shader engines idle), last rows
+  // first (with a causal mask the longest)
+  const int split = p.splits - 1 - bid / p.slots, slot = p.slots - 1 - bid % p.slots;
   const Place at = place_of(p, slot, BM);
   if (!at.any) return;
+  const int seen = seen_of(p, at, BM), parts = parts_of(p, seen);
+  if (split >= parts) return;
 
-  const int r0 = at.tile * BM + 32 * w;
-  const RowOf row = row_of(r0 + (lane & 31), at.lq, at.lk, p.group, kvh, at.q0, p.causal);
-  const int first_row_limit = uniform(row.limit);
-  // keys of this workgroup: to its last row's limit, its share of them
-  const int last_t = min((int)(((int64_t)at.tile * BM + BM - 1) / p.group), at.lq - 1);
-  const int seen = max(p.causal ? min(last_t + at.lk - at.lq, at.lk - 1) + 1 : at.lk, 0);
+  const RowOf row = row_of(at.tile * BM + 32 * w + (lane & 31), at.lq, at.lk, p.group, kvh, at.q0,
+                           p.causal);
   const int chunks = (seen + CK - 1) / CK;
-  const int c0 = (int)((int64_t)chunks * split / p.splits);
-  const int c1 = (int)((int64_t)chunks * (split + 1) / p.splits);
+  const int c0 = (int)((int64_t)chunks * split / parts);
+  const int c1 = (int)((int64_t)chunks * (split + 1) / parts);
+  // chunks before `cut` hide nothing from any of the wave's rows
+  const int cut = min(max((uniform(row.limit) + 1) / CK, c0), c1);
 
   const T* K = (const T*)p.k + at.k_off + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + at.v_off + (int64_t)kvh * p.v_head;
@@ -645,7 +696,7 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
   // chunk c, while chunk c + NST - 1 is fetched; `to` is the whole ring.
   // Every step issues 2 NI loads (of nothing past the last chunk), so what is
   // in flight is known by count.
-  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to) {
+  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to, auto masked) {
     if (c == hidden(c0)) {
 #pragma unroll
       for (int s = 0; s < NST - 1; ++s) {
@@ -677,7 +728,7 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
             pin_loads();
           }
       }
-    if (key0 + CK - 1 > first_row_limit) mask_keys(st, key0, row.limit, lane);
+    if constexpr (decltype(masked)::value) mask_keys(st, key0, row.limit, lane);
     softmax_step(st, acc, m, l, p.scale_log2);
 #pragma unroll
     for (int kc = 0; kc < 4; ++kc) {
@@ -695,13 +746,22 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
       }
     }
   };
-  for (int c = c0; c < c1; ++c) step(c, ring + stage_of(c), ring);
+  int c = c0;
+  if (c < cut) {
+    do step(c, ring + stage_of(c), ring, BoolC<false>{});
+    while (++c < cut);
+    settle();
+  }
+  if (c < c1) {
+    do step(c, ring + stage_of(c), ring, BoolC<true>{});
+    while (++c < c1);
+    settle();
+  }
   wait_vm<0>();
-  settle();
 
   l = both_sum(l);
   const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
-  if (p.part_o) {
+  if (to_parts(p, parts)) {
     const int64_t at_row = (int64_t)(p.split0 + split) * p.rows + out_row;
     if (row.valid && lane < 32) p.part_ml[at_row] = make_float2(m, l);
     if (row.valid && l != 0.0f) {
@@ -722,126 +782,173 @@ __global__ void __launch_bounds__(64 * W) attention_tall(const FwdParams p) {
     p.lse[out_row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
+template <class T, int DC>
+__global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_tall(const FwdParams p) {
+  static_assert(4 * tall_stages<DC>() * 64 * DC <= 160 * 1024, "staging");
+  __shared__ __attribute__((aligned(4096))) T smem[tall_stages<DC>() * 2 * 64 * DC];
+  tall_rows<T, DC>(p, smem, blockIdx.x);
+}
+
 // ------------------------------------------------------ forward, flat
-// Few rows, long keys: 32 rows per workgroup, whose W waves take turns over
-// chunks of 32 keys.  Each wave has its own ring of stages, so no wave waits
-// for another before the end, where the W partial rows are joined in LDS.
-template <int DC>
-MFL_HD constexpr int flat_waves() { return DC == 256 ? 2 : 4; }
-template <int DC>
-MFL_HD constexpr int flat_stages() { return DC == 64 ? 4 : 2; }
+// Few rows, long keys: 16 rows per workgroup (v_mfma 16x16x32: a decoding
+// step's rows, a group of heads times the new tokens, rarely fill more), whose
+// 4 waves take turns over chunks of 32 keys.  Each wave has a buffer of its
+// own for the K and the V of one chunk; the next K is fetched as soon as the
+// scores are formed, the next V after the second product, so a wave always has
+// half a chunk in flight, no wave waits for another before the end, and two
+// workgroups fit a CU (DC <= 128).  The W partial rows are joined in LDS.
+//
+// Lane l holds row l % 16; value v of the scores of keys 16 b .. 16 b + 15 is
+// key 16 b + 4 (l / 16) + v.  The second product's operand takes the values of
+// both 16-key blocks: per lane two runs of 4 keys, as two transposing reads
+// deliver V.
+constexpr int kFlatWaves = 4;
+template <class T, int DC>
+constexpr int flat_elems() {            // LDS: buffers, then (maximum, sum) per wave and row
+  return kFlatWaves * (2 * 32 * DC + 64);
+}
 
 template <class T, int DC>
-__global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const FwdParams p) {
-  constexpr int W = flat_waves<DC>(), NST = flat_stages<DC>(), CK = 32, KS = DC / 16,
-                ND = DC / 32, TILE = CK * DC, NI = TILE / 512, BM = 32;
-  static_assert(2 * (NST - 1) * NI < 64, "loads in flight");
-  constexpr int RING = NST * 2 * TILE;                   // elements per wave
-  // one object: with a second one the compiler's bookkeeping of direct-to-LDS
-  // loads makes every read wait for all of them
-  __shared__ __attribute__((aligned(1024))) T smem[W * RING + W * 32 * 4];
-  float2(*ml)[32] = (float2(*)[32])(smem + W * RING);
-  static_assert(2 * W * RING >= 4 * W * 32 * DC, "the partial rows fit in the rings");
+__device__ __forceinline__ void flat_rows(const FwdParams& p, T* smem, int bid) {
+  constexpr int W = kFlatWaves, BM = 16, CK = 32, KS = DC / 32, ND = DC / 16, TILE = CK * DC,
+                NI = TILE / 512;
+  float2(*ml)[16] = (float2(*)[16])(smem + W * 2 * TILE);
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
-  int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv;
   bid /= p.heads_kv;
-  const int split = bid % p.splits;
-  const int slot = p.slots - 1 - bid / p.splits;
+  const int split = p.splits - 1 - bid / p.slots, slot = p.slots - 1 - bid % p.slots;
   const Place at = place_of(p, slot, BM);
   if (!at.any) return;
+  const int seen = seen_of(p, at, BM), parts = parts_of(p, seen);
+  if (split >= parts) return;
 
-  const RowOf row = row_of(at.tile * BM + (lane & 31), at.lq, at.lk, p.group, kvh, at.q0, p.causal);
-  const int first_row_limit = uniform(row.limit);
-  const int seen = max(__builtin_amdgcn_readlane(row.limit, 31) + 1, 0);
+  const int r16 = lane & 15, quad = lane >> 4;
+  const RowOf row = row_of(at.tile * BM + r16, at.lq, at.lk, p.group, kvh, at.q0, p.causal);
   const int chunks = (seen + CK - 1) / CK;
-  const int c0 = (int)((int64_t)chunks * split / p.splits);
-  const int c1 = (int)((int64_t)chunks * (split + 1) / p.splits);
+  const int c0 = (int)((int64_t)chunks * split / parts);
+  const int c1 = (int)((int64_t)chunks * (split + 1) / parts);
   const T* K = (const T*)p.k + at.k_off + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + at.v_off + (int64_t)kvh * p.v_head;
-  const lds_c ring = (lds_c)smem + 2 * w * RING;
-  const int mine = max((c1 - c0 - w + W - 1) / W, 0);    // chunks c0 + w, + W, ...
-  auto issue = [&](int i, lds_c to) {
-    const int key0 = (c0 + w + i * W) * CK, end = i < mine ? at.lk : 0;
-    const Fetch<T, DC> k = Fetch<T, DC>::of(K, p.k_tok, key0, end, p.dim);
-    const Fetch<T, DC> v = Fetch<T, DC>::of(V, p.v_tok, key0, end, p.dim);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) k.issue(p.k_tok, p.dim, to, j, lane);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) v.issue(p.v_tok, p.dim, to + 2 * TILE, j, lane);
-  };
+  const lds_c mine = (lds_c)smem + w * 4 * TILE;
   const int64_t qn = (int64_t)(row.n / p.q_inner) * p.q_batch + (row.n % p.q_inner) * p.q_tok;
   const T* Q = (const T*)p.q + qn + row.head * p.q_head;
   Vec8<T> qf[KS];
 #pragma unroll
   for (int kk = 0; kk < KS; ++kk) {
-    const int d = 16 * kk + 8 * (lane >> 5);
+    const int d = 32 * kk + 8 * quad;
     if (d < p.dim)
       qf[kk] = load8(Q + d);
     else
 #pragma unroll
       for (int e = 0; e < 8; ++e) qf[kk][e] = (T)0.0f;
   }
-  floatx16 acc[ND];
-  zero(acc);
-  float m = -INFINITY, l = 0.0f;
-  const Reader<T, DC> reader = Reader<T, DC>::of(lane);
-  // chunk i of this wave, while chunk i + NST - 1 is fetched
-  auto step = [&](int i, lds_c __restrict__ from, lds_c __restrict__ to) {
-    if (i == hidden(0))
+  floatx4 acc[ND];
 #pragma unroll
-      for (int s = 0; s < NST - 1; ++s) issue(s, to + 4 * s * TILE);
-    // this wave's reads of the stage of chunk i - 1 are done: refill it
+  for (int j = 0; j < ND; ++j) acc[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;
+  // byte offsets of the lane's reads (see Reader)
+  const unsigned s0 = 2u * tile_off<DC>(r16, 8 * quad);
+  const unsigned t0 = 2u * tile_off<DC>(4 * quad + (r16 >> 2), 4 * (r16 & 3));
+  auto fetch = [&](const T* x, int64_t stride, int c, lds_c to) {
+    const Fetch<T, DC> f = Fetch<T, DC>::of(x, stride, c * CK, c < c1 ? at.lk : 0, p.dim);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) f.issue(stride, p.dim, to, j, lane);
+  };
+  auto reads_done = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    issue(i + NST - 1, to + (i + NST - 1) % NST * 4 * TILE);
-    wait_vm<(NST - 1) * 2 * NI>();   // chunk i has landed
     __builtin_amdgcn_sched_barrier(0);
-    const Reader<T, DC> rd = reader.at(from);
-    const int key0 = (c0 + w + i * W) * CK;
-    floatx16 st[1];
-    zero(st);
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) st[0] = Elem<T>::mma(rd.straight(0, kk), qf[kk], st[0]);
-    if (key0 + CK - 1 > first_row_limit) mask_keys(st, key0, row.limit, lane);
-    softmax_step(st, acc, m, l, p.scale_log2);
-#pragma unroll
-    for (int kc = 0; kc < 2; ++kc) {
-      const Vec8<T> pf = pack8<T>(st[0], kc);
-#pragma unroll
-      for (int db = 0; db < ND; ++db)
-        acc[db] = Elem<T>::mma(rd.transposed(kc, db, 2 * TILE), pf, acc[db]);
-    }
   };
-  for (int i = 0; i < mine; ++i) step(i, ring + i % NST * 4 * TILE, ring);
+  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to) {
+    if (c == hidden(c0 + w)) {
+      fetch(K, p.k_tok, c, to);
+      fetch(V, p.v_tok, c, to + 2 * TILE);
+    }
+    wait_vm<NI>();                       // K has landed, V may be in flight
+    unsigned s = s0 + (unsigned)(uintptr_t)from;
+    asm volatile("" : "+v"(s));
+    floatx4 st[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      st[b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        using ptr = const __attribute__((address_space(3))) Vec8<T>*;
+        st[b] = Elem<T>::mma16(*(ptr)((s ^ (64u * kk)) + 32 * b * DC), qf[kk], st[b]);
+      }
+    }
+    reads_done();
+    fetch(K, p.k_tok, c + W, to);
+    const int room = row.limit - c * CK - 4 * quad;
+    const unsigned visible = low_bits(room + 1);
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        st[b][e] = select_bit(visible, 16 * b + e, st[b][e], -INFINITY);
+        top = fmaxf(top, st[b][e]);
+      }
+    top = all4_max(top) * p.scale_log2;
+    if (__any(top - m > kSlack)) {
+      const float next = fmaxf(m, top);
+      const float f = __builtin_amdgcn_exp2f(m - (next == -INFINITY ? 0.0f : next));
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < ND; ++j) acc[j] *= f;
+      m = next;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    Vec8<T> pf;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(st[i / 4][i % 4], p.scale_log2, -ref));
+      l += v;
+      pf[i] = (T)v;
+    }
+    wait_vm<NI>();                       // V has landed, the next K may be in flight
+    unsigned t = t0 + (unsigned)(uintptr_t)from;
+    asm volatile("" : "+v"(t));
+    auto read_tr = [&](unsigned address) {
+      return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s4)(from + (int)(address - (unsigned)(uintptr_t)from)));
+    };
+#pragma unroll
+    for (int db = 0; db < ND; ++db) {
+      const unsigned x = (t ^ (32u * db)) + 2 * TILE;
+      const shortx4 lo = read_tr(x), hi = read_tr(x + 32 * DC);
+      acc[db] = Elem<T>::mma16(
+          __builtin_bit_cast(Vec8<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)), pf,
+          acc[db]);
+    }
+    reads_done();
+    fetch(V, p.v_tok, c + W, to + 2 * TILE);
+  };
+  int c = c0 + w;
+  if (c < c1) {
+    do step(c, mine, mine);
+    while ((c += W) < c1);
+    settle();
+  }
   wait_vm<0>();
-  settle();
   // join: every wave scales its rows to the common maximum and leaves them in
-  // LDS (16-byte group g of row r at g ^ (r & 15))
-  l = both_sum(l);
-  if (lane < 32) ml[w][lane] = make_float2(m, l);
+  // LDS (16-byte group g of row r at g ^ r)
+  l = all4_sum(l);
+  if (lane < 16) ml[w][lane] = make_float2(m, l);
   __syncthreads();
-  const int r = lane & 31;
   float top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < W; ++i) top = fmaxf(top, ml[i][r].x);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  const float f = __builtin_amdgcn_exp2f(m - ref);
-  float* rows = (float*)smem + w * 32 * DC;
+  for (int i = 0; i < W; ++i) top = fmaxf(top, ml[i][r16].x);
+  const float f = __builtin_amdgcn_exp2f(m - (top == -INFINITY ? 0.0f : top));
+  float* rows = (float*)smem + w * BM * DC;
 #pragma unroll
   for (int db = 0; db < ND; ++db)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int g = (8 * db + 2 * q + (lane >> 5)) ^ (r & 15);
-      *(floatx4*)(rows + r * DC + 4 * g) =
-          floatx4{acc[db][4 * q] * f, acc[db][4 * q + 1] * f, acc[db][4 * q + 2] * f,
-                  acc[db][4 * q + 3] * f};
-    }
+    *(floatx4*)(rows + r16 * DC + 4 * ((4 * db + quad) ^ r16)) = acc[db] * f;
   __syncthreads();
   // 4 elements of a row per thread and turn
   constexpr int GROUPS = DC / 4;
   const int heads = p.heads_kv * p.group;
-  for (int x = threadIdx.x; x < 32 * GROUPS; x += 64 * W) {
+  for (int x = threadIdx.x; x < BM * GROUPS; x += 64 * W) {
     const int rr = x / GROUPS, g = x % GROUPS;
     const RowOf o = row_of(at.tile * BM + rr, at.lq, at.lk, p.group, kvh, at.q0, p.causal);
     if (!o.valid) continue;
@@ -849,17 +956,17 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
 #pragma unroll
     for (int i = 0; i < W; ++i) mt = fmaxf(mt, ml[i][rr].x);
     const float mr = mt == -INFINITY ? 0.0f : mt;
-    floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    floatx4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       lt += ml[i][rr].y * __builtin_amdgcn_exp2f(ml[i][rr].x - mr);
-      s += *(const floatx4*)((const float*)smem + (i * 32 + rr) * DC + 4 * (g ^ (rr & 15)));
+      sum += *(const floatx4*)((const float*)smem + (i * BM + rr) * DC + 4 * (g ^ rr));
     }
     const int64_t out_row = (int64_t)o.n * heads + o.head;
-    if (p.part_o) {
+    if (to_parts(p, parts)) {
       const int64_t at_row = (int64_t)(p.split0 + split) * p.rows + out_row;
       if (g == 0) p.part_ml[at_row] = make_float2(mt, lt);
-      if (lt != 0.0f) *(floatx4*)(p.part_o + at_row * DC + 4 * g) = s;
+      if (lt != 0.0f) *(floatx4*)(p.part_o + at_row * DC + 4 * g) = sum;
       continue;
     }
     const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
@@ -868,7 +975,7 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
       const int64_t on = (int64_t)(o.n / p.q_inner) * p.o_batch + (o.n % p.q_inner) * p.o_tok;
       vec4 y;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = (T)(s[e] * inv);
+      for (int e = 0; e < 4; ++e) y[e] = (T)(sum[e] * inv);
       *(vec4*)((T*)p.o + on + o.head * p.o_head + 4 * g) = y;
     }
     if (p.lse && g == 0)
@@ -876,44 +983,122 @@ __global__ void __launch_bounds__(64 * flat_waves<DC>()) attention_flat(const Fw
   }
 }
 
-// ------------------------------------------------------ joining splits
-// One wave per row: the splits' weights from their maxima and sums, then
-// their accumulators in split order.
 template <class T, int DC>
-__global__ void __launch_bounds__(256) attention_join(const CombineParams p) {
+__global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2) attention_flat(const FwdParams p) {
+  __shared__ __attribute__((aligned(4096))) T smem[flat_elems<T, DC>()];
+  flat_rows<T, DC>(p, smem, blockIdx.x);
+}
+
+// Two problems in one launch, for decoding behind a prefix: the first `n0`
+// workgroups work on `a` (the prefix, tall or flat rows), the others on `b`
+// (the sequences' own keys, flat rows).  The prefix is bound by the matrix
+// pipe when many rows share it, the own keys by memory; side by side on a CU
+// each fills the other's waits.
+template <class T, int DC, bool TALL>
+__global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_pair(const FwdParams a, const FwdParams b, int n0) {
+  constexpr int E0 = TALL ? tall_stages<DC>() * 2 * 64 * DC : 0, E1 = flat_elems<T, DC>();
+  __shared__ __attribute__((aligned(4096))) T smem[E0 > E1 ? E0 : E1];
+  const int bid = blockIdx.x;
+  if (bid < n0) {
+    if constexpr (TALL)
+      tall_rows<T, DC>(a, smem, bid);
+    else
+      flat_rows<T, DC>(a, smem, bid);
+  } else {
+    flat_rows<T, DC>(b, smem, bid - n0);
+  }
+}
+
+// ------------------------------------------------------ joining splits
+// One wave: the weights of a row's splits from their maxima and sums (a split
+// per lane), then their accumulators in split order, 8 in flight.
+template <class T, int DC>
+__device__ __forceinline__ void join_row(const float* part_o, const float2* part_ml, int64_t rows,
+                                         int64_t row, int splits, int dim, T* out, float* lse) {
   const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= p.rows) return;
-  float top = -INFINITY;
-  for (int s = lane; s < p.splits; s += 64) top = fmaxf(top, p.part_ml[s * p.rows + row].x);
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  const float ref = top == -INFINITY ? 0.0f : top;
   constexpr int E = DC / 64;
   typedef float vecE __attribute__((ext_vector_type(E)));
+  // 64 splits at a time; what came before carries over as one more
+  float m = -INFINITY, l = 0.0f;
   vecE sum;
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = 0.0f;
-  float l = 0.0f;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = p.part_ml[s * p.rows + row];
-    if (ml.y == 0.0f) continue;        // no key of the split is visible
-    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-    l += ml.y * f;
-    const vecE v = *(const vecE*)(p.part_o + (s * p.rows + row) * DC + E * lane);
+  for (int s0 = 0; s0 < splits; s0 += 64) {
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (s0 + lane < splits) ml = part_ml[(s0 + lane) * rows + row];
+    float top = ml.x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] += v[e] * f;
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    top = fmaxf(top, m);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    // (a split without visible keys has weight 0, and nothing was written)
+    const float f = ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - ref);
+    const float old = __builtin_amdgcn_exp2f(m - ref);
+    float part = ml.y * f;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) part += __shfl_xor(part, d);
+    l = l * old + part;
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] *= old;
+    m = top;
+    const int n = min(splits - s0, 64);
+    for (int i = 0; i < n; i += 8) {
+      vecE v[8];
+      float g[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[j] = __shfl(f, i + j);
+        const int s = s0 + i + j;
+        if (i + j < n && g[j] != 0.0f) v[j] = *(const vecE*)(part_o + (s * rows + row) * DC + E * lane);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < n && g[j] != 0.0f)
+#pragma unroll
+          for (int e = 0; e < E; ++e) sum[e] += v[j][e] * g[j];
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int n = (int)(row / p.heads), head = (int)(row % p.heads);
-  T* o = (T*)p.o + (int64_t)(n / p.q_inner) * p.o_batch + (n % p.q_inner) * p.o_tok +
-         head * p.o_head;
-  if (E * lane < p.dim) {
+  if (E * lane < dim) {
+    typedef T outE __attribute__((ext_vector_type(E)));
+    outE y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[E * lane + e] = (T)(sum[e] * inv);
+    for (int e = 0; e < E; ++e) y[e] = (T)(sum[e] * inv);
+    *(outE*)(out + E * lane) = y;
   }
-  if (p.lse && lane == 0)
-    p.lse[row] = l == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(l)) * kLn2;
+  if (lse && lane == 0) *lse = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// every row, one wave each
+template <class T, int DC>
+__global__ void __launch_bounds__(256) attention_join(const CombineParams p) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+  if (row >= p.rows) return;
+  const int n = (int)(row / p.heads), head = (int)(row % p.heads);
+  join_row<T, DC>(p.part_o, p.part_ml, p.rows, row, p.splits, p.dim,
+                  (T*)p.o + (int64_t)(n / p.q_inner) * p.o_batch + (n % p.q_inner) * p.o_tok +
+                      head * p.o_head,
+                  p.lse ? p.lse + row : nullptr);
+}
+
+// the rows of the tiles that took more than one split, one wave each
+template <class T, int DC>
+__global__ void __launch_bounds__(256) attention_join_tiles(const FwdParams p, int bm) {
+  int bid = blockIdx.x;
+  const int kvh = bid % p.heads_kv;
+  bid /= p.heads_kv;
+  const int per = bm / 4;
+  const Place at = place_of(p, bid / per, bm);
+  if (!at.any) return;
+  const int parts = parts_of(p, seen_of(p, at, bm));
+  if (parts == 1) return;
+  const int r = at.tile * bm + 4 * (bid % per) + uniform(threadIdx.x >> 6);
+  const RowOf row = row_of(r, at.lq, at.lk, p.group, kvh, at.q0, p.causal);
+  if (!row.valid) return;
+  const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
+  join_row<T, DC>(p.part_o, p.part_ml, p.rows, out_row, parts, p.dim,
+                  (T*)p.o + row.n * p.o_tok + row.head * p.o_head,
+                  p.lse ? p.lse + out_row : nullptr);
 }
 
 }  // namespace att

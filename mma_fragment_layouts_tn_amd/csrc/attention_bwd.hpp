@@ -86,10 +86,11 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
   }
   const int r0 = at.tile * BM + 32 * w;
   const RowOf row = row_of(r0 + (lane & 31), at.lq, at.lk, p.group, kvh, at.q0, p.causal);
-  const int first_row_limit = uniform(row.limit);
   const int last_t = min((int)(((int64_t)at.tile * BM + BM - 1) / p.group), at.lq - 1);
   const int seen = max(p.causal ? min(last_t + at.lk - at.lq, at.lk - 1) + 1 : at.lk, 0);
   const int chunks = (seen + CK - 1) / CK;
+  // chunks before `cut` hide nothing from any of the wave's rows
+  const int cut = min(max((uniform(row.limit) + 1) / CK, 0), chunks);
   const T* K = (const T*)p.k + (int64_t)at.k0 * p.k_tok + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + (int64_t)at.k0 * p.v_tok + (int64_t)kvh * p.v_head;
   const lds_c ring = (lds_c)smem;
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
 
   const Reader<T, DC> reader = Reader<T, DC>::of(lane);
   // chunk c, while chunk c + NST - 1 is fetched; every step issues 2 NI loads
-  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to) {
+  auto step = [&](int c, lds_c __restrict__ from, lds_c __restrict__ to, auto masked) {
     if (c == hidden(0)) {
 #pragma unroll
       for (int s = 0; s < NST - 1; ++s) {
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
             pin_loads();
           }
       }
-      if (key0 + 31 > first_row_limit) mask_keys(st, key0, row.limit, lane);
+      if constexpr (decltype(masked)::value) mask_keys(st, key0, row.limit, lane);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float w_ = __builtin_amdgcn_exp2f(__builtin_fmaf(st[0][i], p.scale_log2, -lse2));
@@ -188,9 +189,18 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
       }
     }
   };
-  for (int c = 0; c < chunks; ++c) step(c, ring + c % NST * 4 * TILE, ring);
+  int c = 0;
+  if (c < cut) {
+    do step(c, ring + c % NST * 4 * TILE, ring, BoolC<false>{});
+    while (++c < cut);
+    settle();
+  }
+  if (c < chunks) {
+    do step(c, ring + c % NST * 4 * TILE, ring, BoolC<true>{});
+    while (++c < chunks);
+    settle();
+  }
   wait_vm<0>();
-  settle();
   store_row<T, DC>((T*)p.dq + row.n * p.dq_tok + row.head * p.dq_head, acc, p.scale, p.dim, lane,
                    row.valid);
 }
@@ -235,11 +245,6 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, const BwdPlace
   r.parts = min(max((r.steps + p.part_steps - 1) / p.part_steps, 1), p.max_parts);
   return r;
 }
-
-template <bool B>
-struct BoolC {
-  static constexpr bool value = B;
-};
 
 template <class T, int DC, int KW, int RW, int KB>
 __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p) {
@@ -384,10 +389,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   // takes is ready half a phase before, and the vector work is spread over
   // three of the four phases.  Fragments are read RA fragments ahead; the next
   // stage's loads are spread over the slots.
-#ifndef RAV
-#define RAV 2
-#endif
-  constexpr int RA = RAV, H = KS / 2;
+  constexpr int RA = 2, H = KS / 2;
   auto block = [&](const Reader<T, DC>& rd, const Reader<T, DC>& rv, const float* stat, int tb,
                    const Next& nx, lds_c to, int stage, auto masked) {
     floatx16 st[KB], dp[KB];

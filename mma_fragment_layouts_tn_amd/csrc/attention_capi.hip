@@ -9,12 +9,6 @@
 #include "attention.hpp"
 #include "attention_bwd.hpp"
 #include "attention_launch.hpp"
-#ifndef FDIV
-#define FDIV 1
-#endif
-#ifndef PMIN
-#define PMIN 8
-#endif
 
 namespace {
 
@@ -85,32 +79,57 @@ int64_t tile_slots(int64_t rows, int64_t batch, int64_t bm, bool packed) {
 
 struct Choice {
   int algo;
-  int64_t splits, slots;
+  int64_t splits, slots, part_keys;
 };
 
-// Workgroups that fill the chip once: 256 CUs, one of the large-LDS kernels
-// each.
+// Workgroups that occupy every CU.
 constexpr int64_t kFill = 256;
 
+// Kernel and parts of packed attention.  The host knows the sums of the
+// lengths, not each one (they are on the device), so the rules go by means.
+//
+// FLAT (16 rows, 4 waves share the keys) against TALL (128 rows, each wave
+// all keys), 32 query and 8 key heads of 128, bf16, causal: 1 token 4.5 and
+// 5.1 us, 16 tokens against 8192 keys 18 and 20, 128 tokens 5.5 and 7.3, 256
+// tokens 7.6 and 9.6, but 512 tokens 16.1 and 14.4 and 2048 tokens 102 and 49.
+// So FLAT where a sequence has up to 64 rows, or where its workgroups are at
+// most two per CU and the keys are few (64 tokens against 8192 keys: 35 and
+// 30, both split).
+//
+// Parts: where the tiles leave CUs idle, a tile's keys are shared out to
+// workgroups, as many as make two per CU with the mean of the keys, if that
+// saves more than it costs: a workgroup takes 18 ns per key (TALL, 128
+// columns) or 6.4 ns (FLAT); partial rows are written and read at 4 TB/s, and
+// the launch that joins them takes 4 us.  64 tokens against 8192 keys: 150 us
+// in one part, 30 in 16; 1024 against 1024: 25 and 43 in two.
 Choice choose(int64_t rows, int64_t batch, bool packed, int64_t keys, int64_t heads_kv, int dc,
               int algo, int64_t splits) {
   Choice c;
-  const int64_t mean_rows = ceil_div(rows, batch);
+  const int64_t mean_rows = ceil_div(rows, batch), mean_keys = ceil_div(keys, batch);
   if (algo == MFL_ATTENTION_AUTO) {
-    if (mean_rows <= 32)
-      algo = MFL_ATTENTION_FLAT;
-    else if (dc == 256 || mean_rows <= 128 ||
-             tile_slots(rows, batch, 256, packed) * heads_kv < kFill)
-      algo = MFL_ATTENTION_TALL_4;
-    else
-      algo = MFL_ATTENTION_TALL;
+    const bool few = ceil_div(rows, 16) * heads_kv <= 2 * kFill && mean_keys <= 2048;
+    algo = mean_rows <= 64 || few ? MFL_ATTENTION_FLAT : MFL_ATTENTION_TALL;
   }
   c.algo = algo;
   c.slots = tile_slots(rows, batch, tile_rows(algo), packed);
-  const int64_t units = ceil_div(ceil_div(keys, batch), algo == MFL_ATTENTION_FLAT ? 256 : 128);
-  if (splits == 0)
-    splits = clamp(kFill / (c.slots * heads_kv > 0 ? c.slots * heads_kv : 1), 1, clamp(units, 1, 64));
   c.splits = splits;
+  c.part_keys = 0;
+  if (splits == 0) {
+    c.splits = 1;
+    const int64_t tiles = ceil_div(rows, tile_rows(algo)),
+                  wgs = (tiles > batch ? tiles : batch) * heads_kv,
+                  least = algo == MFL_ATTENTION_FLAT ? 256 : 512;
+    if (wgs > 0 && wgs <= kFill) {
+      const int64_t fair = ceil_div(mean_keys, 2 * kFill / wgs),
+                    part = clamp(ceil_div(fair, 64) * 64, least, INT_MAX / 2),
+                    saved = (mean_keys - part) * (algo == MFL_ATTENTION_FLAT ? 64 : 180) * dc / 1280,
+                    bytes = ceil_div(mean_keys, part) * rows * heads_kv * dc * 8;
+      if (saved > 4000 + bytes / 4000) {
+        c.part_keys = part;
+        c.splits = clamp(ceil_div(keys, part), 1, 64);
+      }
+    }
+  }
   return c;
 }
 
@@ -122,18 +141,26 @@ bool grid_fits(const Choice& c, int64_t heads_kv) {
   return (__int128)c.slots * heads_kv * c.splits < INT_MAX;
 }
 
-int run(KernelRef k, int64_t blocks, void* params, void* stream, int a = 0, int b = 0) {
-  if (!k.fn) return MFL_E_UNSUPPORTED;
+int launch(KernelRef k, int64_t blocks, void** args, void* stream) {
   if (blocks == 0) return MFL_OK;
-  void* args[] = {params, &a, &b};   // (a kernel takes as many as it has)
   const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
                                        (hipStream_t)stream);
   return e == hipSuccess ? MFL_OK : MFL_E_LAUNCH;
 }
 
-int run_forward(FwdParams& p, const Choice& c, bool bf16, int dc, void* stream) {
+int run(KernelRef k, int64_t blocks, void* params, void* stream, int a = 0, int b = 0) {
+  void* args[] = {params, &a, &b};   // (a kernel takes as many as it has)
+  return launch(k, blocks, args, stream);
+}
+
+void place_choice(FwdParams& p, const Choice& c) {
   p.splits = (int)c.splits;
   p.slots = (int)c.slots;
+  p.part_keys = (int)c.part_keys;
+}
+
+int run_forward(FwdParams& p, const Choice& c, bool bf16, int dc, void* stream) {
+  place_choice(p, c);
   return run(fwd_kernel(bf16, dc, c.algo), c.slots * p.heads_kv * c.splits, &p, stream);
 }
 
@@ -151,7 +178,7 @@ int run_join(const FwdParams& p, int splits, bool bf16, int dc, void* stream) {
   j.o_batch = p.o_batch;
   j.o_tok = p.o_tok;
   j.o_head = p.o_head;
-  return run(join_kernel(bf16, dc), ceil_div(p.rows, 4), &j, stream);
+  return run(other_kernel(bf16, dc, kJoin), ceil_div(p.rows, 4), &j, stream);
 }
 
 int check_packed(const mfl_attention_t& a, const void* q, const void* k, const void* v,
@@ -181,7 +208,6 @@ int check_packed(const mfl_attention_t& a, const void* q, const void* k, const v
 
 int plan_packed(const mfl_attention_t& a, bool packed, Choice& c, int64_t& bytes) {
   const int dc = dim_class(a.head_dim);
-  if (dc == 256 && a.algo == MFL_ATTENTION_TALL) return MFL_E_ALGO_CASE;
   c = choose(a.total_q * (a.heads_q / a.heads_kv), a.batch, packed, a.total_k, a.heads_kv, dc,
              a.algo, a.splits);
   if (!grid_fits(c, a.heads_kv)) return MFL_E_TOO_LARGE;
@@ -220,8 +246,8 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   const int64_t tiles = ceil_div(f.total_k, dkv_keys(dc)) * f.heads_kv;
   if (tiles > 0 && tiles < 4 * kFill) {
     const int64_t steps = group * ceil_div(ceil_div(f.total_q, f.batch), dkv_chunk(dc));
-    const int64_t fair = tiles * steps / (f.causal ? 2 : 1) / kFill / FDIV;
-    r.part_steps = (int)clamp(fair, PMIN, INT_MAX / 2);
+    const int64_t fair = tiles * steps / (f.causal ? 2 : 1) / kFill;
+    r.part_steps = (int)clamp(fair, 8, INT_MAX / 2);
     r.max_parts = (int)clamp(ceil_div(2 * steps, r.part_steps), 1, 8);
   }
   r.bytes = r.stats_bytes;
@@ -309,18 +335,25 @@ struct PrefixPlan {
 
 int plan_prefix(const mfl_attention_prefix_t& a, PrefixPlan& r) {
   const int dc = dim_class(a.head_dim);
-  if (dc == 256 && a.algo == MFL_ATTENTION_TALL) return MFL_E_ALGO_CASE;
   const int64_t group = a.heads_q / a.heads_kv, rows = a.batch * a.q_tokens * group;
-  r.prefix = choose(rows, 1, false, a.prefix, a.heads_kv, dc, a.algo, a.splits_prefix);
-  if (a.prefix == 0) r.prefix.splits = 0;
-  // tiles of one sequence's rows
+  r.prefix.algo = a.algo ? a.algo : rows <= 64 ? MFL_ATTENTION_FLAT : MFL_ATTENTION_TALL;
   r.own.algo = MFL_ATTENTION_FLAT;
+  r.prefix.slots = ceil_div(rows, tile_rows(r.prefix.algo));
   r.own.slots = a.batch * ceil_div(a.q_tokens * group, tile_rows(MFL_ATTENTION_FLAT));
-  const int64_t wgs = r.own.slots * a.heads_kv;
-  r.own.splits = a.splits_own ? a.splits_own
-                              : clamp(wgs ? kFill / wgs : 1, 1, clamp(a.capacity / 256, 1, 64));
+  r.prefix.part_keys = r.own.part_keys = 0;
+  // each part gets a workgroup per CU
+  auto parts = [&](int64_t slots, int64_t keys, int64_t least) {
+    const int64_t wgs = slots * a.heads_kv;
+    return clamp(wgs > 0 ? kFill / wgs : 1, 1, clamp(keys / least, 1, 64));
+  };
+  r.prefix.splits = a.splits_prefix ? a.splits_prefix : parts(r.prefix.slots, a.prefix, 128);
+  r.own.splits = a.splits_own ? a.splits_own : parts(r.own.slots, a.capacity, 256);
+  if (a.prefix == 0) r.prefix.splits = 0;
   if (a.capacity == 0) r.own.splits = a.prefix == 0 ? 1 : 0;
-  if (!grid_fits(r.prefix, a.heads_kv) || !grid_fits(r.own, a.heads_kv)) return MFL_E_TOO_LARGE;
+  if (!grid_fits(r.prefix, a.heads_kv) || !grid_fits(r.own, a.heads_kv) ||
+      (__int128)(r.prefix.slots * r.prefix.splits + r.own.slots * r.own.splits) * a.heads_kv >=
+          INT_MAX)
+    return MFL_E_TOO_LARGE;
   r.bytes = partial_bytes(a.batch * a.q_tokens * a.heads_q, r.prefix.splits + r.own.splits, dc);
   return MFL_OK;
 }
@@ -391,7 +424,9 @@ int attention_packed(const mfl_attention_t* a, const void* q, const void* k, con
   if (c.splits > 1) place_partials(p, workspace, c.splits, dc);
   rc = run_forward(p, c, bf16, dc, stream);
   if (rc || c.splits == 1) return rc;
-  return run_join(p, (int)c.splits, bf16, dc, stream);
+  if (c.part_keys == 0) return run_join(p, (int)c.splits, bf16, dc, stream);
+  const int bm = tile_rows(c.algo);
+  return run(other_kernel(bf16, dc, kJoinTiles), c.slots * (bm / 4) * p.heads_kv, &p, stream, bm);
 }
 
 int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* dout,
@@ -526,39 +561,47 @@ int attention_prefix(const mfl_attention_prefix_t* a, const void* q, const void*
   p.o_head = a->out_head;
   p.scale_log2 = a->scale * kLog2e;
   if (splits > 1) place_partials(p, workspace, splits, dc);
-  if (r.prefix.splits > 0) {     // one sequence of all rows against the prefix
-    FwdParams s = p;
-    s.k = prefix_k;
-    s.v = prefix_v;
-    s.batch = 1;
-    s.q_len = p.total_q;
-    s.total_k = (int)a->prefix;
-    s.k_tok = a->prefix_k_token;
-    s.k_head = a->prefix_k_head;
-    s.v_tok = a->prefix_v_token;
-    s.v_head = a->prefix_v_head;
-    rc = run_forward(s, r.prefix, bf16, dc, stream);
-    if (rc) return rc;
+  FwdParams x = p;               // one sequence of all rows against the prefix
+  x.k = prefix_k;
+  x.v = prefix_v;
+  x.batch = 1;
+  x.q_len = p.total_q;
+  x.total_k = (int)a->prefix;
+  x.k_tok = a->prefix_k_token;
+  x.k_head = a->prefix_k_head;
+  x.v_tok = a->prefix_v_token;
+  x.v_head = a->prefix_v_head;
+  FwdParams y = p;               // each sequence's rows against its own keys
+  y.k = k;
+  y.v = v;
+  y.lengths = lengths;
+  y.batch = (int)a->batch;
+  y.q_len = (int)a->q_tokens;
+  y.total_k = (int)a->capacity;
+  y.causal = 1;
+  y.k_batch = a->k_batch;
+  y.k_tok = a->k_token;
+  y.k_head = a->k_head;
+  y.v_batch = a->v_batch;
+  y.v_tok = a->v_token;
+  y.v_head = a->v_head;
+  y.split0 = (int)r.prefix.splits;
+  place_choice(x, r.prefix);
+  place_choice(y, r.own);
+  const int64_t nx = r.prefix.slots * r.prefix.splits * p.heads_kv,
+                ny = r.own.slots * r.own.splits * p.heads_kv;
+  if (nx == 0) {
+    rc = run(fwd_kernel(bf16, dc, MFL_ATTENTION_FLAT), ny, &y, stream);
+  } else if (ny == 0) {
+    rc = run(fwd_kernel(bf16, dc, r.prefix.algo), nx, &x, stream);
+  } else {
+    const KernelRef f = other_kernel(
+        bf16, dc, r.prefix.algo == MFL_ATTENTION_FLAT ? kPairFlat : kPairTall);
+    int n0 = (int)nx;
+    void* args[] = {&x, &y, &n0};
+    rc = launch(f, nx + ny, args, stream);
   }
-  if (r.own.splits > 0) {        // each sequence's rows against its own keys
-    FwdParams s = p;
-    s.k = k;
-    s.v = v;
-    s.lengths = lengths;
-    s.batch = (int)a->batch;
-    s.q_len = (int)a->q_tokens;
-    s.total_k = (int)a->capacity;
-    s.causal = 1;
-    s.k_batch = a->k_batch;
-    s.k_tok = a->k_token;
-    s.k_head = a->k_head;
-    s.v_batch = a->v_batch;
-    s.v_tok = a->v_token;
-    s.v_head = a->v_head;
-    s.split0 = (int)r.prefix.splits;
-    rc = run_forward(s, r.own, bf16, dc, stream);
-    if (rc) return rc;
-  }
+  if (rc) return rc;
   return splits > 1 ? run_join(p, splits, bf16, dc, stream) : MFL_OK;
 }
 

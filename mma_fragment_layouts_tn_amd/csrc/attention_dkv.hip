@@ -9,12 +9,6 @@
 namespace mfl {
 namespace att {
 namespace {
-#ifndef V64
-#define V64 2,2,2
-#endif
-#ifndef V128
-#define V128 4,1,2
-#endif
 template <class T, int DC, int KW, int RW, int KB>
 KernelRef dkv_ref() {
   static_assert(dkv_keys(DC) == 32 * KW * KB && dkv_chunk(DC) == 32 * RW, "tile");
@@ -22,8 +16,8 @@ KernelRef dkv_ref() {
 }
 template <class T>
 KernelRef dkv(int dc) {
-  return dc == 64    ? dkv_ref<T, 64, V64>()
-         : dc == 128 ? dkv_ref<T, 128, V128>()
+  return dc == 64    ? dkv_ref<T, 64, 2, 2, 2>()
+         : dc == 128 ? dkv_ref<T, 128, 4, 1, 2>()
                      : dkv_ref<T, 256, 4, 1, 1>();
 }
 }  // namespace
