@@ -159,9 +159,9 @@ struct BwdParams {
   int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head, do_tok, do_head;
   int64_t dq_tok, dq_head, dk_tok, dk_head, dv_tok, dv_head;
   float scale, scale_log2;
-  // dK, dV: a tile's steps go to one workgroup per part_steps of them, at
-  // most max_parts; the parts' sums are dK then dV of part 0, 1, ...
-  int part_steps, max_parts;
+  // dK, dV: workgroups per kv head, 0: one per tile; sums of the tiles cut,
+  // two places per share and kv head, dK then dV of the keys of a tile
+  int shares;
   float* partials;
 };
 

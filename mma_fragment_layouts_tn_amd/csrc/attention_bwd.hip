@@ -8,14 +8,12 @@
 namespace mfl {
 namespace att {
 namespace {
-static_assert(dq_rows(64) == 32 * dq_waves<64>() && dq_rows(128) == 32 * dq_waves<128>() &&
-                  dq_rows(256) == 32 * dq_waves<256>(),
-              "rows per workgroup");
 template <class T>
 KernelRef dq(int dc) {
-  return dc == 64    ? KernelRef{(const void*)attention_dq<T, 64>, 64 * dq_waves<64>()}
-         : dc == 128 ? KernelRef{(const void*)attention_dq<T, 128>, 64 * dq_waves<128>()}
-                     : KernelRef{(const void*)attention_dq<T, 256>, 64 * dq_waves<256>()};
+  return {dc == 64    ? (const void*)attention_dq<T, 64>
+          : dc == 128 ? (const void*)attention_dq<T, 128>
+                      : (const void*)attention_dq<T, 256>,
+          256};
 }
 template <class T>
 KernelRef join(int dc) {

@@ -11,6 +11,7 @@
 #pragma once
 
 #include "attention.hpp"
+#include "attention_launch.hpp"
 
 namespace mfl {
 namespace att {
@@ -60,15 +61,11 @@ __device__ __forceinline__ void zero_rows(T* base, int64_t tok, int64_t head, in
 }
 
 // ------------------------------------------------------------------- dQ
-template <int DC>
-MFL_HD constexpr int dq_waves() { return DC == 256 ? 4 : 8; }
-template <int DC>
-MFL_HD constexpr int dq_stages() { return DC == 256 ? 2 : 4; }
-
 template <class T, int DC>
-__global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdParams p) {
-  constexpr int W = dq_waves<DC>(), NST = dq_stages<DC>(), BM = 32 * W, CK = 64, KS = DC / 16,
-                ND = DC / 32, TILE = CK * DC, NI = TILE / 512 / W;
+__global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const BwdParams p) {
+  constexpr int W = 4, NST = tall_stages<DC>(), BM = 32 * W, CK = 64, KS = DC / 16, ND = DC / 32,
+                TILE = CK * DC, NI = TILE / 512 / W, RA = 2;
+  static_assert(BM == kDqRows, "rows per workgroup");
   __shared__ __attribute__((aligned(1024))) T smem[NST * 2 * TILE];
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int kvh = blockIdx.x % p.heads_kv, heads = p.heads_kv * p.group;
@@ -155,39 +152,83 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
     const Next nx = next_chunk(c + NST - 1);
     const lds_c fill = to + (c + NST - 1) % NST * 4 * TILE;
     const Reader<T, DC> rd = reader.at(from);
+    // Six products of KS slots of one matrix instruction each, pinned in this
+    // order: S and dP of keys 0 - 31, S and dP of keys 32 - 63, dQ of both.
+    // The weights of the first block are formed under the second's S, its
+    // score gradients under the second's dP, the second's under the first's
+    // dQ.  Fragments are read RA slots ahead (left to itself the compiler
+    // reads each just before its use), the next chunk's loads are spread out.
+    floatx16 st[2][1], dp[2][1];
+    Vec8<T> fr[RA + 1], df[2][2];
+    unsigned seen_keys[2];
+    auto read = [&](int n) {
+      if (n >= 6 * KS) return;
+      const int ph = n / KS, kk = n % KS;
+      Vec8<T>& f = fr[n % (RA + 1)];
+      if (ph < 4)
+        f = rd.straight(ph / 2, kk, ph % 2 ? 2 * TILE : 0);
+      else
+        f = rd.transposed(2 * (ph - 4) + kk / ND, kk % ND);
+    };
+    // unit u of 32: value u % 16; 0 - 15 weights, 16 - 31 score gradients
+    auto work = [&](int b, int u) {
+      const int i = u % 16;
+      if (u < 16) {
+        float x = __builtin_amdgcn_exp2f(__builtin_fmaf(st[b][0][i], p.scale_log2, -lse2));
+        if constexpr (decltype(masked)::value)
+          x = select_bit(seen_keys[b], 8 * (i / 4) + i % 4, x, 0.0f);
+        st[b][0][i] = x;
+      } else {
+        dp[b][0][i] = st[b][0][i] * (dp[b][0][i] - delta);
+        if (i % 8 == 7) df[b][i / 8] = pack8<T>(dp[b][0], i / 8);
+      }
+    };
+    auto fill_slot = [&](int n) {
+      const int ph = n / KS, m = n % KS;
+      // units of a phase: 16 (phases 2, 3) or 32 (4) over KS slots
+      const int each = ph == 4 ? 32 : 16;
+      if (ph >= 2 && ph <= 4)
+#pragma unroll
+        for (int u = each * m / KS; u < each * (m + 1) / KS; ++u)
+          work(ph == 4 ? 1 : 0, ph == 3 ? 16 + u : u);
+#pragma unroll
+      for (int j = 0; j < 2 * NI; ++j)
+        if ((2 * j + 1) * 6 * KS / (4 * NI) == n) issue(nx, fill, j);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    if constexpr (decltype(masked)::value)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) seen_keys[b] = low_bits(row.limit + 1 - c * CK - 32 * b - 4 * (lane >> 5));
+#pragma unroll
+    for (int n = 0; n < RA; ++n) read(n);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int key0 = c * CK + 32 * b;
-      floatx16 st[1], dp[1];
-      zero(st);
-      zero(dp);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) st[0] = Elem<T>::mma(rd.straight(b, kk), qf[kk], st[0]);
+      zero(st[b]);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
-        dp[0] = Elem<T>::mma(rd.straight(b, kk, 2 * TILE), gf[kk], dp[0]);
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          if ((2 * j + 1) * KS / (2 * NI) == kk) {
-            pin_loads();
-            issue(nx, fill, b * NI + j);
-            pin_loads();
-          }
+        const int n = 2 * b * KS + kk;
+        read(n + RA);
+        st[b][0] = Elem<T>::mma(fr[n % (RA + 1)], qf[kk], st[b][0]);
+        fill_slot(n);
       }
-      if constexpr (decltype(masked)::value) mask_keys(st, key0, row.limit, lane);
+      zero(dp[b]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w_ = __builtin_amdgcn_exp2f(__builtin_fmaf(st[0][i], p.scale_log2, -lse2));
-        st[0][i] = w_ * (dp[0][i] - delta);
-      }
-#pragma unroll
-      for (int kc = 0; kc < 2; ++kc) {
-        const Vec8<T> df = pack8<T>(st[0], kc);
-#pragma unroll
-        for (int db = 0; db < ND; ++db)
-          acc[db] = Elem<T>::mma(rd.transposed(2 * b + kc, db), df, acc[db]);
+      for (int kk = 0; kk < KS; ++kk) {
+        const int n = (2 * b + 1) * KS + kk;
+        read(n + RA);
+        dp[b][0] = Elem<T>::mma(fr[n % (RA + 1)], gf[kk], dp[b][0]);
+        fill_slot(n);
       }
     }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        const int n = (4 + b) * KS + kk;
+        read(n + RA);
+        acc[kk % ND] = Elem<T>::mma(fr[n % (RA + 1)], df[b][kk / ND], acc[kk % ND]);
+        fill_slot(n);
+      }
   };
   int c = 0;
   if (c < cut) {
@@ -219,21 +260,18 @@ __global__ void __launch_bounds__(64 * dq_waves<DC>()) attention_dq(const BwdPar
 // reads, waits and scalar instructions per matrix instruction, and those, not
 // the matrix pipe, set their pace: 4,600 cycles for 2,048 of matrix work.
 //
-// A tile's steps (chunks of all heads) are shared out over as many workgroups
-// as dkv_steps() says, in order; with more than one, their sums go to the
-// workspace and attention_dkv_join adds them in order.  The chunks that the
-// causal mask cuts come first, in a loop of their own: the mask as a branch
-// inside one loop made the compiler spill accumulators.
+// The chunks that the causal mask cuts come first, in a loop of their own: the
+// mask as a branch inside one loop made the compiler spill accumulators.
 struct DkvSteps {
   int first, cut, last;     // chunks: first that sees the tile, first without
                             // hidden keys, last of the sequence
-  int steps, parts;
+  int steps;                // over the heads of the group
 };
-__device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, const BwdPlace& at, int bn,
+__device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, int lq, int lk, int tile, int bn,
                                               int rc) {
   DkvSteps r;
-  const int off = at.lk - at.lq, j0 = at.tile * bn;
-  r.last = (at.lq + rc - 1) / rc - 1;
+  const int off = lk - lq, j0 = tile * bn;
+  r.last = (lq + rc - 1) / rc - 1;
   r.first = r.cut = 0;
   if (p.causal) {           // token t sees the keys up to t + off
     r.first = max(j0 - off, 0) / rc;
@@ -242,47 +280,109 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, const BwdPlace
     r.cut = min(r.cut, r.last + 1);
   }
   r.steps = (r.last + 1 - r.first) * p.group;
-  r.parts = min(max((r.steps + p.part_steps - 1) / p.part_steps, 1), p.max_parts);
   return r;
 }
 
+// Equal shares.  With a causal mask the tiles of a sequence differ in steps by
+// as much as its length, and with one tile or equal parts of a tile per
+// workgroup the last ones ran alone: 443 us for 8192 tokens in 4 sequences
+// where the CUs were busy for 286.  So the units of all tiles of a kv head, in
+// order (a tile's steps, and kDkvFixed more for its loads and stores), are cut
+// into p.shares ranges of `each`, one per workgroup: up to two tiles of a
+// share are cut, and their sums go to the workspace, the tile that began in
+// an earlier share to place 0, the one that goes on in the next to place 1;
+// attention_dkv_join adds them in order.
+struct DkvUnits {
+  int64_t n, r, c, group;   // chunks of rows; chunks per tile; chunks before the diagonal
+  bool causal;
+  // units of tiles 0 .. t - 1: group * sum of (n - max(0, i r - c))
+  __device__ __forceinline__ int64_t before(int64_t t) const {
+    int64_t hidden_chunks = 0;
+    if (causal) {
+      const int64_t i0 = c < 0 ? 0 : c / r + 1, m = t - i0;
+      if (m > 0) hidden_chunks = r * ((i0 + t - 1) * m / 2) - c * m;
+    }
+    return t * (kDkvFixed + group * n) - group * hidden_chunks;
+  }
+};
+__device__ __forceinline__ DkvUnits units_of(const BwdParams& p, int lq, int lk, int bn, int rc) {
+  const int off = lk - lq;
+  // ceil(off / rc), off of either sign
+  const int c = off >= 0 ? (off + rc - 1) / rc : -(-off / rc);
+  return DkvUnits{(lq + rc - 1) / rc, bn / rc, c, p.group, p.causal != 0};
+}
+struct Lens {
+  int q0, lq, k0, lk;
+};
+__device__ __forceinline__ Lens lens_of(const BwdParams& p, int s) {
+  if (!p.seq_k) return Lens{0, p.total_q, 0, p.total_k};
+  const int q0 = min(max(p.seq_q[s], 0), p.total_q), q1 = min(max(p.seq_q[s + 1], 0), p.total_q);
+  const int k0 = min(max(p.seq_k[s], 0), p.total_k), k1 = min(max(p.seq_k[s + 1], 0), p.total_k);
+  return Lens{q0, max(q1 - q0, 0), k0, max(k1 - k0, 0)};
+}
+// the sequence that holds unit u and its first unit, and all units of a head
+struct DkvFound {
+  int s;
+  int64_t base, total;
+};
+__device__ __forceinline__ DkvFound find_units(const BwdParams& p, int64_t u, int bn, int rc) {
+  const int lane = threadIdx.x & 63;
+  DkvFound r{0, 0, 0};
+  for (int s0 = 0; s0 < p.batch; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t sum = 0;
+    if (s < p.batch) {
+      const Lens l = lens_of(p, s);
+      sum = units_of(p, l.lq, l.lk, bn, rc).before((l.lk + bn - 1) / bn);
+    }
+    const int64_t own = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t y = __shfl_up((long long)sum, d);
+      if (lane >= d) sum += y;
+    }
+    const int64_t base = r.total + sum - own;
+    const int n = (int)__popcll(__ballot(s < p.batch && base <= u));   // bases never fall
+    if (n > 0) {
+      r.s = uniform(s0 + n - 1);
+      r.base = __shfl((long long)base, n - 1);
+    }
+    r.total += __shfl((long long)sum, 63);
+  }
+  return r;
+}
+__device__ __forceinline__ int64_t dkv_each(int64_t total, int shares) {
+  return max((total + shares - 1) / shares, (int64_t)kDkvLeast);
+}
+// largest t in [0, n) with before(t) <= u
+__device__ __forceinline__ int find_tile(const DkvUnits& x, int n, int64_t u) {
+  return find_sequence(n, 0, [&](int t) { return x.before(t) <= u ? 0 : 1; });
+}
+
 template <class T, int DC, int KW, int RW, int KB>
-__global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p) {
-  // the tile's K and V in registers (else in LDS for all steps)
-  constexpr bool KREG = true, VREG = DC == 64;
-  constexpr int W = KW * RW, NST = DC == 256 ? 2 : 4, BN = 32 * KW * KB, RC = 32 * RW,
-                KS = DC / 16, ND = DC / 32, TILE = RC * DC, NI = TILE / 512 / W,
-                PER = 2 * NI + 1;                        // loads per wave and stage
+struct DkvShape {
+  // V of the tile in registers beside K (else in LDS for all steps)
+  static constexpr bool VREG = DC == 64;
+  static constexpr int W = KW * RW, NST = DC == 256 ? 2 : 4, BN = 32 * KW * KB, RC = 32 * RW,
+                       TILE = RC * DC, NI = TILE / 512 / W, PER = 2 * NI + 1;  // loads per wave and stage
+  static constexpr int STATS = NST * 2 * TILE + (VREG ? 0 : BN * DC), ELEMS = STATS + NST * 256;
   static_assert(KB <= 2 && NI >= 1, "key blocks, loads");
   static_assert((RW - 1) * KW * 32 * DC * 4 <= NST * 4 * TILE, "sums fit in the stages");
-  // one object: with a second one the compiler's bookkeeping of direct-to-LDS
-  // loads makes every read wait for all of them
-  constexpr int HELD = (KREG ? 0 : 1) + (VREG ? 0 : 1);
-  __shared__ __attribute__((aligned(4096))) T smem[NST * 2 * TILE + HELD * BN * DC + NST * 256];
-  float(*sstat)[2][64] = (float(*)[2][64])(smem + NST * 2 * TILE + HELD * BN * DC);
-  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE,
-              sk = sv + (VREG ? 0 : 2 * BN * DC);
+};
+
+// steps [first, first + steps) of a tile; `part`: where the sums go if these
+// are not all of its steps
+template <class T, int DC, int KW, int RW, int KB>
+__device__ __forceinline__ void dkv_tile(const BwdParams& p, T* smem, const BwdPlace& at, int kvh,
+                                         const DkvSteps& all, int first, int steps, float* part) {
+  using S = DkvShape<T, DC, KW, RW, KB>;
+  constexpr bool VREG = S::VREG;
+  constexpr int W = S::W, NST = S::NST, BN = S::BN, RC = S::RC, TILE = S::TILE, NI = S::NI,
+                PER = S::PER, KS = DC / 16, ND = DC / 32;
+  float(*sstat)[2][64] = (float(*)[2][64])(smem + S::STATS);
+  const lds_c ring = (lds_c)smem, sv = ring + NST * 4 * TILE;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6), kw = w % KW, rw = w / KW;
-  int bid = blockIdx.x;
-  const int kvh = bid % p.heads_kv, heads = p.heads_kv * p.group;
-  bid /= p.heads_kv;
-  // the tiles' last parts first: only the longest tiles have them
-  const int slot = bid % p.slots_k, part = p.max_parts - 1 - bid / p.slots_k;
-  const BwdPlace at = bwd_place(p, slot, BN, false);
-  if (!at.any) {
-    if (at.spare >= 0 && part == 0) {
-      const int64_t from =
-          (int64_t)min(max(p.seq_k[p.batch], 0), p.total_k) + (int64_t)at.spare * BN;
-      const int64_t to = min(from + BN, (int64_t)p.total_k);
-      zero_rows<T>((T*)p.dk, p.dk_tok, p.dk_head, 1, kvh, from, to, p.dim, 64 * W);
-      zero_rows<T>((T*)p.dv, p.dv_tok, p.dv_head, 1, kvh, from, to, p.dim, 64 * W);
-    }
-    return;
-  }
-  const DkvSteps all = dkv_steps(p, at, BN, RC);
-  if (part >= all.parts) return;
-  const int first = uniform((int)((int64_t)all.steps * part / all.parts));
-  const int steps = uniform((int)((int64_t)all.steps * (part + 1) / all.parts)) - first;
+  const int heads = p.heads_kv * p.group;
   const int j0 = at.tile * BN + 32 * KB * kw, off = at.lk - at.lq;
 
   // Steps in order: the cut chunks of every head, then the others, each from
@@ -350,7 +450,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   };
   const T* K = (const T*)p.k + (int64_t)at.k0 * p.k_tok + (int64_t)kvh * p.k_head;
   const T* V = (const T*)p.v + (int64_t)at.k0 * p.v_tok + (int64_t)kvh * p.v_head;
-  Vec8<T> kf[KREG ? KB : 1][KREG ? KS : 1], vf[VREG ? KB : 1][VREG ? KS : 1];
+  Vec8<T> kf[KB][KS], vf[VREG ? KB : 1][VREG ? KS : 1];
 #pragma unroll
   for (int x = 0; x < KB; ++x)
 #pragma unroll
@@ -360,20 +460,17 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       Vec8<T> none;
 #pragma unroll
       for (int e = 0; e < 8; ++e) none[e] = (T)0.0f;
-      if constexpr (KREG) kf[x][kk] = d < p.dim ? load8(K + n * p.k_tok + d) : none;
+      kf[x][kk] = d < p.dim ? load8(K + n * p.k_tok + d) : none;
       if constexpr (VREG) vf[x][kk] = d < p.dim ? load8(V + n * p.v_tok + d) : none;
     }
   // (64 rows at a time: what a descriptor covers)
   constexpr int NV = 64 * DC / 512 / W;
 #pragma unroll
-  for (int b = 0; b < BN / 64; ++b) {
+  for (int b = 0; !VREG && b < BN / 64; ++b) {
     const Fetch<T, DC> f = Fetch<T, DC>::of(V, p.v_tok, at.tile * BN + 64 * b, at.lk, p.dim);
-    const Fetch<T, DC> g = Fetch<T, DC>::of(K, p.k_tok, at.tile * BN + 64 * b, at.lk, p.dim);
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (!VREG) f.issue(p.v_tok, p.dim, sv + 128 * b * DC, w * NV + j, lane);
-      if (!KREG) g.issue(p.k_tok, p.dim, sk + 128 * b * DC, w * NV + j, lane);
-    }
+    for (int j = 0; j < NV; ++j)
+      f.issue(p.v_tok, p.dim, sv + 128 * b * DC, w * NV + j, lane);
   }
   floatx16 dk[KB][ND], dv[KB][ND];
 #pragma unroll
@@ -389,7 +486,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   // takes is ready half a phase before, and the vector work is spread over
   // three of the four phases.  Fragments are read RA fragments ahead; the next
   // stage's loads are spread over the slots.
-  constexpr int RA = 2, H = KS / 2;
+    constexpr int RA = 2, H = KS / 2;
   auto block = [&](const Reader<T, DC>& rd, const Reader<T, DC>& rv, const float* stat, int tb,
                    const Next& nx, lds_c to, int stage, auto masked) {
     floatx16 st[KB], dp[KB];
@@ -408,10 +505,9 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       Vec8<T>& f = fr[n % (RA + 1)];
       if (ph == 0) f = rd.straight(0, kk);
       if (ph == 1) f = rd.straight(0, kk, 2 * TILE);
-      if ((ph == 0 && !KREG) || (ph == 1 && !VREG))
+      if (ph == 1 && !VREG)
 #pragma unroll
-        for (int x = 0; x < KB; ++x)
-          fv[n % (RA + 1)][x] = rv.straight(x, kk, ph == 0 ? (int)(sk - sv) : 0);
+        for (int x = 0; x < KB; ++x) fv[n % (RA + 1)][x] = rv.straight(x, kk);
       if (ph == 2) f = rd.transposed(kk / ND, kk % ND, 2 * TILE);
       if (ph == 3) f = rd.transposed(kk / ND, kk % ND);
     };
@@ -482,11 +578,10 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       read(m + RA);
 #pragma unroll
       for (int x = 0; x < KB; ++x) {
-        const Vec8<T>& kx = KREG ? kf[KREG ? x : 0][KREG ? m : 0] : fv[m % (RA + 1)][x];
         if (m == 0)
-          Elem<T>::mma_begin(fr[0], kx, st[x]);
+          Elem<T>::mma_begin(fr[0], kf[x][0], st[x]);
         else
-          Elem<T>::mma_add(fr[m % (RA + 1)], kx, st[x]);
+          Elem<T>::mma_add(fr[m % (RA + 1)], kf[x][m], st[x]);
         fill(m, x);
       }
     }
@@ -605,16 +700,15 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       add(dk[x]);
       add(dv[x]);
     }
-    if (rw > 0) return;
   }
+  const bool whole = steps == all.steps;
 #pragma unroll
   for (int x = 0; x < KB; ++x) {
     const int key = j0 + 32 * x + (lane & 31);
-    const bool valid = key < at.lk;
+    const bool valid = key < at.lk && rw == 0;
     const int64_t n = (int64_t)at.k0 + min(key, at.lk - 1);
-    if (all.parts > 1) {
-      const int64_t stride = (int64_t)p.total_k * p.heads_kv * DC;
-      float* o = p.partials + 2 * part * stride + (n * p.heads_kv + kvh) * DC + 4 * (lane >> 5);
+    if (!whole) {
+      float* o = part + (32 * KB * kw + 32 * x + (lane & 31)) * DC + 4 * (lane >> 5);
       if (valid)
 #pragma unroll
         for (int db = 0; db < ND; ++db)
@@ -623,7 +717,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
             *(floatx4*)(o + 32 * db + 8 * q) =
                 floatx4{dk[x][db][4 * q], dk[x][db][4 * q + 1], dk[x][db][4 * q + 2],
                         dk[x][db][4 * q + 3]};
-            *(floatx4*)(o + stride + 32 * db + 8 * q) =
+            *(floatx4*)(o + BN * DC + 32 * db + 8 * q) =
                 floatx4{dv[x][db][4 * q], dv[x][db][4 * q + 1], dv[x][db][4 * q + 2],
                         dv[x][db][4 * q + 3]};
           }
@@ -635,39 +729,109 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   }
 }
 
-// The parts' sums of a tile whose steps were shared out, in part order; a
-// workgroup per tile, kv head and 32 keys, 8 elements of dK and dV per thread
-// and turn.
+// A workgroup per kv head and share, or, where there are tiles enough to fill
+// the chip many times (p.shares = 0), per tile.
+template <class T, int DC, int KW, int RW, int KB>
+__global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p) {
+  using S = DkvShape<T, DC, KW, RW, KB>;
+  constexpr int BN = S::BN, RC = S::RC;
+  // one object: with a second one the compiler's bookkeeping of direct-to-LDS
+  // loads makes every read wait for all of them
+  __shared__ __attribute__((aligned(4096))) T smem[S::ELEMS];
+  const int kvh = blockIdx.x % p.heads_kv, w = blockIdx.x / p.heads_kv;
+  const int parts = p.shares ? p.shares : p.slots_k;
+  if (p.seq_k) {            // keys behind the last sequence
+    const int end = min(max(p.seq_k[p.batch], 0), p.total_k);
+    const int64_t rest = p.total_k - end;
+    const int64_t from = end + rest * w / parts, to = end + rest * (w + 1) / parts;
+    zero_rows<T>((T*)p.dk, p.dk_tok, p.dk_head, 1, kvh, from, to, p.dim, 64 * S::W);
+    zero_rows<T>((T*)p.dv, p.dv_tok, p.dv_head, 1, kvh, from, to, p.dim, 64 * S::W);
+  }
+  BwdPlace at;
+  int64_t u = 0, end = 0, base = 0;     // units left: [u, end); base: the sequence's first
+  int s = 0;
+  if (p.shares) {
+    const int64_t total = find_units(p, 0, BN, RC).total, each = dkv_each(total, p.shares);
+    u = w * each;
+    end = min(u + each, total);
+    if (u >= end) return;
+    const DkvFound f = find_units(p, u, BN, RC);
+    s = f.s;
+    base = f.base;
+    const Lens l = lens_of(p, s);
+    at = BwdPlace{uniform(l.q0), uniform(l.lq), uniform(l.k0), uniform(l.lk), 0, 0, true};
+    at.tile = uniform(find_tile(units_of(p, at.lq, at.lk, BN, RC), (at.lk + BN - 1) / BN, u - base));
+  } else {
+    at = bwd_place(p, w, BN, false);
+    if (!at.any) return;
+  }
+  for (;;) {
+    const DkvSteps all = dkv_steps(p, at.lq, at.lk, at.tile, BN, RC);
+    int first = 0, steps = all.steps;
+    bool mine = true;
+    float* part = nullptr;
+    if (p.shares) {
+      const int64_t a = base + units_of(p, at.lq, at.lk, BN, RC).before(at.tile) + kDkvFixed;
+      first = uniform((int)max(u - a, (int64_t)0));
+      steps = uniform((int)(min(max(end - a, (int64_t)0), (int64_t)all.steps) - first));
+      mine = all.steps ? steps > 0 : u <= a - kDkvFixed;
+      part = p.partials + ((int64_t)(2 * w + (u <= a)) * p.heads_kv + kvh) * (2 * BN * DC);
+      u = a + all.steps;
+    }
+    if (mine) dkv_tile<T, DC, KW, RW, KB>(p, smem, at, kvh, all, first, steps, part);
+    if (u >= end) return;
+    if (++at.tile * (int64_t)BN >= at.lk) {
+      Lens l;
+      base = u;
+      do l = lens_of(p, ++s);           // (there are units left, so there is one)
+      while (l.lk == 0);
+      at = BwdPlace{uniform(l.q0), uniform(l.lq), uniform(l.k0), uniform(l.lk), 0, 0, true};
+    }
+    __syncthreads();                    // the tile's reads of LDS are done
+  }
+}
+
+// The sums of the tile that a share cut off at its end, over the shares that
+// it went on in, in order; a workgroup per share, kv head and 32 keys, 8
+// elements of dK and dV per thread and turn.
 template <class T, int DC>
 __global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int bn, int rc) {
   int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv;
   bid /= p.heads_kv;
-  const BwdPlace at = bwd_place(p, bid / (bn / 32), bn, false);
-  if (!at.any) return;
-  const int parts = dkv_steps(p, at, bn, rc).parts;
-  if (parts == 1) return;
-  const int j0 = at.tile * bn + 32 * (bid % (bn / 32)), per = p.dim / 8;
-  const int64_t stride = (int64_t)p.total_k * p.heads_kv * DC;
-  for (int x = threadIdx.x; x < min(32, at.lk - j0) * per; x += 256) {
-    const int64_t n = (int64_t)at.k0 + j0 + x / per;
-    const int d = 8 * (x % per);
-    const float* i = p.partials + (n * p.heads_kv + kvh) * DC + d;
+  const int w = bid / (bn / 32);
+  const int64_t total = find_units(p, 0, bn, rc).total, each = dkv_each(total, p.shares);
+  const int64_t end = (w + 1) * each;
+  if (end >= total) return;
+  const DkvFound f = find_units(p, end - 1, bn, rc);
+  const Lens l = lens_of(p, f.s);
+  const DkvUnits x = units_of(p, l.lq, l.lk, bn, rc);
+  const int tile = find_tile(x, (l.lk + bn - 1) / bn, end - 1 - f.base);
+  const int64_t a = f.base + x.before(tile) + kDkvFixed, b = f.base + x.before(tile + 1);
+  if (b <= end || a >= end || a < w * each) return;   // whole, or began elsewhere
+  const int w1 = (int)((b - 1) / each);
+  const int j0 = 32 * (bid % (bn / 32)), per = p.dim / 8;
+  for (int i = threadIdx.x; i < min(32, l.lk - tile * bn - j0) * per; i += 256) {
+    const int key = j0 + i / per, d = 8 * (i % per);
     float k[8] = {}, v[8] = {};
-    for (int g = 0; g < parts; ++g, i += 2 * stride)
+    for (int g = w; g <= w1; ++g) {
+      const float* o = p.partials + ((int64_t)(2 * g + (g == w)) * p.heads_kv + kvh) * (2 * bn * DC) +
+                       key * DC + d;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        k[e] += i[e];
-        v[e] += i[stride + e];
+        k[e] += o[e];
+        v[e] += o[bn * DC + e];
       }
-    Vec8<T> a, b;
+    }
+    Vec8<T> y, z;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      a[e] = (T)(k[e] * p.scale);
-      b[e] = (T)v[e];
+      y[e] = (T)(k[e] * p.scale);
+      z[e] = (T)v[e];
     }
-    *(Vec8<T>*)((T*)p.dk + n * p.dk_tok + kvh * p.dk_head + d) = a;
-    *(Vec8<T>*)((T*)p.dv + n * p.dv_tok + kvh * p.dv_head + d) = b;
+    const int64_t n = (int64_t)l.k0 + tile * bn + key;
+    *(Vec8<T>*)((T*)p.dk + n * p.dk_tok + kvh * p.dk_head + d) = y;
+    *(Vec8<T>*)((T*)p.dv + n * p.dv_tok + kvh * p.dv_head + d) = z;
   }
 }
 

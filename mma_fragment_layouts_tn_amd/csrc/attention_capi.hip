@@ -82,6 +82,9 @@ struct Choice {
   int64_t splits, slots, part_keys;
 };
 
+#ifndef SHF
+#define SHF 8
+#endif
 // Workgroups that occupy every CU.
 constexpr int64_t kFill = 256;
 
@@ -226,11 +229,9 @@ void place_partials(FwdParams& p, void* workspace, int64_t splits, int dc) {
   p.part_ml = (float2*)((char*)workspace + 4 * splits * p.rows * dc);
 }
 
-// How dK and dV are shared out: the steps of a tile (chunks of query tokens of
-// every head of the group) per workgroup, and the workspace.
+// Shares of dK and dV per kv head (0: a workgroup per tile), and the workspace.
 struct BackwardPlan {
-  int64_t slots_q, slots_k, bytes, stats_bytes;
-  int part_steps, max_parts;
+  int64_t slots_q, slots_k, shares, bytes, stats_bytes;
 };
 
 BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
@@ -238,22 +239,26 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   const int64_t group = f.heads_q / f.heads_kv;
   BackwardPlan r;
   // one slot more than tiles can need: the tokens behind the last sequence
-  r.slots_q = tile_slots(f.total_q * group, f.batch, dq_rows(dc), packed) + (packed ? 1 : 0);
-  r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed) + (packed ? 1 : 0);
-  r.stats_bytes = 8 * f.heads_q * f.total_q;
-  r.part_steps = INT_MAX / 2;
-  r.max_parts = 1;
-  const int64_t tiles = ceil_div(f.total_k, dkv_keys(dc)) * f.heads_kv;
-  if (tiles > 0 && tiles < 4 * kFill) {
-    const int64_t steps = group * ceil_div(ceil_div(f.total_q, f.batch), dkv_chunk(dc));
-    const int64_t fair = tiles * steps / (f.causal ? 2 : 1) / kFill;
-    r.part_steps = (int)clamp(fair, 8, INT_MAX / 2);
-    r.max_parts = (int)clamp(ceil_div(2 * steps, r.part_steps), 1, 8);
-  }
-  r.bytes = r.stats_bytes;
-  if (r.max_parts > 1) {
+  r.slots_q = tile_slots(f.total_q * group, f.batch, kDqRows, packed) + (packed ? 1 : 0);
+  r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed);
+  r.stats_bytes = r.bytes = 8 * f.heads_q * f.total_q;
+  r.shares = 0;
+  const int64_t fill = dkv_per_cu(dc) * kFill;
+  if (f.batch <= 256 && r.slots_k * f.heads_kv < SHF * fill) {
+    // as many rounds of the chip, up to four, as leave the fewest CUs idle
+    int64_t best = 0;
+    for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+      const int64_t n = rounds * fill / f.heads_kv;
+      if (n * f.heads_kv * 1024 / rounds > best) {
+        best = n * f.heads_kv * 1024 / rounds;
+        r.shares = n;
+      }
+    }
+    // no more than the steps that there can be would fill
+    const int64_t chunks = ceil_div(f.total_q, dkv_chunk(dc)) + f.batch;
+    r.shares = clamp(r.slots_k * (chunks * group + kDkvFixed) / kDkvLeast, 1, r.shares);
     r.stats_bytes = ceil_div(r.stats_bytes, 16) * 16;
-    r.bytes = r.stats_bytes + r.max_parts * 8 * f.total_k * f.heads_kv * dc;
+    r.bytes = r.stats_bytes + r.shares * f.heads_kv * 2 * 8 * dkv_keys(dc) * dc;
   }
   return r;
 }
@@ -292,7 +297,7 @@ int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* 
   rc = check_output(f.head_dim, {f.total_k, a.dv_token}, {f.heads_kv, a.dv_head}, {1, 0});
   if (rc) return rc;
   const BackwardPlan r = plan_backward(f, seq_q != nullptr);
-  if (r.slots_q * f.heads_kv >= INT_MAX || r.slots_k * 8 * f.heads_kv >= INT_MAX)
+  if (r.slots_q * f.heads_kv >= INT_MAX || r.slots_k * f.heads_kv >= INT_MAX)
     return MFL_E_TOO_LARGE;
   return MFL_OK;
 }
@@ -495,17 +500,17 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.scale_log2 = f.scale * kLog2e;
   p.slots_q = (int)plan.slots_q;
   p.slots_k = (int)plan.slots_k;
-  p.part_steps = plan.part_steps;
-  p.max_parts = plan.max_parts;
+  p.shares = (int)plan.shares;
   p.partials = (float*)((char*)workspace + plan.stats_bytes);
   if (f.total_q > 0) {
     rc = run(dq_kernel(bf16, dc), plan.slots_q * p.heads_kv, &p, stream);
     if (rc) return rc;
   }
   if (f.total_k == 0) return MFL_OK;
-  rc = run(dkv_kernel(bf16, dc), plan.slots_k * p.max_parts * p.heads_kv, &p, stream);
-  if (rc || p.max_parts == 1) return rc;
-  return run(dkv_join_kernel(bf16, dc), plan.slots_k * (dkv_keys(dc) / 32) * p.heads_kv, &p, stream,
+  rc = run(dkv_kernel(bf16, dc), (plan.shares ? plan.shares : plan.slots_k) * p.heads_kv, &p,
+           stream);
+  if (rc || plan.shares <= 1) return rc;
+  return run(dkv_join_kernel(bf16, dc), plan.shares * (dkv_keys(dc) / 32) * p.heads_kv, &p, stream,
              dkv_keys(dc), dkv_chunk(dc));
 }
 

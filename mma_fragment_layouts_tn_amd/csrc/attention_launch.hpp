@@ -29,10 +29,16 @@ KernelRef dkv_join_kernel(bool bf16, int dc);
 constexpr int dim_class(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 // rows (forward, dQ) and keys (dK, dV) per workgroup
 constexpr int tile_rows(int algo) { return algo == 2 ? 16 : 128; }
-constexpr int dq_rows(int dc) { return dc == 256 ? 128 : 256; }
+constexpr int kDqRows = 128;
 constexpr int dkv_keys(int dc) { return dc == 128 ? 256 : 128; }
 // rows that a workgroup of dK and dV takes at a time
 constexpr int dkv_chunk(int dc) { return dc == 64 ? 64 : 32; }
+// units of its steps (attention_dkv): beside a tile's steps, least of a share
+constexpr int kDkvFixed = 4, kDkvLeast = 8;
+#ifndef PCU
+#define PCU 1
+#endif
+constexpr int dkv_per_cu(int dc) { return dc == 64 ? PCU : 1; }
 
 }  // namespace att
 }  // namespace mfl
