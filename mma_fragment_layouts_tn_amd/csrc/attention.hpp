@@ -564,12 +564,13 @@ __device__ __forceinline__ RowOf row_of(int r, int lq, int lk, int group, int kv
   return x;
 }
 
-// Running softmax of the lane's row over the scores in st: updates the
-// reference maximum m (in units of log2), the lane's share l of the sum and
-// the accumulators, leaves the weights in st.
+// Running softmax of the lane's row over the scores in st: the reference that
+// the weights are formed with (in units of log2), after updating the maximum m
+// and, if it grew by more than the slack, the lane's share l of the sum and
+// the accumulators.
 template <int NB, int ND>
-__device__ __forceinline__ void softmax_step(floatx16 (&st)[NB], floatx16 (&acc)[ND], float& m,
-                                             float& l, float c) {
+__device__ __forceinline__ float new_reference(const floatx16 (&st)[NB], floatx16 (&acc)[ND],
+                                               float& m, float& l, float c) {
   float top = -INFINITY;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -586,17 +587,7 @@ __device__ __forceinline__ void softmax_step(floatx16 (&st)[NB], floatx16 (&acc)
       for (int i = 0; i < 16; ++i) acc[j][i] *= f;
     m = to;
   }
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float sum = 0.0f;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(st[b][i], c, -ref));
-      st[b][i] = w;
-      sum += w;
-    }
-  l += sum;
+  return m == -INFINITY ? 0.0f : m;
 }
 
 // bits 0 .. n - 1 (none for n <= 0, all for n > 31)
@@ -713,38 +704,60 @@ __device__ __forceinline__ void tall_rows(const FwdParams& p, T* smem, int bid) 
     const lds_c fill = to + stage_of(c + NST - 1);
     const int key0 = c * CK;
     const Reader<T, DC> rd = reader.at(from);
+    // 2 KS slots of one matrix instruction each for S, as many for O, pinned
+    // in this order: fragments are read RA slots ahead (left to itself the
+    // compiler reads each just before its use), the next chunk's loads are
+    // spread out, and the weights of keys 32 - 63 are formed under the first
+    // half of O.
+    constexpr int RA = 2, N = 4 * KS;
+    Vec8<T> fr[RA + 1], pf[4];
+    auto read = [&](int n) {
+      if (n >= N) return;
+      Vec8<T>& f = fr[n % (RA + 1)];
+      if (n < 2 * KS)
+        f = rd.straight(n / KS, n % KS);
+      else
+        f = rd.transposed((n - 2 * KS) / ND, n % ND, 2 * TILE);
+    };
+    auto load_at = [&](int n) {
+#pragma unroll
+      for (int j = 0; j < 2 * NI; ++j)
+        if ((2 * j + 1) * N / (8 * NI) == n) issue(nx, fill, j);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int n = 0; n < RA; ++n) read(n);
     floatx16 st[2];
     zero(st);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        st[b] = Elem<T>::mma(rd.straight(b, kk), qf[kk], st[b]);
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          if ((2 * j + 1) * 2 * KS / (2 * NI) == b * KS + kk) {
-            pin_loads();
-            issue(nx, fill, j);
-            pin_loads();
-          }
-      }
-    if constexpr (decltype(masked)::value) mask_keys(st, key0, row.limit, lane);
-    softmax_step(st, acc, m, l, p.scale_log2);
-#pragma unroll
-    for (int kc = 0; kc < 4; ++kc) {
-      const Vec8<T> pf = pack8<T>(st[kc / 2], kc % 2);
-#pragma unroll
-      for (int db = 0; db < ND; ++db) {
-        acc[db] = Elem<T>::mma(rd.transposed(kc, db, 2 * TILE), pf, acc[db]);
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-          if ((2 * j + 1) * 4 * ND / (2 * NI) == kc * ND + db) {
-            pin_loads();
-            issue(nx, fill, NI + j);
-            pin_loads();
-          }
-      }
+    for (int n = 0; n < 2 * KS; ++n) {
+      read(n + RA);
+      st[n / KS] = Elem<T>::mma(fr[n % (RA + 1)], qf[n % KS], st[n / KS]);
+      load_at(n);
     }
+    if constexpr (decltype(masked)::value) mask_keys(st, key0, row.limit, lane);
+    const float ref = new_reference(st, acc, m, l, p.scale_log2);
+    float sum = 0.0f;
+    auto weight = [&](int v) {
+      const float w_ = __builtin_amdgcn_exp2f(__builtin_fmaf(st[v / 16][v % 16], p.scale_log2, -ref));
+      st[v / 16][v % 16] = w_;
+      sum += w_;
+      if (v % 8 == 7) pf[v / 8] = pack8<T>(st[v / 16], v / 8 % 2);
+    };
+#pragma unroll
+    for (int v = 0; v < 16; ++v) weight(v);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 2 * KS; n < N; ++n) {
+      const int k = n - 2 * KS;
+      read(n + RA);
+      acc[k % ND] = Elem<T>::mma(fr[n % (RA + 1)], pf[k / ND], acc[k % ND]);
+      if (k < KS)
+#pragma unroll
+        for (int v = 16 + 16 * k / KS; v < 16 + 16 * (k + 1) / KS; ++v) weight(v);
+      load_at(n);
+    }
+    l += sum;
   };
   int c = c0;
   if (c < cut) {

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const Bwd
           work(ph == 4 ? 1 : 0, ph == 3 ? 16 + u : u);
 #pragma unroll
       for (int j = 0; j < 2 * NI; ++j)
-        if ((2 * j + 1) * 6 * KS / (4 * NI) == n) issue(nx, fill, j);
+        if ((2 * j + 1) * 6 * KS / (8 * NI) == n) issue(nx, fill, j);
       __builtin_amdgcn_sched_barrier(0);
     };
     if constexpr (decltype(masked)::value)

@@ -82,9 +82,6 @@ struct Choice {
   int64_t splits, slots, part_keys;
 };
 
-#ifndef SHF
-#define SHF 8
-#endif
 // Workgroups that occupy every CU.
 constexpr int64_t kFill = 256;
 
@@ -243,12 +240,19 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed);
   r.stats_bytes = r.bytes = 8 * f.heads_q * f.total_q;
   r.shares = 0;
-  const int64_t fill = dkv_per_cu(dc) * kFill;
-  if (f.batch <= 256 && r.slots_k * f.heads_kv < SHF * fill) {
+  // Equal shares cost the partial sums of the tiles cut and their join (256 KB
+  // per part at 128 columns; 28 us for 8192 tokens, 8 key heads).  With a
+  // causal mask they pay until there are many tiles per CU (that case: 420 us
+  // with the join, 769 a tile each); without one tiles differ little, and from
+  // two per CU on a tile each is as good (16 key heads of 64, 600 tiles: 91
+  // and 93 us).  Every workgroup walks the sequences' lengths to find its
+  // share, so not for more than 256 sequences.
+  const int64_t tiles = r.slots_k * f.heads_kv;
+  if (f.batch <= 256 && tiles < (f.causal ? 8 : 2) * kFill) {
     // as many rounds of the chip, up to four, as leave the fewest CUs idle
     int64_t best = 0;
     for (int64_t rounds = 1; rounds <= 4; ++rounds) {
-      const int64_t n = rounds * fill / f.heads_kv;
+      const int64_t n = rounds * kFill / f.heads_kv;
       if (n * f.heads_kv * 1024 / rounds > best) {
         best = n * f.heads_kv * 1024 / rounds;
         r.shares = n;

@@ -35,10 +35,6 @@ constexpr int dkv_keys(int dc) { return dc == 128 ? 256 : 128; }
 constexpr int dkv_chunk(int dc) { return dc == 64 ? 64 : 32; }
 // units of its steps (attention_dkv): beside a tile's steps, least of a share
 constexpr int kDkvFixed = 4, kDkvLeast = 8;
-#ifndef PCU
-#define PCU 1
-#endif
-constexpr int dkv_per_cu(int dc) { return dc == 64 ? PCU : 1; }
 
 }  // namespace att
 }  // namespace mfl
