@@ -196,11 +196,12 @@ def _heads(hq, hk):
         raise ValueError("the query heads must be a multiple of the key heads")
 
 
-def _packed_args(q, k, v, seq_q, seq_k, causal, scale, out_strides, algo, splits):
+def _packed_args(q, k, v, seq_q, seq_k, causal, scale, out, algo, splits):
     code = _dtype("q, k and v", q, k, v)
     q0, q1 = _strides3(q, "q")
     k0, k1 = _strides3(k, "k")
     v0, v1 = _strides3(v, "v")
+    o0, o1 = _fresh(q.shape) if out is None else _strides3(out, "out")
     total_q, hq, d = q.shape
     total_k, hk, dk = k.shape
     if v.shape != k.shape:
@@ -209,7 +210,7 @@ def _packed_args(q, k, v, seq_q, seq_k, causal, scale, out_strides, algo, splits
         raise ValueError("q and k disagree on the head dimension")
     _heads(hq, hk)
     return AttentionArgs(code, 1 if causal else 0, _offsets(seq_q, seq_k), total_q, total_k, hq,
-                         hk, d, q0, q1, k0, k1, v0, v1, out_strides[0], out_strides[1],
+                         hk, d, q0, q1, k0, k1, v0, v1, o0, o1,
                          _scale(scale, d), ATTENTION_ALGOS[algo], splits)
 
 
@@ -223,6 +224,19 @@ def _like(t, ref, name):
 def _fresh(shape):
     """Strides of a new 3-D tensor, as _strides."""
     return [shape[1] * shape[2] if shape[0] > 1 else 0, shape[2] if shape[1] > 1 else 0]
+
+
+def _rows(t, stream):
+    """t, or where its tokens lie less than a row apart (a sum's gradient,
+    expanded) a contiguous copy, made on the stream that reads it."""
+    if t.dim() != 3 or t.shape[0] < 2 or t.stride(0) >= t.shape[2]:
+        return t
+    if stream is None or not t.is_cuda:
+        return t.contiguous()
+    other = torch.cuda.ExternalStream(int(stream), device=t.device)
+    t.record_stream(other)
+    with torch.cuda.stream(other):
+        return t.contiguous()
 
 
 # ------------------------------------------------------------------ functions
@@ -248,8 +262,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
         seq_k = seq_q
     if out is not None:
         _like(out, q, "out")
-    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale,
-                     _strides3(out, "out") if out is not None else _fresh(q.shape), algo, splits)
+    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, out, algo, splits)
     run = _Run([t for t in (q, k, v, seq_q, seq_k, out) if t is not None], stream)
     if out is None:
         out = run.like(q)
@@ -271,7 +284,7 @@ def attention_plan(q, k, v, *, seq_q=None, seq_k=None, causal=True, scale=None, 
     tensors; their data is not read."""
     if seq_k is None:
         seq_k = seq_q
-    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, _fresh(q.shape), algo, splits)
+    a = _packed_args(q, k, v, seq_q, seq_k, causal, scale, None, algo, splits)
     al, sp, n = _i32(0), _i32(0), _i64(0)
     _check(_lib.attention_packed_plan(a, _ptr(q), _ptr(k), _ptr(v), _ptr(seq_q), _ptr(seq_k),
                                       1 << 40, None, al, sp, n))
@@ -285,13 +298,15 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        scale: Optional[float] = None, stream=None):
     """(dq, dk, dv) of sum(out * dout) for attention()'s arguments and its out
     and lse.  The gradients of a group's shared kv head are summed over its
-    query heads; tokens of no sequence have gradient 0.  The same arguments
-    give the same bits."""
+    query heads; tokens of no sequence have gradient 0.  q and dout whose
+    tokens overlap (expanded ones) are copied first.  The same arguments give
+    the same bits."""
     if seq_k is None:
         seq_k = seq_q
     _like(dout, q, "dout")
     _like(out, q, "out")
-    f = _packed_args(q, k, v, seq_q, seq_k, causal, scale, _strides3(out, "out"), "auto", 0)
+    dout, q = _rows(dout, stream), _rows(q, stream)
+    f = _packed_args(q, k, v, seq_q, seq_k, causal, scale, out, "auto", 0)
     if lse.dtype != torch.float32:
         raise TypeError("lse must be float32")
     if lse.shape != q.shape[:2] or not lse.is_contiguous():

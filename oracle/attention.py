@@ -23,6 +23,7 @@ import numpy as np
 UNIT = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
 TINY = {"f16": 2.0 ** -25, "bf16": 2.0 ** -134}
 F32 = 2.0 ** -24
+NORMAL = 2.0 ** -126     # fp32's least normal: an exponential below it is 0
 
 
 @dataclass
@@ -113,11 +114,14 @@ def gradients(dout, q, k, v, out, lse, seq_q, seq_k, causal, scale, kind):
             dq[a:b, i] = scale * (ds @ ki)
             dk[x:y, j] += scale * (ds.T @ qi)
             # a score gradient: its weight's error, the fp32 sums of dP and
-            # delta, one rounding
+            # delta, one rounding.  A weight below 2^-126 is formed as 0: off by
+            # less than that, its score gradient by that times |dP - delta|
+            # (for a key that no row gives more this is all of its gradient)
             sums = 2 * (d + 8) * F32 * (np.abs(do) @ np.abs(vi).T +
                                         (np.abs(do) * np.abs(o)).sum(axis=1)[:, None])
-            eds = np.abs(ds) * (u + 2 * eta + 4 * F32) + p * sums + np.where(seen, tiny, 0.0)
-            ep = p * (u + 2 * eta) + np.where(seen, tiny, 0.0)
+            eds = np.abs(ds) * (u + 2 * eta + 4 * F32) + p * sums + \
+                np.where(seen, tiny + NORMAL * np.abs(dp - delta[:, None]), 0.0)
+            ep = p * (u + 2 * eta) + np.where(seen, tiny + NORMAL, 0.0)
             n, m = y - x, (b - a) * g
             tq[a:b, i] = scale * ((eds + 2 * (n + 8) * F32 * np.abs(ds)) @ np.abs(ki))
             tk[x:y, j] += scale * ((eds + 2 * (m + 8) * F32 * np.abs(ds)).T @ np.abs(qi))
