@@ -814,14 +814,27 @@ __global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int
   for (int i = threadIdx.x; i < min(32, l.lk - tile * bn - j0) * per; i += 256) {
     const int key = j0 + i / per, d = 8 * (i % per);
     float k[8] = {}, v[8] = {};
-    for (int g = w; g <= w1; ++g) {
-      const float* o = p.partials + ((int64_t)(2 * g + (g == w)) * p.heads_kv + kvh) * (2 * bn * DC) +
-                       key * DC + d;
+    for (int g0 = w; g0 <= w1; g0 += 4) {     // four parts in flight
+      floatx4 y[4][4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        k[e] += o[e];
-        v[e] += o[bn * DC + e];
+      for (int j = 0; j < 4; ++j) {
+        const int g = min(g0 + j, w1);
+        const float* o = p.partials +
+                         ((int64_t)(2 * g + (g == w)) * p.heads_kv + kvh) * (2 * bn * DC) +
+                         key * DC + d;
+        y[j][0] = *(const floatx4*)o;
+        y[j][1] = *(const floatx4*)(o + 4);
+        y[j][2] = *(const floatx4*)(o + bn * DC);
+        y[j][3] = *(const floatx4*)(o + bn * DC + 4);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (g0 + j <= w1)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            k[e] += y[j][e / 4][e % 4];
+            v[e] += y[j][2 + e / 4][e % 4];
+          }
     }
     Vec8<T> y, z;
 #pragma unroll

@@ -34,7 +34,7 @@ constexpr int dkv_keys(int dc) { return dc == 128 ? 256 : 128; }
 // rows that a workgroup of dK and dV takes at a time
 constexpr int dkv_chunk(int dc) { return dc == 64 ? 64 : 32; }
 // units of its steps (attention_dkv): beside a tile's steps, least of a share
-constexpr int kDkvFixed = 4, kDkvLeast = 8;
+constexpr int kDkvFixed = 8, kDkvLeast = 6;
 
 }  // namespace att
 }  // namespace mfl
