@@ -22,7 +22,10 @@
  *
  * Addressing (elements): x(t, h, d) = X[t * x_token + h * x_head + d].  Every
  * pointer is 16-byte aligned and every stride a multiple of 8 (else
- * MFL_E_MISALIGNED); strides are not negative, 0 lets an input be shared.
+ * MFL_E_MISALIGNED); strides are not negative (MFL_E_LEADING_DIM), 0 lets an
+ * input be shared, and those between tokens are at most 2^23 (q, k, v, dout,
+ * and the prefix; MFL_E_TOO_LARGE).  No two elements of an output share an
+ * address (MFL_E_ALIAS).
  * head_dim is a multiple of 8 up to 256 (else MFL_E_UNSUPPORTED).
  *
  * Packed sequences.  seq_q and seq_k hold batch + 1 offsets each in device
@@ -35,7 +38,9 @@
  *
  * Values of keys outside a sequence never reach it, whatever they are.  A
  * key inside it whose v holds infinities or NaNs can make NaN of out in the
- * rows the causal mask hides it from: a weight of 0 times NaN.
+ * rows the causal mask hides it from: a weight of 0 times NaN.  In the
+ * backward functions a score gradient is rounded to the inputs' type: in fp16
+ * one beyond 65504 becomes infinite.
  *
  * Ownership and execution are gemm_tn's (mfl_gemm.h): nothing is allocated,
  * kept or synchronised; work runs on `stream`.  A workspace belongs to one
@@ -91,7 +96,9 @@ int attention_packed_plan(const mfl_attention_t* a, const void* q, const void* k
                           int64_t* workspace_bytes);
 
 /* Gradients of sum(out * dout) with respect to q, k and v, from the forward
- * call's out and lse; `f` as in that call (algo and splits are not read). */
+ * call's out and lse; `f` as in that call (algo and splits are not read).
+ * With more than one token q_token and dout_token are at least head_dim
+ * (MFL_E_LEADING_DIM).  Gradients of tokens behind the last sequence are 0. */
 typedef struct {
   mfl_attention_t f;
   int64_t dout_token, dout_head, dq_token, dq_head, dk_token, dk_head, dv_token, dv_head;

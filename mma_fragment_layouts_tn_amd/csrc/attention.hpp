@@ -491,9 +491,6 @@ constexpr bool swizzle_is_linear() {
 }
 static_assert(swizzle_is_linear<64>() && swizzle_is_linear<128>() && swizzle_is_linear<256>(),
               "a lane's column of another instruction by XOR");
-// memory loads stay on their side, everything else may pass
-__device__ __forceinline__ void pin_loads() { __builtin_amdgcn_sched_barrier(0x38f); }
-
 // 8 values of a row from the two halves of the wave: value i of block x is
 // d = 8 (i / 4) + 4 (l / 32) + i % 4; after the exchange lane l holds
 // d = 8 (q + l / 32) + 0..7 of the pair of groups q, q + 1
@@ -617,7 +614,17 @@ __device__ __forceinline__ void mask_keys(floatx16 (&st)[NB], int key0, int limi
 // ------------------------------------------------------ forward, tall
 // Four waves of 32 rows each over chunks of 64 keys staged in a ring of NST
 // LDS stages (K and V of a chunk together), shared by the workgroup: 64 KB, so
-// that two workgroups fit a CU up to 128 columns.
+// that two workgroups fit a CU up to 128 columns.  Eight waves in one
+// workgroup per CU took 1 - 6 % longer on long prompts and 30 % on 2048 tokens
+// (62 against 49 us).
+//
+// Bound by the matrix pipe and what it may draw: 8192 causal tokens, 32/8
+// heads of 128, fp16, take 532 us (1,033 TFLOP/s; a large library product
+// reaches 1,470), and 420 - 450 with loads, LDS reads, exponentials and maxima
+// all taken out.  Scores formed one chunk ahead of their weights, so that a
+// wave's own matrix instructions cover its softmax, took 2 % longer (the
+// copies of the scores, one product more per tile); raised wave priority
+// around the products, 4 slots of lead and alternating sums changed nothing.
 template <int DC>
 MFL_HD constexpr int tall_stages() {
   return DC == 64 ? 4 : 2;
@@ -626,7 +633,7 @@ MFL_HD constexpr int tall_stages() {
 template <class T, int DC>
 __device__ __forceinline__ void tall_rows(const FwdParams& p, T* smem, int bid) {
   constexpr int W = 4, BM = 32 * W, CK = 64, NST = tall_stages<DC>(), KS = DC / 16, ND = DC / 32;
-  constexpr int TILE = CK * DC, NI = CK * DC / 512 / W;   // elements, instructions per matrix and wave
+  constexpr int TILE = CK * DC, NI = TILE / 512 / W;   // elements, loads per matrix and wave
   static_assert(NI >= 1, "loads");
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const int kvh = bid % p.heads_kv;
@@ -739,7 +746,8 @@ __device__ __forceinline__ void tall_rows(const FwdParams& p, T* smem, int bid) 
     const float ref = new_reference(st, acc, m, l, p.scale_log2);
     float sum = 0.0f;
     auto weight = [&](int v) {
-      const float w_ = __builtin_amdgcn_exp2f(__builtin_fmaf(st[v / 16][v % 16], p.scale_log2, -ref));
+      const float w_ =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(st[v / 16][v % 16], p.scale_log2, -ref));
       st[v / 16][v % 16] = w_;
       sum += w_;
       if (v % 8 == 7) pf[v / 8] = pack8<T>(st[v / 16], v / 8 % 2);
@@ -810,6 +818,8 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_tall(const F
 // scores are formed, the next V after the second product, so a wave always has
 // half a chunk in flight, no wave waits for another before the end, and two
 // workgroups fit a CU (DC <= 128).  The W partial rows are joined in LDS.
+// Bound by latency at few keys, by memory at many: one token of 32/8 heads of
+// 128 against 8192 keys takes 12.5 us in 16 parts, join included.
 //
 // Lane l holds row l % 16; value v of the scores of keys 16 b .. 16 b + 15 is
 // key 16 b + 4 (l / 16) + v.  The second product's operand takes the values of
@@ -997,7 +1007,8 @@ __device__ __forceinline__ void flat_rows(const FwdParams& p, T* smem, int bid) 
 }
 
 template <class T, int DC>
-__global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2) attention_flat(const FwdParams p) {
+__global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2)
+    attention_flat(const FwdParams p) {
   __shared__ __attribute__((aligned(4096))) T smem[flat_elems<T, DC>()];
   flat_rows<T, DC>(p, smem, blockIdx.x);
 }
@@ -1006,9 +1017,13 @@ __global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2) attention_
 // workgroups work on `a` (the prefix, tall or flat rows), the others on `b`
 // (the sequences' own keys, flat rows).  The prefix is bound by the matrix
 // pipe when many rows share it, the own keys by memory; side by side on a CU
-// each fills the other's waits.
+// each fills the other's waits.  64 rows of 32/8 heads of 128 behind 8192 keys
+// with up to 1000 own: 39 us, in two launches one after the other 55; 128 rows
+// behind 32768 keys with 256 - 2048 own: 179 us (1.1 GB of own keys and
+// values and 550 GFLOP: 4 TB/s would take 140), two launches 249.
 template <class T, int DC, bool TALL>
-__global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_pair(const FwdParams a, const FwdParams b, int n0) {
+__global__ void __launch_bounds__(256, DC == 256 ? 1 : 2)
+    attention_pair(const FwdParams a, const FwdParams b, int n0) {
   constexpr int E0 = TALL ? tall_stages<DC>() * 2 * 64 * DC : 0, E1 = flat_elems<T, DC>();
   __shared__ __attribute__((aligned(4096))) T smem[E0 > E1 ? E0 : E1];
   const int bid = blockIdx.x;
@@ -1062,7 +1077,8 @@ __device__ __forceinline__ void join_row(const float* part_o, const float2* part
       for (int j = 0; j < 8; ++j) {
         g[j] = __shfl(f, i + j);
         const int s = s0 + i + j;
-        if (i + j < n && g[j] != 0.0f) v[j] = *(const vecE*)(part_o + (s * rows + row) * DC + E * lane);
+        if (i + j < n && g[j] != 0.0f)
+          v[j] = *(const vecE*)(part_o + (s * rows + row) * DC + E * lane);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)

@@ -61,6 +61,15 @@ __device__ __forceinline__ void zero_rows(T* base, int64_t tok, int64_t head, in
 }
 
 // ------------------------------------------------------------------- dQ
+// Four waves of 32 rows each, as the forward kernel's tall form, over chunks of
+// 64 keys; also forms the rows' log-sum-exps in base 2 and deltas, which the
+// kernel of dK and dV reads.  delta is the fp32 sum over the 16-bit out, dS is
+// rounded to 16 bits as the third product's operand: together with the
+// results' own rounding the error of dQ and dK is 0.0027 of their norm (bf16).
+//
+// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 279 us, 1,016 TFLOP/s,
+// the matrix pipe busy for 55 % of the cycles.  Reads placed by the compiler,
+// one before each use: 315; 8 waves in one workgroup per CU 316.
 template <class T, int DC>
 __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const BwdParams p) {
   constexpr int W = 4, NST = tall_stages<DC>(), BM = 32 * W, CK = 64, KS = DC / 16, ND = DC / 32,
@@ -198,7 +207,8 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const Bwd
     };
     if constexpr (decltype(masked)::value)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) seen_keys[b] = low_bits(row.limit + 1 - c * CK - 32 * b - 4 * (lane >> 5));
+      for (int b = 0; b < 2; ++b)
+        seen_keys[b] = low_bits(row.limit + 1 - c * CK - 32 * b - 4 * (lane >> 5));
 #pragma unroll
     for (int n = 0; n < RA; ++n) read(n);
 #pragma unroll
@@ -255,10 +265,17 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const Bwd
 // operands of dV^T = dO^T P and dK^T = Q^T dS as they are, and every fragment
 // read from LDS serves the KB key blocks of the wave.
 //
-// With KB = 2 a wave's sums take all 256 accumulation registers, one wave per
-// SIMD, and K and V of the tile stay in LDS.  Two waves of 32 keys each instead issue twice the LDS
-// reads, waits and scalar instructions per matrix instruction, and those, not
-// the matrix pipe, set their pace: 4,600 cycles for 2,048 of matrix work.
+// With KB = 2 and 128 columns a wave's sums take all 256 accumulation
+// registers, one wave per SIMD; K of the tile is held in registers, V in LDS.
+// Two waves of 32 keys each instead issue twice the LDS reads, waits and
+// scalar instructions per matrix instruction, and those, not the matrix pipe,
+// set their pace: 4,600 cycles for 2,048 of matrix work, here 3,600.
+//
+// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 417 us, 907 TFLOP/s,
+// the matrix pipe busy for 47 % of the cycles, a wave issuing for as many;
+// with one wave per SIMD what it waits for is not filled.  Reads 1, 3 or 4
+// slots ahead instead of 2 change nothing.  The join takes 30 us more, for
+// 137 MB of partial sums written and read.
 //
 // The chunks that the causal mask cuts come first, in a loop of their own: the
 // mask as a branch inside one loop made the compiler spill accumulators.
@@ -285,13 +302,14 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, int lq, int lk
 
 // Equal shares.  With a causal mask the tiles of a sequence differ in steps by
 // as much as its length, and with one tile or equal parts of a tile per
-// workgroup the last ones ran alone: 443 us for 8192 tokens in 4 sequences
-// where the CUs were busy for 286.  So the units of all tiles of a kv head, in
-// order (a tile's steps, and kDkvFixed more for its loads and stores), are cut
-// into p.shares ranges of `each`, one per workgroup: up to two tiles of a
-// share are cut, and their sums go to the workspace, the tile that began in
-// an earlier share to place 0, the one that goes on in the next to place 1;
-// attention_dkv_join adds them in order.
+// workgroup the last ones ran alone: 443 us, and 21 for the join, for 8192
+// tokens in 4 sequences where the CUs were busy for 286.  So the units of all
+// tiles of a kv head, in order (a tile's steps, and kDkvFixed more for its
+// loads and stores), are cut into p.shares ranges of `each`, one per
+// workgroup: 417 us, and 30 for the join.  Up to two tiles of a share are cut,
+// and their sums go to the workspace, the tile that began in an earlier share
+// to place 0, the one that goes on in the next to place 1; attention_dkv_join
+// adds them in order.
 struct DkvUnits {
   int64_t n, r, c, group;   // chunks of rows; chunks per tile; chunks before the diagonal
   bool causal;
@@ -364,7 +382,8 @@ struct DkvShape {
   // V of the tile in registers beside K (else in LDS for all steps)
   static constexpr bool VREG = DC == 64;
   static constexpr int W = KW * RW, NST = DC == 256 ? 2 : 4, BN = 32 * KW * KB, RC = 32 * RW,
-                       TILE = RC * DC, NI = TILE / 512 / W, PER = 2 * NI + 1;  // loads per wave and stage
+                       TILE = RC * DC, NI = TILE / 512 / W,
+                       PER = 2 * NI + 1;                 // loads per wave and stage
   static constexpr int STATS = NST * 2 * TILE + (VREG ? 0 : BN * DC), ELEMS = STATS + NST * 256;
   static_assert(KB <= 2 && NI >= 1, "key blocks, loads");
   static_assert((RW - 1) * KW * 32 * DC * 4 <= NST * 4 * TILE, "sums fit in the stages");
@@ -760,7 +779,8 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
     base = f.base;
     const Lens l = lens_of(p, s);
     at = BwdPlace{uniform(l.q0), uniform(l.lq), uniform(l.k0), uniform(l.lk), 0, 0, true};
-    at.tile = uniform(find_tile(units_of(p, at.lq, at.lk, BN, RC), (at.lk + BN - 1) / BN, u - base));
+    at.tile = uniform(
+        find_tile(units_of(p, at.lq, at.lk, BN, RC), (at.lk + BN - 1) / BN, u - base));
   } else {
     at = bwd_place(p, w, BN, false);
     if (!at.any) return;
