@@ -227,9 +227,11 @@ def _fresh(shape):
 
 
 def _rows(t, stream):
-    """t, or where its tokens lie less than a row apart (a sum's gradient,
-    expanded) a contiguous copy, made on the stream that reads it."""
-    if t.dim() != 3 or t.shape[0] < 2 or t.stride(0) >= t.shape[2]:
+    """t, or where its elements do not follow each other or its tokens lie less
+    than a row apart (a sum's gradient, expanded) a contiguous copy, made on
+    the stream that reads it."""
+    if t.dim() != 3 or t.numel() == 0 or \
+            (t.stride(2) == 1 and (t.shape[0] < 2 or t.stride(0) >= t.shape[2])):
         return t
     if stream is None or not t.is_cuda:
         return t.contiguous()
@@ -298,8 +300,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
                        scale: Optional[float] = None, stream=None):
     """(dq, dk, dv) of sum(out * dout) for attention()'s arguments and its out
     and lse.  The gradients of a group's shared kv head are summed over its
-    query heads; tokens of no sequence have gradient 0.  q and dout whose
-    tokens overlap (expanded ones) are copied first.  The same arguments give
+    query heads; tokens of no sequence have gradient 0.  Expanded or
+    transposed q and dout are copied first.  The same arguments give
     the same bits."""
     if seq_k is None:
         seq_k = seq_q

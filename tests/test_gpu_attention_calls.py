@@ -340,3 +340,91 @@ def test_prompt_then_decoding_then_training():
     p = Packed(kind, [n0 + steps] * b, [n0 + steps] * b, h, g, d, True)
     p.q, p.k, p.v = q, k, v
     p.check_backward(*p.check_forward())
+
+
+@pytest.mark.parametrize("dim", [8, 24, 136, 248])
+def test_head_dims(dim):
+    p = Packed("bf16", [70, 1, 140], [95, 1, 140], 4, 2, dim, True)
+    p.check_backward(*p.check_forward(algo="tall"))
+    p.check_forward(algo="flat")
+    Prefix("bf16", 3, 2, 100, 40, [0, 2, 40], 4, 2, dim).check()
+
+
+def test_many_sequences():
+    """Thousands of sequences of up to three tokens, many empty."""
+    n = [(11 * i) % 7 % 4 for i in range(5000)]
+    p = Packed("bf16", n, n, 2, 1, 64, True)
+    for algo in ("flat", "tall"):
+        out, lse = p.check_forward(algo=algo)
+    p.check_backward(out, lse)
+
+
+def test_neighbours_do_not_leak():
+    """A sequence full of NaN between two others: theirs stay the same bits."""
+    lens = [37, 50, 90]
+    p = Packed("bf16", lens, lens, 4, 2, 64, True)
+    dev = [x.cuda() for x in (p.q, p.k, p.v, p.dout)]
+    how = p.how()
+
+    def run():
+        res = []
+        for algo in ("tall", "flat"):
+            for splits in (1, 3):
+                res += mfl.attention(*dev[:3], return_lse=True, algo=algo, splits=splits, **how)
+        out, lse = mfl.attention(*dev[:3], return_lse=True, **how)
+        return [*res, *mfl.attention_backward(dev[3], *dev[:3], out, lse, **how)]
+    clean = run()
+    for x in dev:
+        x[37:87] = float("nan")
+    for a, b in zip(run(), clean):
+        assert same(a[:37], b[:37]) and same(a[87:], b[87:])
+
+
+def test_prefix_lengths_are_held():
+    """Lengths below 0 and beyond the capacity count as 0 and the capacity;
+    one cache for the whole batch."""
+    x = Prefix("bf16", 4, 2, 70, 33, [0, 33, 33, 0], 4, 2, 64)
+    dev = [t.cuda() for t in (x.q, x.pk, x.pv, x.k, x.v)]
+    want = mfl.attention_prefix(*dev, x.lengths.cuda())
+    wrong = torch.tensor([-7, 34, (1 << 31) - 1, -(1 << 31)], dtype=torch.int32).cuda()
+    assert same(mfl.attention_prefix(*dev, wrong), want)
+    k, v = (t[1:2].expand(4, 33, 2, 64) for t in dev[3:])
+    n = torch.tensor([33, 5, 1, 20], dtype=torch.int32).cuda()
+    assert same(mfl.attention_prefix(*dev[:3], k, v, n),
+                mfl.attention_prefix(*dev[:3], k.contiguous(), v.contiguous(), n))
+
+
+def test_one_token_sum():
+    """The gradient of a sum at one token: every stride 0."""
+    gen = torch.Generator().manual_seed(4)
+    q, k = values(gen, (1, 4, 64), "f16").cuda(), values(gen, (9, 2, 64), "f16").cuda()
+    out, lse = mfl.attention(q, k, k, return_lse=True)
+    ones = torch.ones((), dtype=torch.float16).cuda().expand(1, 4, 64)
+    want = mfl.attention_backward(ones.contiguous(), q, k, k, out, lse)
+    for a, b in zip(mfl.attention_backward(ones, q, k, k, out, lse), want):
+        assert same(a, b)
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces in flight on two streams together."""
+    p = Packed("bf16", [600, 300], [600, 300], 8, 2, 128, True)
+    x = Prefix("bf16", 32, 1, 2000, 100, [3 * i for i in range(32)], 8, 2, 128)
+    dev = [t.cuda() for t in (p.q, p.k, p.v, p.dout)]
+    pre = [t.cuda() for t in (x.q, x.pk, x.pv, x.k, x.v, x.lengths)]
+    how = p.how()
+    out, lse = mfl.attention(*dev[:3], return_lse=True, splits=4, **how)
+    grads = mfl.attention_backward(dev[3], *dev[:3], out, lse, **how)
+    dec = mfl.attention_prefix(*pre)
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        with torch.cuda.stream(a):
+            o, l = mfl.attention(*dev[:3], return_lse=True, splits=4, **how)
+            got.append((o, out))
+            got += zip(mfl.attention_backward(dev[3], *dev[:3], o, l, **how), grads)
+        with torch.cuda.stream(b):
+            for _ in range(4):
+                got.append((mfl.attention_prefix(*pre), dec))
+    torch.cuda.synchronize()
+    assert all(same(x, y) for x, y in got)
