@@ -2,6 +2,11 @@
 operands, rows of no sequence, other streams, captured graphs, caches beyond
 32-bit offsets, the same bits every time, gradients against differences, and
 the three together (a prompt, then decoding behind it, then training on it).
+
+The file's name sorts behind test_gpu_probe.py: once a process has used several
+streams, the die that a launch on the default one starts on is no longer the
+first (the dies still take turns, which is what the kernels need), and a test
+there asks for the first.
 """
 import numpy as np
 import pytest
