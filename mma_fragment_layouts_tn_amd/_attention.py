@@ -169,6 +169,15 @@ def _strides4(t: torch.Tensor, name: str):
     return w if b > 1 else 0, x if n > 1 else 0, y if h > 1 else 0
 
 
+def _strides_q(t: torch.Tensor, name: str):
+    """_strides4 of (batch, tokens, heads, dim), or of (batch, heads, dim) as
+    one token each."""
+    if t.dim() == 4:
+        return _strides4(t, name)
+    w, y = _strides3(t, name)
+    return w, 0, y
+
+
 def _scale(scale, dim):
     scale = 1.0 / math.sqrt(dim or 1) if scale is None else float(scale)
     if not (scale > 0.0 and math.isfinite(scale)):
@@ -346,8 +355,11 @@ def attention_prefix(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     code = _dtype("q, the prefix, k and v", q, prefix_k, prefix_v, k, v)
     if q.dim() not in (3, 4):
         raise ValueError("q must be (batch, heads, dim) or (batch, tokens, heads, dim)")
-    x = q if q.dim() == 4 else q.unsqueeze(1)
-    batch, tokens, hq, d = x.shape
+    if q.dim() == 4:
+        batch, tokens, hq, d = q.shape
+    else:
+        (batch, hq, d), tokens = q.shape, 1
+    qs = _strides_q(q, "q")
     pks, pvs = _strides3(prefix_k, "prefix_k"), _strides3(prefix_v, "prefix_v")
     ks, vs = _strides4(k, "k"), _strides4(v, "v")
     prefix, hk, dim = prefix_k.shape
@@ -368,9 +380,11 @@ def attention_prefix(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     run = _Run([t for t in (q, prefix_k, prefix_v, k, v, lengths, out) if t is not None], stream)
     if out is None:
         out = run.like(q)
-    os = _strides4(out if q.dim() == 4 else out.unsqueeze(1), "out")
+        os = (tokens * hq * d if batch > 1 else 0, hq * d if tokens > 1 else 0, d if hq > 1 else 0)
+    else:
+        os = _strides_q(out, "out")
     a = AttentionPrefixArgs(code, ATTENTION_ALGOS[algo], batch, tokens, prefix, capacity, hq, hk,
-                            d, *_strides4(x, "q"), *pks, *pvs, *ks, *vs, *os, _scale(scale, d),
+                            d, *qs, *pks, *pvs, *ks, *vs, *os, _scale(scale, d),
                             *splits)
     lse = run.empty(q.shape[:-1], torch.float32) if return_lse else None
     ptrs = (_ptr(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(k), _ptr(v), _ptr(lengths), _ptr(out),
