@@ -1110,24 +1110,27 @@ __global__ void __launch_bounds__(256) attention_join(const CombineParams p) {
                   p.lse ? p.lse + row : nullptr);
 }
 
-// the rows of the tiles that took more than one split, one wave each
+// the rows of the tiles that took more than one split, one after the other
+// where a workgroup has `each` > 4 of them
 template <class T, int DC>
-__global__ void __launch_bounds__(256) attention_join_tiles(const FwdParams p, int bm) {
+__global__ void __launch_bounds__(256) attention_join_tiles(const FwdParams p, int bm, int each) {
   int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv;
   bid /= p.heads_kv;
-  const int per = bm / 4;
+  const int per = bm / each;
   const Place at = place_of(p, bid / per, bm);
   if (!at.any) return;
   const int parts = parts_of(p, seen_of(p, at, bm));
   if (parts == 1) return;
-  const int r = at.tile * bm + 4 * (bid % per) + uniform(threadIdx.x >> 6);
-  const RowOf row = row_of(r, at.lq, at.lk, p.group, kvh, at.q0, p.causal);
-  if (!row.valid) return;
-  const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
-  join_row<T, DC>(p.part_o, p.part_ml, p.rows, out_row, parts, p.dim,
-                  (T*)p.o + row.n * p.o_tok + row.head * p.o_head,
-                  p.lse ? p.lse + out_row : nullptr);
+  for (int i = 0; i < each; i += 4) {
+    const int r = at.tile * bm + each * (bid % per) + i + uniform(threadIdx.x >> 6);
+    const RowOf row = row_of(r, at.lq, at.lk, p.group, kvh, at.q0, p.causal);
+    if (!row.valid) return;
+    const int64_t out_row = (int64_t)row.n * (p.heads_kv * p.group) + row.head;
+    join_row<T, DC>(p.part_o, p.part_ml, p.rows, out_row, parts, p.dim,
+                    (T*)p.o + row.n * p.o_tok + row.head * p.o_head,
+                    p.lse ? p.lse + out_row : nullptr);
+  }
 }
 
 }  // namespace att
