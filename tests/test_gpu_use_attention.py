@@ -433,3 +433,14 @@ def test_two_streams_at_once():
                 got.append((mfl.attention_prefix(*pre), dec))
     torch.cuda.synchronize()
     assert all(same(x, y) for x, y in got)
+
+
+@pytest.mark.parametrize("heads", [(300, 300, 64), (1100, 1100, 8), (64, 1, 64), (34, 2, 128)],
+                         ids=str)
+def test_many_heads(heads):
+    """More key heads than workgroups for shares of the keys; groups wider
+    than a tile's 16 rows, and not a power of two."""
+    p = Packed("bf16", [33, 2], [40, 2], *heads, True)
+    p.check_backward(*p.check_forward(algo="flat"))
+    p.check_forward(algo="tall")
+    Prefix("bf16", 2, 1, 40, 9, [9, 3], *heads).check()
