@@ -141,6 +141,12 @@ struct CombineParams {
   int64_t o_batch, o_tok, o_head;
 };
 
+// The tile that a share cut off at its end: first key, keys (0: none), the
+// last share that it went on in.
+struct DkvCut {
+  int key, keys, last;
+};
+
 struct BwdParams {
   const void* q;
   const void* k;
@@ -162,6 +168,7 @@ struct BwdParams {
   // dK, dV: workgroups per kv head, 0: one per tile; sums of the tiles cut,
   // two places per share and kv head, dK then dV of the keys of a tile
   int shares;
+  DkvCut* cuts;               // one per share
   float* partials;
 };
 

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const Bwd
 // 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 417 us, 907 TFLOP/s,
 // the matrix pipe busy for 47 % of the cycles, a wave issuing for as many;
 // with one wave per SIMD what it waits for is not filled.  Reads 1, 3 or 4
-// slots ahead instead of 2 change nothing.  The join takes 30 us more, for
+// slots ahead instead of 2 change nothing.  The join takes 26 us more, for
 // 137 MB of partial sums written and read.
 //
 // The chunks that the causal mask cuts come first, in a loop of their own: the
@@ -306,10 +306,10 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, int lq, int lk
 // tokens in 4 sequences where the CUs were busy for 286.  So the units of all
 // tiles of a kv head, in order (a tile's steps, and kDkvFixed more for its
 // loads and stores), are cut into p.shares ranges of `each`, one per
-// workgroup: 417 us, and 30 for the join.  Up to two tiles of a share are cut,
+// workgroup: 417 us, and 26 for the join.  Up to two tiles of a share are cut,
 // and their sums go to the workspace, the tile that began in an earlier share
-// to place 0, the one that goes on in the next to place 1; attention_dkv_join
-// adds them in order.
+// to place 0, the one that goes on in the next to place 1; the latter is noted
+// in p.cuts, and attention_dkv_join adds its sums in order.
 struct DkvUnits {
   int64_t n, r, c, group;   // chunks of rows; chunks per tile; chunks before the diagonal
   bool causal;
@@ -768,11 +768,14 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
   }
   BwdPlace at;
   int64_t u = 0, end = 0, base = 0;     // units left: [u, end); base: the sequence's first
+  int64_t each = 0;
   int s = 0;
   if (p.shares) {
-    const int64_t total = find_units(p, 0, BN, RC).total, each = dkv_each(total, p.shares);
+    const int64_t total = find_units(p, 0, BN, RC).total;
+    each = dkv_each(total, p.shares);
     u = w * each;
     end = min(u + each, total);
+    if (kvh == 0 && threadIdx.x == 0) p.cuts[w] = DkvCut{0, 0, 0};
     if (u >= end) return;
     const DkvFound f = find_units(p, u, BN, RC);
     s = f.s;
@@ -796,6 +799,9 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       steps = uniform((int)(min(max(end - a, (int64_t)0), (int64_t)all.steps) - first));
       mine = all.steps ? steps > 0 : u <= a - kDkvFixed;
       part = p.partials + ((int64_t)(2 * w + (u <= a)) * p.heads_kv + kvh) * (2 * BN * DC);
+      if (u <= a && steps > 0 && steps < all.steps && kvh == 0 && threadIdx.x == 0)
+        p.cuts[w] = DkvCut{at.k0 + at.tile * BN, min(BN, at.lk - at.tile * BN),
+                           (int)((a + all.steps - 1) / each)};
       u = a + all.steps;
     }
     if (mine) dkv_tile<T, DC, KW, RW, KB>(p, smem, at, kvh, all, first, steps, part);
@@ -815,23 +821,15 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
 // it went on in, in order; a workgroup per share, kv head and 32 keys, 8
 // elements of dK and dV per thread and turn.
 template <class T, int DC>
-__global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int bn, int rc) {
+__global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int bn) {
   int bid = blockIdx.x;
   const int kvh = bid % p.heads_kv;
   bid /= p.heads_kv;
   const int w = bid / (bn / 32);
-  const int64_t total = find_units(p, 0, bn, rc).total, each = dkv_each(total, p.shares);
-  const int64_t end = (w + 1) * each;
-  if (end >= total) return;
-  const DkvFound f = find_units(p, end - 1, bn, rc);
-  const Lens l = lens_of(p, f.s);
-  const DkvUnits x = units_of(p, l.lq, l.lk, bn, rc);
-  const int tile = find_tile(x, (l.lk + bn - 1) / bn, end - 1 - f.base);
-  const int64_t a = f.base + x.before(tile) + kDkvFixed, b = f.base + x.before(tile + 1);
-  if (b <= end || a >= end || a < w * each) return;   // whole, or began elsewhere
-  const int w1 = (int)((b - 1) / each);
+  const DkvCut cut = p.cuts[w];
+  const int w1 = cut.last;
   const int j0 = 32 * (bid % (bn / 32)), per = p.dim / 8;
-  for (int i = threadIdx.x; i < min(32, l.lk - tile * bn - j0) * per; i += 256) {
+  for (int i = threadIdx.x; i < min(32, cut.keys - j0) * per; i += 256) {
     const int key = j0 + i / per, d = 8 * (i % per);
     float k[8] = {}, v[8] = {};
     for (int g0 = w; g0 <= w1; g0 += 4) {     // four parts in flight
@@ -862,7 +860,7 @@ __global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int
       y[e] = (T)(k[e] * p.scale);
       z[e] = (T)v[e];
     }
-    const int64_t n = (int64_t)l.k0 + tile * bn + key;
+    const int64_t n = (int64_t)cut.key + key;
     *(Vec8<T>*)((T*)p.dk + n * p.dk_tok + kvh * p.dk_head + d) = y;
     *(Vec8<T>*)((T*)p.dv + n * p.dv_tok + kvh * p.dv_head + d) = z;
   }

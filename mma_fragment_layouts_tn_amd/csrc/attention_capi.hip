@@ -228,7 +228,7 @@ void place_partials(FwdParams& p, void* workspace, int64_t splits, int dc) {
 
 // Shares of dK and dV per kv head (0: a workgroup per tile), and the workspace.
 struct BackwardPlan {
-  int64_t slots_q, slots_k, shares, bytes, stats_bytes;
+  int64_t slots_q, slots_k, shares, bytes, cuts_at, partials_at;
 };
 
 BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
@@ -238,11 +238,11 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   // one slot more than tiles can need: the tokens behind the last sequence
   r.slots_q = tile_slots(f.total_q * group, f.batch, kDqRows, packed) + (packed ? 1 : 0);
   r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed);
-  r.stats_bytes = r.bytes = 8 * f.heads_q * f.total_q;
+  r.bytes = r.cuts_at = r.partials_at = 8 * f.heads_q * f.total_q;   // the statistics first
   r.shares = 0;
   // Equal shares cost the partial sums of the tiles cut and their join (256 KB
-  // per part at 128 columns; 28 us for 8192 tokens, 8 key heads).  With a
-  // causal mask they pay until there are many tiles per CU (that case: 420 us
+  // per part at 128 columns; 26 us for 8192 tokens, 8 key heads).  With a
+  // causal mask they pay until there are many tiles per CU (that case: 440 us
   // with the join, 769 a tile each); without one tiles differ little, and from
   // two per CU on a tile each is as good (16 key heads of 64, 600 tiles: 91
   // and 93 us).  Every workgroup walks the sequences' lengths to find its
@@ -261,8 +261,8 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
     // no more than the steps that there can be would fill
     const int64_t chunks = ceil_div(f.total_q, dkv_chunk(dc)) + f.batch;
     r.shares = clamp(r.slots_k * (chunks * group + kDkvFixed) / kDkvLeast, 1, r.shares);
-    r.stats_bytes = ceil_div(r.stats_bytes, 16) * 16;
-    r.bytes = r.stats_bytes + r.shares * f.heads_kv * 2 * 8 * dkv_keys(dc) * dc;
+    r.partials_at = ceil_div(r.cuts_at + r.shares * (int64_t)sizeof(DkvCut), 16) * 16;
+    r.bytes = r.partials_at + r.shares * f.heads_kv * 2 * 8 * dkv_keys(dc) * dc;
   }
   return r;
 }
@@ -509,7 +509,8 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.slots_q = (int)plan.slots_q;
   p.slots_k = (int)plan.slots_k;
   p.shares = (int)plan.shares;
-  p.partials = (float*)((char*)workspace + plan.stats_bytes);
+  p.cuts = (DkvCut*)((char*)workspace + plan.cuts_at);
+  p.partials = (float*)((char*)workspace + plan.partials_at);
   if (f.total_q > 0) {
     rc = run(dq_kernel(bf16, dc), plan.slots_q * p.heads_kv, &p, stream);
     if (rc) return rc;
@@ -519,7 +520,7 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
            stream);
   if (rc || plan.shares <= 1) return rc;
   return run(dkv_join_kernel(bf16, dc), plan.shares * (dkv_keys(dc) / 32) * p.heads_kv, &p, stream,
-             dkv_keys(dc), dkv_chunk(dc));
+             dkv_keys(dc));
 }
 
 int attention_prefix_plan(const mfl_attention_prefix_t* a, const void* q, const void* prefix_k,
