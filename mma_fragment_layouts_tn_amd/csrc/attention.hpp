@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2)
 // (the sequences' own keys, flat rows).  The prefix is bound by the matrix
 // pipe when many rows share it, the own keys by memory; side by side on a CU
 // each fills the other's waits.  64 tokens of 32/8 heads of 128 behind 8192
-// keys with up to 1000 own: 39 us, in two launches one after the other 55; 128
+// keys with up to 1000 own: 35 us, in two launches one after the other 55; 128
 // behind 32768 keys with 256 - 2048 own: 179 us, two launches 249 (740 MB of
 // keys and values, 4.1 TB/s of a large copy's 4.66, and 71 GFLOP).
 template <class T, int DC, bool TALL>

@@ -357,6 +357,14 @@ int plan_prefix(const mfl_attention_prefix_t& a, PrefixPlan& r) {
   };
   r.prefix.splits = a.splits_prefix ? a.splits_prefix : parts(r.prefix.slots, a.prefix, 128);
   r.own.splits = a.splits_own ? a.splits_own : parts(r.own.slots, a.capacity, 256);
+  // Half as many of the prefix where the own keys alone give two workgroups
+  // per CU, as long as none walks more than 4096 keys (64 sequences behind
+  // 8192 keys: 8 parts 40 us, 16 parts 48; 256 sequences: 2 and 4 parts 137 and
+  // 142; 128 behind 32768: 8 and 4 parts 172 and more than 205).
+  const int64_t half = r.prefix.splits / 2;
+  if (!a.splits_prefix && half > 0 && r.own.slots * a.heads_kv >= 2 * kFill && a.capacity > 0 &&
+      ceil_div(a.prefix, half) <= 4096)
+    r.prefix.splits = half;
   if (a.prefix == 0) r.prefix.splits = 0;
   if (a.capacity == 0) r.own.splits = a.prefix == 0 ? 1 : 0;
   if (!grid_fits(r.prefix, a.heads_kv) || !grid_fits(r.own, a.heads_kv) ||
