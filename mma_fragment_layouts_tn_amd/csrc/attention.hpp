@@ -1105,7 +1105,7 @@ __device__ __forceinline__ void join_row(const float* part_o, const float2* part
   if (lse && lane == 0) *lse = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// every row, one wave each
+// every row, one wave each: decoding behind a prefix, where each has its parts
 template <class T, int DC>
 __global__ void __launch_bounds__(256) attention_join(const CombineParams p) {
   const int64_t row = (int64_t)blockIdx.x * 4 + uniform(threadIdx.x >> 6);
@@ -1117,8 +1117,9 @@ __global__ void __launch_bounds__(256) attention_join(const CombineParams p) {
                   p.lse ? p.lse + row : nullptr);
 }
 
-// the rows of the tiles that took more than one split, one after the other
-// where a workgroup has `each` > 4 of them
+// The rows of the tiles that took more than one split, one after the other
+// where a workgroup has `each` > 4 of them.  Rows of no sequence are in no
+// tile: nothing is known of their parts, and nothing is written.
 template <class T, int DC>
 __global__ void __launch_bounds__(256) attention_join_tiles(const FwdParams p, int bm, int each) {
   int bid = blockIdx.x;

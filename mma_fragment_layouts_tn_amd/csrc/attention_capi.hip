@@ -141,6 +141,16 @@ bool grid_fits(const Choice& c, int64_t heads_kv) {
   return (__int128)c.slots * heads_kv * c.splits < INT_MAX;
 }
 
+// Rows per workgroup of the join by tiles: one per wave, or two where there
+// are more workgroups than are resident at a time (20,000 rows 15.4 and
+// 11.4 us, 3,000 rows 4 and 6).
+int join_rows(const Choice& c, int64_t heads_kv) {
+  return c.slots * (tile_rows(c.algo) / 4) * heads_kv > 16 * kFill ? 8 : 4;
+}
+int64_t join_blocks(const Choice& c, int64_t heads_kv) {
+  return c.slots * (tile_rows(c.algo) / join_rows(c, heads_kv)) * heads_kv;
+}
+
 int launch(KernelRef k, int64_t blocks, void** args, void* stream) {
   if (blocks == 0) return MFL_OK;
   const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
@@ -210,7 +220,8 @@ int plan_packed(const mfl_attention_t& a, bool packed, Choice& c, int64_t& bytes
   const int dc = dim_class(a.head_dim);
   c = choose(a.total_q * (a.heads_q / a.heads_kv), a.batch, packed, a.total_k, a.heads_kv, dc,
              a.algo, a.splits);
-  if (!grid_fits(c, a.heads_kv)) return MFL_E_TOO_LARGE;
+  if (!grid_fits(c, a.heads_kv) || (c.splits > 1 && join_blocks(c, a.heads_kv) >= INT_MAX))
+    return MFL_E_TOO_LARGE;
   bytes = partial_bytes(a.total_q * a.heads_q, c.splits, dc);
   return MFL_OK;
 }
@@ -441,13 +452,9 @@ int attention_packed(const mfl_attention_t* a, const void* q, const void* k, con
   if (c.splits > 1) place_partials(p, workspace, c.splits, dc);
   rc = run_forward(p, c, bf16, dc, stream);
   if (rc || c.splits == 1) return rc;
-  if (c.part_keys == 0) return run_join(p, (int)c.splits, bf16, dc, stream);
-  const int bm = tile_rows(c.algo);
-  // A row per wave, or two where there are more workgroups than are resident
-  // at a time: 20,000 rows 15.4 and 11.4 us, 3,000 rows 4 and 6.
-  const int64_t quads = c.slots * (bm / 4) * p.heads_kv;
-  const int each = quads > 16 * kFill ? 8 : 4;
-  return run(other_kernel(bf16, dc, kJoinTiles), quads / (each / 4), &p, stream, bm, each);
+  // by tiles: rows of no sequence have no partial sums and stay as they were
+  return run(other_kernel(bf16, dc, kJoinTiles), join_blocks(c, p.heads_kv), &p, stream,
+             tile_rows(c.algo), join_rows(c, p.heads_kv));
 }
 
 int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* dout,
