@@ -89,7 +89,10 @@ int attention_packed(const mfl_attention_t* a, const void* q, const void* k, con
                      const int32_t* seq_q, const int32_t* seq_k, void* out, float* lse,
                      void* workspace, int64_t workspace_bytes, void* stream);
 /* the same checks; on success the kernel, the splits and the workspace's size
- * (0: none needed).  Any out pointer may be NULL. */
+ * (0: none needed).  Any out pointer may be NULL.
+ * With dc = head_dim rounded up to 64, 128 or 256 the workspace of n > 1
+ * splits is n * total_q * heads_q * (4 dc + 8) bytes; for splits = 0 n is at
+ * most 64 and the workspace at most 256 MiB. */
 int attention_packed_plan(const mfl_attention_t* a, const void* q, const void* k, const void* v,
                           const int32_t* seq_q, const int32_t* seq_k, const void* out,
                           const float* lse, int32_t* algo, int32_t* splits,

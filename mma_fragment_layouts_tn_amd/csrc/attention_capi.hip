@@ -82,8 +82,16 @@ struct Choice {
   int64_t splits, slots, part_keys;
 };
 
+// one part's partial rows, and all of them
+int64_t plane_bytes(int64_t rows, int dc) { return rows * (4 * (int64_t)dc + 8); }
+int64_t partial_bytes(int64_t rows, int64_t splits, int dc) {
+  return splits > 1 ? splits * plane_bytes(rows, dc) : 0;
+}
+
 // Workgroups that occupy every CU.
 constexpr int64_t kFill = 256;
+// Partial rows at most, where the number of parts is chosen here.
+constexpr int64_t kPartialBytes = (int64_t)1 << 28;
 
 // Kernel and parts of packed attention.  The host knows the sums of the
 // lengths, not each one (they are on the device), so the rules go by means.
@@ -102,6 +110,14 @@ constexpr int64_t kFill = 256;
 // columns) or 6.4 ns (FLAT); partial rows are written and read at 4 TB/s, and
 // the launch that joins them takes 4 us.  64 tokens against 8192 keys: 150 us
 // in one part, 30 in 16; 1024 against 1024: 25 and 43 in two.
+//
+// A plane of partial rows per part: one sequence may have most of the keys, so
+// the planes are as many as all keys would take, up to 256 MiB (7 planes at
+// least; equal lengths take 2 - 4 where planes are that large), and a longer
+// sequence gets longer parts.  32 sequences of 32 tokens against 8192 keys:
+// 294 us with 15 planes, 338 with 64 (1.1 GB, and as many workgroups that find
+// nothing to do); 64 tokens against 65536 keys beside 15 times 64 against 256:
+// 177 with 15 and with 32, 377 with 4.
 Choice choose(int64_t rows, int64_t batch, bool packed, int64_t keys, int64_t heads_kv, int dc,
               int algo, int64_t splits) {
   Choice c;
@@ -119,22 +135,19 @@ Choice choose(int64_t rows, int64_t batch, bool packed, int64_t keys, int64_t he
     const int64_t tiles = ceil_div(rows, tile_rows(algo)),
                   wgs = (tiles > batch ? tiles : batch) * heads_kv,
                   least = algo == MFL_ATTENTION_FLAT ? 256 : 512;
-    if (wgs > 0 && wgs <= kFill) {
+    if (rows > 0 && wgs <= kFill) {
       const int64_t fair = ceil_div(mean_keys, 2 * kFill / wgs),
                     part = clamp(ceil_div(fair, 64) * 64, least, INT_MAX / 2),
                     saved = (mean_keys - part) * (algo == MFL_ATTENTION_FLAT ? 64 : 180) * dc / 1280,
                     bytes = ceil_div(mean_keys, part) * rows * heads_kv * dc * 8;
       if (saved > 4000 + bytes / 4000) {
         c.part_keys = part;
-        c.splits = clamp(ceil_div(keys, part), 1, 64);
+        c.splits = clamp(ceil_div(keys, part), 1,
+                         clamp(kPartialBytes / plane_bytes(rows * heads_kv, dc), 1, 64));
       }
     }
   }
   return c;
-}
-
-int64_t partial_bytes(int64_t rows, int64_t splits, int dc) {
-  return splits > 1 ? splits * rows * (4 * (int64_t)dc + 8) : 0;
 }
 
 bool grid_fits(const Choice& c, int64_t heads_kv) {
