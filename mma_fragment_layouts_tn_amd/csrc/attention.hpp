@@ -142,9 +142,9 @@ struct CombineParams {
 };
 
 // The tile that a share cut off at its end: first key, keys (0: none), the
-// last share that it went on in.
+// last share that it went on in, its number (attention_dkv).
 struct DkvCut {
-  int key, keys, last;
+  int key, keys, last, number;
 };
 
 struct BwdParams {
@@ -165,9 +165,9 @@ struct BwdParams {
   int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, o_tok, o_head, do_tok, do_head;
   int64_t dq_tok, dq_head, dk_tok, dk_head, dv_tok, dv_head;
   float scale, scale_log2;
-  // dK, dV: workgroups per kv head, 0: one per tile; sums of the tiles cut,
-  // two places per share and kv head, dK then dV of the keys of a tile
-  int shares;
+  // dK, dV: workgroups per kv head, 0: one per tile; sums of the tiles cut, a
+  // place per part and kv head (dkv_place), dK then dV of the keys of a tile
+  int shares, by_tile;
   DkvCut* cuts;               // one per share
   float* partials;
 };

@@ -307,9 +307,19 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, int lq, int lk
 // tiles of a kv head, in order (a tile's steps, and kDkvFixed more for its
 // loads and stores), are cut into p.shares ranges of `each`, one per
 // workgroup: 417 us, and 26 for the join.  Up to two tiles of a share are cut,
-// and their sums go to the workspace, the tile that began in an earlier share
-// to place 0, the one that goes on in the next to place 1; the latter is noted
-// in p.cuts, and attention_dkv_join adds its sums in order.
+// and their sums go to the workspace; the one that goes on in the next share is
+// noted in p.cuts, and attention_dkv_join adds its sums in order.
+//
+// Places.  A part is a share and a tile, and from each part to the next one or
+// both grow: with tiles numbered in order, share + number is another place
+// for each, shares + tiles - 1 in all.  Where there are more tiles than shares
+// it is two places per share (the tile that began in an earlier share, the
+// one that goes on in the next).  A tile's number is its slot (bwd_place): no
+// less than the tiles before it, less than slots_k whatever the offsets are.
+__device__ __forceinline__ int64_t dkv_place(const BwdParams& p, int share, int number,
+                                             bool began) {
+  return p.by_tile ? share + number : 2 * share + (began ? 1 : 0);
+}
 struct DkvUnits {
   int64_t n, r, c, group;   // chunks of rows; chunks per tile; chunks before the diagonal
   bool causal;
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
     each = dkv_each(total, p.shares);
     u = w * each;
     end = min(u + each, total);
-    if (kvh == 0 && threadIdx.x == 0) p.cuts[w] = DkvCut{0, 0, 0};
+    if (kvh == 0 && threadIdx.x == 0) p.cuts[w] = DkvCut{0, 0, 0, 0};
     if (u >= end) return;
     const DkvFound f = find_units(p, u, BN, RC);
     s = f.s;
@@ -798,10 +808,11 @@ __global__ void __launch_bounds__(64 * KW * RW) attention_dkv(const BwdParams p)
       first = uniform((int)max(u - a, (int64_t)0));
       steps = uniform((int)(min(max(end - a, (int64_t)0), (int64_t)all.steps) - first));
       mine = all.steps ? steps > 0 : u <= a - kDkvFixed;
-      part = p.partials + ((int64_t)(2 * w + (u <= a)) * p.heads_kv + kvh) * (2 * BN * DC);
+      const int number = at.k0 / BN + s + at.tile;
+      part = p.partials + (dkv_place(p, w, number, u <= a) * p.heads_kv + kvh) * (2 * BN * DC);
       if (u <= a && steps > 0 && steps < all.steps && kvh == 0 && threadIdx.x == 0)
         p.cuts[w] = DkvCut{at.k0 + at.tile * BN, min(BN, at.lk - at.tile * BN),
-                           (int)((a + all.steps - 1) / each)};
+                           (int)((a + all.steps - 1) / each), number};
       u = a + all.steps;
     }
     if (mine) dkv_tile<T, DC, KW, RW, KB>(p, smem, at, kvh, all, first, steps, part);
@@ -838,7 +849,8 @@ __global__ void __launch_bounds__(256) attention_dkv_join(const BwdParams p, int
       for (int j = 0; j < 4; ++j) {
         const int g = min(g0 + j, w1);
         const float* o = p.partials +
-                         ((int64_t)(2 * g + (g == w)) * p.heads_kv + kvh) * (2 * bn * DC) +
+                         (dkv_place(p, g, cut.number, g == w) * p.heads_kv + kvh) *
+                             (2 * bn * DC) +
                          key * DC + d;
         y[j][0] = *(const floatx4*)o;
         y[j][1] = *(const floatx4*)(o + 4);

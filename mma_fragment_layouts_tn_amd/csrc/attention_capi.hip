@@ -253,6 +253,7 @@ void place_partials(FwdParams& p, void* workspace, int64_t splits, int dc) {
 // Shares of dK and dV per kv head (0: a workgroup per tile), and the workspace.
 struct BackwardPlan {
   int64_t slots_q, slots_k, shares, bytes, cuts_at, partials_at;
+  bool by_tile;
 };
 
 BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
@@ -264,6 +265,7 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   r.slots_k = tile_slots(f.total_k, f.batch, dkv_keys(dc), packed);
   r.bytes = r.cuts_at = r.partials_at = 8 * f.heads_q * f.total_q;   // the statistics first
   r.shares = 0;
+  r.by_tile = false;
   // Equal shares cost the partial sums of the tiles cut and their join (256 KB
   // per part at 128 columns; 26 us for 8192 tokens, 8 key heads).  With a
   // causal mask they pay until there are many tiles per CU (that case: 440 us
@@ -273,12 +275,16 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
   // share, so not for more than 256 sequences.
   const int64_t tiles = r.slots_k * f.heads_kv;
   if (f.batch <= 256 && tiles < (f.causal ? 8 : 2) * kFill) {
-    // as many rounds of the chip, up to four, as leave the fewest CUs idle
+    // One round of the chip, or two to four if that leaves fewer CUs idle by
+    // more than a sixteenth of them: every share more is a cut more, a place
+    // in the workspace and sums to join.  dK, dV and dQ of 4096 tokens, 24
+    // query and 3 key heads of 128: 384 us in one round of 255 and 462 in three
+    // of 256; 40 and 20 heads 596 in one of 240, 735 in four of 255.
     int64_t best = 0;
     for (int64_t rounds = 1; rounds <= 4; ++rounds) {
-      const int64_t n = rounds * kFill / f.heads_kv;
-      if (n * f.heads_kv * 1024 / rounds > best) {
-        best = n * f.heads_kv * 1024 / rounds;
+      const int64_t n = rounds * kFill / f.heads_kv, busy = n * f.heads_kv * 1024 / rounds;
+      if (busy > best + (rounds > 1 ? kFill * 64 : 0)) {
+        best = busy;
         r.shares = n;
       }
     }
@@ -286,7 +292,10 @@ BackwardPlan plan_backward(const mfl_attention_t& f, bool packed) {
     const int64_t chunks = ceil_div(f.total_q, dkv_chunk(dc)) + f.batch;
     r.shares = clamp(r.slots_k * (chunks * group + kDkvFixed) / kDkvLeast, 1, r.shares);
     r.partials_at = ceil_div(r.cuts_at + r.shares * (int64_t)sizeof(DkvCut), 16) * 16;
-    r.bytes = r.partials_at + r.shares * f.heads_kv * 2 * 8 * dkv_keys(dc) * dc;
+    const int64_t numbered = r.shares + r.slots_k - 1;     // dkv_place
+    r.by_tile = numbered < 2 * r.shares;
+    r.bytes = r.partials_at +
+              (r.by_tile ? numbered : 2 * r.shares) * f.heads_kv * 8 * dkv_keys(dc) * dc;
   }
   return r;
 }
@@ -537,6 +546,7 @@ int attention_packed_backward(const mfl_attention_grad_t* a, const void* dout, c
   p.slots_q = (int)plan.slots_q;
   p.slots_k = (int)plan.slots_k;
   p.shares = (int)plan.shares;
+  p.by_tile = plan.by_tile;
   p.cuts = (DkvCut*)((char*)workspace + plan.cuts_at);
   p.partials = (float*)((char*)workspace + plan.partials_at);
   if (f.total_q > 0) {
