@@ -28,6 +28,13 @@
  * address (MFL_E_ALIAS).
  * head_dim is a multiple of 8 up to 256 (else MFL_E_UNSUPPORTED).
  *
+ * Sizes.  total_q * heads_q (batch * q_tokens * heads_q) is below 2^31 - 2^16,
+ * and no launch has 2^24 workgroups or more (else MFL_E_TOO_LARGE, before
+ * anything is launched): FLAT takes one per kv head, split and 16 rows (a
+ * sequence's last ones may be fewer), TALL and dQ per 128 rows, dK and dV per
+ * 128 or 256 keys, joining splits per 8 rows of a tile and per 4
+ * rows of the prefix form.
+ *
  * Packed sequences.  seq_q and seq_k hold batch + 1 offsets each in device
  * memory, the first of them 0, growing: sequence s owns query tokens
  * seq_q[s] .. seq_q[s+1] - 1 and keys seq_k[s] .. seq_k[s+1] - 1; lengths of

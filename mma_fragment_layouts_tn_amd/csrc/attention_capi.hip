@@ -150,8 +150,12 @@ Choice choose(int64_t rows, int64_t batch, bool packed, int64_t keys, int64_t he
   return c;
 }
 
+// Workgroups of a launch: every kernel here has 256 threads, and a launch has
+// fewer than 2^32.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
+
 bool grid_fits(const Choice& c, int64_t heads_kv) {
-  return (__int128)c.slots * heads_kv * c.splits < INT_MAX;
+  return (__int128)c.slots * heads_kv * c.splits <= kMaxBlocks;
 }
 
 // Rows per workgroup of the join by tiles: one per wave, or two where there
@@ -163,6 +167,8 @@ int join_rows(const Choice& c, int64_t heads_kv) {
 int64_t join_blocks(const Choice& c, int64_t heads_kv) {
   return c.slots * (tile_rows(c.algo) / join_rows(c, heads_kv)) * heads_kv;
 }
+
+constexpr int kJoinRows = 4;   // of the join of all rows: one per wave
 
 int launch(KernelRef k, int64_t blocks, void** args, void* stream) {
   if (blocks == 0) return MFL_OK;
@@ -201,7 +207,7 @@ int run_join(const FwdParams& p, int splits, bool bf16, int dc, void* stream) {
   j.o_batch = p.o_batch;
   j.o_tok = p.o_tok;
   j.o_head = p.o_head;
-  return run(other_kernel(bf16, dc, kJoin), ceil_div(p.rows, 4), &j, stream);
+  return run(other_kernel(bf16, dc, kJoin), ceil_div(p.rows, kJoinRows), &j, stream);
 }
 
 int check_packed(const mfl_attention_t& a, const void* q, const void* k, const void* v,
@@ -233,7 +239,7 @@ int plan_packed(const mfl_attention_t& a, bool packed, Choice& c, int64_t& bytes
   const int dc = dim_class(a.head_dim);
   c = choose(a.total_q * (a.heads_q / a.heads_kv), a.batch, packed, a.total_k, a.heads_kv, dc,
              a.algo, a.splits);
-  if (!grid_fits(c, a.heads_kv) || (c.splits > 1 && join_blocks(c, a.heads_kv) >= INT_MAX))
+  if (!grid_fits(c, a.heads_kv) || (c.splits > 1 && join_blocks(c, a.heads_kv) > kMaxBlocks))
     return MFL_E_TOO_LARGE;
   bytes = partial_bytes(a.total_q * a.heads_q, c.splits, dc);
   return MFL_OK;
@@ -334,7 +340,7 @@ int check_backward(const mfl_attention_grad_t& a, const void* dout, const void* 
   rc = check_output(f.head_dim, {f.total_k, a.dv_token}, {f.heads_kv, a.dv_head}, {1, 0});
   if (rc) return rc;
   const BackwardPlan r = plan_backward(f, seq_q != nullptr);
-  if (r.slots_q * f.heads_kv >= INT_MAX || r.slots_k * f.heads_kv >= INT_MAX)
+  if (r.slots_q * f.heads_kv > kMaxBlocks || r.slots_k * f.heads_kv > kMaxBlocks)
     return MFL_E_TOO_LARGE;
   return MFL_OK;
 }
@@ -401,8 +407,10 @@ int plan_prefix(const mfl_attention_prefix_t& a, PrefixPlan& r) {
   if (a.prefix == 0) r.prefix.splits = 0;
   if (a.capacity == 0) r.own.splits = a.prefix == 0 ? 1 : 0;
   if (!grid_fits(r.prefix, a.heads_kv) || !grid_fits(r.own, a.heads_kv) ||
-      (__int128)(r.prefix.slots * r.prefix.splits + r.own.slots * r.own.splits) * a.heads_kv >=
-          INT_MAX)
+      (__int128)(r.prefix.slots * r.prefix.splits + r.own.slots * r.own.splits) * a.heads_kv >
+          kMaxBlocks ||
+      (r.prefix.splits + r.own.splits > 1 &&
+       ceil_div(a.batch * a.q_tokens * a.heads_q, kJoinRows) > kMaxBlocks))
     return MFL_E_TOO_LARGE;
   r.bytes = partial_bytes(a.batch * a.q_tokens * a.heads_q, r.prefix.splits + r.own.splits, dc);
   return MFL_OK;
