@@ -45,9 +45,10 @@
  *
  * Values of keys outside a sequence never reach it, whatever they are.  A
  * key inside it whose v holds infinities or NaNs can make NaN of out in the
- * rows the causal mask hides it from: a weight of 0 times NaN.  In the
- * backward functions a score gradient is rounded to the inputs' type: in fp16
- * one beyond 65504 becomes infinite.
+ * rows the causal mask hides it from: a weight of 0 times NaN.  Likewise q, k,
+ * v and dout in the gradients of what they are hidden from.  In the backward
+ * functions a score gradient is rounded to the inputs' type: in fp16 one
+ * beyond 65504 becomes infinite.
  *
  * Ownership and execution are gemm_tn's (mfl_gemm.h): nothing is allocated,
  * kept or synchronised; work runs on `stream`.  A workspace belongs to one
@@ -73,7 +74,10 @@ extern "C" {
 /* Kernel of the forward functions: AUTO chooses by sizes.  TALL: four
  * waves of 32 rows (a row is a token of one query head) share each chunk of
  * keys; FLAT: 16 rows per workgroup, whose four waves take turns over the
- * keys. */
+ * keys.  The lengths are on the device, so AUTO and splits = 0 go by their
+ * means: for one long sequence among many short ones the caller does better
+ * to give both (TALL for a prompt among single tokens, splits for one
+ * sequence with most of the keys). */
 #define MFL_ATTENTION_AUTO 0
 #define MFL_ATTENTION_TALL 1
 #define MFL_ATTENTION_FLAT 2
@@ -137,7 +141,8 @@ int attention_packed_backward_plan(const mfl_attention_grad_t* a, const void* do
  * query token t of sequence b also sees the keys j <= lengths[b] - q_tokens + t
  * of its own cache k(b, j, g, d) = K[b * k_batch + j * k_token + g * k_head + d],
  * which holds lengths[b] keys (device memory, held inside [0, capacity]), the
- * new tokens' among them.  Prefix keys are read once for all sequences. */
+ * new tokens' among them.  Prefix keys are held and fetched once for all
+ * sequences' rows together, per tile of 128 rows of a kv head (16 in FLAT). */
 typedef struct {
   int32_t dtype;
   int32_t algo;                 /* of the prefix's part: AUTO, TALL or FLAT */

@@ -268,7 +268,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     log-sum-exp (tokens, heads) float32; a query without visible keys has out
     0 and -inf.  Rows behind the last sequence are not written.  No autograd
     graph is recorded: attention_backward gives the gradients.  algo and
-    splits choose the kernel and the parts its keys are split into."""
+    splits choose the kernel and the parts its keys are split into; by
+    themselves they follow the mean lengths, so for one long sequence among
+    many short ones it pays to give them."""
     if seq_k is None:
         seq_k = seq_q
     if out is not None:
@@ -348,8 +350,8 @@ def attention_prefix(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     prefix_v (prefix, kv heads, dim); k, v (batch, capacity, kv heads, dim):
     each sequence's own cache, of which lengths[b] (int32, on the device) keys
     are held, those of the new tokens last.  A new token sees the whole prefix
-    and its own sequence's keys up to itself.  The prefix is read once for the
-    whole batch.  Returns out of q's shape, with return_lse also the
+    and its own sequence's keys up to itself.  The prefix is read for the whole
+    batch together, per tile of rows.  Returns out of q's shape, with return_lse also the
     log-sum-exp (float32, q's shape without dim).  algo and splits choose the
     prefix's kernel and the parts the prefix and the caches are split into."""
     code = _dtype("q, the prefix, k and v", q, prefix_k, prefix_v, k, v)

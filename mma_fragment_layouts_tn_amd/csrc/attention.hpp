@@ -625,12 +625,16 @@ __device__ __forceinline__ void mask_keys(floatx16 (&st)[NB], int key0, int limi
 // workgroup per CU took 1 - 6 % longer on long prompts and 30 % on 2048 tokens
 // (62 against 49 us).
 //
-// Bound by the matrix pipe and what it may draw: 8192 causal tokens, 32/8
-// heads of 128, fp16, take 532 us (1,033 TFLOP/s; a large library product
-// reaches 1,470), and 420 - 450 with loads, LDS reads, exponentials and maxima
-// all taken out.  Scores formed one chunk ahead of their weights, so that a
-// wave's own matrix instructions cover its softmax, took 2 % longer (the
-// copies of the scores, one product more per tile); raised wave priority
+// Bound by matrix and vector instructions that take turns: 8192 causal tokens,
+// 32/8 heads of 128, fp16, take 556 us (989 TFLOP/s; a large library product
+// reaches 1,500).  The matrix pipe is busy for 58 % of the cycles, vector
+// instructions are issued in 52 %, both at once in 20 %.  The maximum over a
+// chunk and the first half of its weights run with no matrix instruction of
+// the wave in flight, and the second wave of the SIMD fills only some of it.
+// With loads, LDS reads, exponentials and maxima all taken out 419 us of 568
+// were left (one device).  Scores formed one chunk ahead of their weights, so
+// that a wave's own matrix instructions cover its softmax, took 2 % longer
+// (the copies of the scores, one product more per tile); raised wave priority
 // around the products, 4 slots of lead and alternating sums changed nothing.
 template <int DC>
 MFL_HD constexpr int tall_stages() {
@@ -826,7 +830,8 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_tall(const F
 // half a chunk in flight, no wave waits for another before the end, and two
 // workgroups fit a CU (DC <= 128).  The W partial rows are joined in LDS.
 // Bound by latency at few keys, by memory at many: one token of 32/8 heads of
-// 128 against 8192 keys takes 12.5 us in 16 parts, join included.
+// 128 against 8192 keys takes 6.9 us in 32 parts (7.9 in 16) and 4.4 - 6.8 to
+// join them.
 //
 // Lane l holds row l % 16; value v of the scores of keys 16 b .. 16 b + 15 is
 // key 16 b + 4 (l / 16) + v.  The second product's operand takes the values of
@@ -1026,8 +1031,10 @@ __global__ void __launch_bounds__(64 * kFlatWaves, DC == 256 ? 1 : 2)
 // pipe when many rows share it, the own keys by memory; side by side on a CU
 // each fills the other's waits.  64 tokens of 32/8 heads of 128 behind 8192
 // keys with up to 1000 own: 35 us, in two launches one after the other 55; 128
-// behind 32768 keys with 256 - 2048 own: 179 us, two launches 249 (740 MB of
-// keys and values, 4.1 TB/s of a large copy's 4.66, and 71 GFLOP).
+// behind 32768 keys with 256 - 2048 own: 181 us, two launches 249 (740 MB of
+// keys and values, 4.1 TB/s of a large copy's 4.77, and 71 GFLOP).  Every tile
+// of rows stages the whole prefix: those 128 tokens are four tiles of 128 rows
+// per kv head and read it four times, from the caches mostly.
 template <class T, int DC, bool TALL>
 __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2)
     attention_pair(const FwdParams a, const FwdParams b, int n0) {

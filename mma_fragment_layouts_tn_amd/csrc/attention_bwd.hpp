@@ -64,12 +64,17 @@ __device__ __forceinline__ void zero_rows(T* base, int64_t tok, int64_t head, in
 // Four waves of 32 rows each, as the forward kernel's tall form, over chunks of
 // 64 keys; also forms the rows' log-sum-exps in base 2 and deltas, which the
 // kernel of dK and dV reads.  delta is the fp32 sum over the 16-bit out, dS is
-// rounded to 16 bits as the third product's operand: together with the
-// results' own rounding the error of dQ and dK is 0.0027 of their norm (bf16).
+// rounded to 16 bits as the third product's operand.  Error of dQ and dK: 0.0027
+// of their norm (bf16; fp16 0.0003), where the results' own rounding alone is
+// 0.0017.  With an exact delta it would be 0.0024, with an unrounded dS 0.0021;
+// delta is exact only after all keys, too late for this kernel but for a fourth
+// product (P K), and dS in two halves is a fourth product as well.  In fp16 a
+// dS beyond 65504 is infinite.
 //
-// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 279 us, 1,016 TFLOP/s,
-// the matrix pipe busy for 55 % of the cycles.  Reads placed by the compiler,
-// one before each use: 315; 8 waves in one workgroup per CU 316.
+// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 278 us, 1,020 TFLOP/s,
+// the matrix pipe busy for 55 % of the cycles, vector instructions issued in
+// 40 %, both at once in 20 %.  Reads placed by the compiler, one before each
+// use: 315; 8 waves in one workgroup per CU 316.
 template <class T, int DC>
 __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const BwdParams p) {
   constexpr int W = 4, NST = tall_stages<DC>(), BM = 32 * W, CK = 64, KS = DC / 16, ND = DC / 32,
@@ -271,11 +276,13 @@ __global__ void __launch_bounds__(256, DC == 256 ? 1 : 2) attention_dq(const Bwd
 // scalar instructions per matrix instruction, and those, not the matrix pipe,
 // set their pace: 4,600 cycles for 2,048 of matrix work, here 3,600.
 //
-// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 417 us, 907 TFLOP/s,
-// the matrix pipe busy for 47 % of the cycles, a wave issuing for as many;
-// with one wave per SIMD what it waits for is not filled.  Reads 1, 3 or 4
-// slots ahead instead of 2 change nothing.  The join takes 26 us more, for
-// 137 MB of partial sums written and read.
+// 8192 tokens in 4 sequences, 32/8 heads of 128, bf16: 411 us, 920 TFLOP/s,
+// the matrix pipe busy for 47 % of the cycles, vector instructions issued in
+// 28 %, both at once in 12 %; with one wave per SIMD what it waits for is not
+// filled.  Reads 1, 3 or 4 slots ahead instead of 2 change nothing.  The join
+// takes 26 us more, for the partial sums written and read.  At 128 and 256
+// columns 65 and 81 registers are spilled (224 and 256 bytes per lane), all of
+// them around the steps of a tile, none in them.
 //
 // The chunks that the causal mask cuts come first, in a loop of their own: the
 // mask as a branch inside one loop made the compiler spill accumulators.
@@ -306,7 +313,7 @@ __device__ __forceinline__ DkvSteps dkv_steps(const BwdParams& p, int lq, int lk
 // tokens in 4 sequences where the CUs were busy for 286.  So the units of all
 // tiles of a kv head, in order (a tile's steps, and kDkvFixed more for its
 // loads and stores), are cut into p.shares ranges of `each`, one per
-// workgroup: 417 us, and 26 for the join.  Up to two tiles of a share are cut,
+// workgroup: 411 us, and 26 for the join.  Up to two tiles of a share are cut,
 // and their sums go to the workspace; the one that goes on in the next share is
 // noted in p.cuts, and attention_dkv_join adds its sums in order.
 //
