@@ -90,7 +90,7 @@ typedef struct {
   int64_t heads_q, heads_kv;    /* heads_q a multiple of heads_kv */
   int64_t head_dim;
   int64_t q_token, q_head, k_token, k_head, v_token, v_head, out_token, out_head;
-  float scale;                  /* > 0, finite */
+  float scale;                  /* > 0, scale * log2(e) finite */
   int32_t algo;                 /* MFL_ATTENTION_* */
   int32_t splits;               /* parts the keys are split into, 0: by sizes */
 } mfl_attention_t;

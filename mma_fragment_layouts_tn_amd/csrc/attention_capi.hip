@@ -64,7 +64,7 @@ int check_heads(int32_t dtype, int64_t batch, int64_t heads_q, int64_t heads_kv,
   if (dtype != MFL_F16 && dtype != MFL_BF16) return MFL_E_UNSUPPORTED;
   if (batch == 0 || heads_kv == 0 || heads_q == 0 || heads_q % heads_kv) return MFL_E_UNSUPPORTED;
   if (dim == 0 || dim % 8 || dim > 256) return MFL_E_UNSUPPORTED;
-  if (!(scale > 0.0f) || !isfinite(scale)) return MFL_E_UNSUPPORTED;
+  if (!(scale > 0.0f) || !isfinite(scale * kLog2e)) return MFL_E_UNSUPPORTED;
   if (heads_q > (1 << 16) || batch > (1 << 24)) return MFL_E_TOO_LARGE;
   return MFL_OK;
 }

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from mma_fragment_layouts_tn_amd import _attention as B
-from test_attention_api import GPTRS, LARGE, packed, plan, prefix, prefix_plan
+from test_attention_api import GPTRS, LARGE, UNSUP, packed, plan, prefix, prefix_plan
 
 FLAT, TALL = 2, 1
 
@@ -65,3 +65,10 @@ def test_prefix(kw, fits):
              prefix_v_token=8 * hk, prefix_v_head=8, k_token=8 * hk, k_head=8, v_token=8 * hk,
              v_head=8, k_batch=0, v_batch=0)
     assert prefix_plan(prefix(**dict(a, **kw)))[0] == (0 if fits else LARGE)
+
+
+@pytest.mark.parametrize("scale,code", [(2.3e38, 0), (2.4e38, UNSUP), (3.4e38, UNSUP)])
+def test_scale(scale, code):
+    """The kernels work in powers of two: scale * log2(e) has to be a number."""
+    assert plan(packed(scale=scale))[0] == code
+    assert prefix_plan(prefix(scale=scale))[0] == code
