@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the GEMM runs in the HIP kernels
 behind the C ABI declared in include/mfl_gemm.h, include/mfl_chain.h,
-include/mfl_attention.h, include/mfl_layout.h and include/mfl_probe.h.  PyTorch provides device memory and the current stream.
+include/mfl_attention.h, include/mfl_grouped.h, include/mfl_layout.h and
+include/mfl_probe.h.  PyTorch provides device memory and the current stream.
 There is no fallback: if the library is missing, importing this package
 raises.
 
@@ -20,10 +21,12 @@ from typing import Optional, Tuple
 import torch  # noqa: E402
 import numpy as np
 
-from . import _attention
+from . import _attention, _grouped
 from ._attention import (ATTENTION_ALGOS, BF16, AttentionArgs, AttentionGradArgs,  # noqa: F401
                          AttentionPrefixArgs, attention, attention_backward, attention_plan,
                          attention_prefix)
+from ._grouped import (GROUPED_ALGOS, combine_rows, combine_rows_backward,  # noqa: F401
+                       gemm_grouped, gemm_grouped_backward, gemm_grouped_plan, group_rows)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmfl_gemm.so")
@@ -260,6 +263,10 @@ def gemm_tn(A: torch.Tensor, B: torch.Tensor, C: Optional[torch.Tensor] = None,
 
 # ------------------------------------------------------------ attention
 _attention.bind(_lib, _check)   # attention, attention_backward, attention_prefix
+
+
+# ---------------------------------------------- products by groups of rows
+_grouped.bind(_lib, _check)     # group_rows, gemm_grouped, combine_rows, their gradients
 
 
 # ------------------------------------------------------- back-to-back GEMM

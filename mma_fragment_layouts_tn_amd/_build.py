@@ -24,7 +24,9 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["gemm_inst_256.hip", "gemm_inst_256w4.hip", "gemm_inst_128.hip",
            "gemm_inst_128w1.hip", "gemm_inst_splitk.hip", "gemm_inst_256w4x16.hip",
            "gemm_inst_256x16.hip", "gemm_inst_128x16.hip", "gemm_inst_splitk16.hip", "chain_inst.hip", "attention_fwd.hip",
-           "attention_bwd.hip", "attention_dkv.hip", "attention_capi.hip", "gemm_dispatch.hip", "probe_kernels.hip", "microbench.hip", "probe_dump.hip", "capi.cpp"]
+           "attention_bwd.hip", "attention_dkv.hip", "attention_capi.hip",
+           "grouped_rows.hip", "grouped_weights.hip", "grouped_few.hip", "grouped_capi.hip",
+           "gemm_dispatch.hip", "probe_kernels.hip", "microbench.hip", "probe_dump.hip", "capi.cpp"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-mcode-object-version=5",
@@ -104,7 +106,7 @@ def _blocks(lines):
 
 # sources whose kernels tie accumulators to other instructions by hand: every
 # matrix instruction is taken for one of them
-TIED_SOURCES = {"attention_dkv.hip"}
+TIED_SOURCES = {"attention_dkv.hip", "grouped_rows.hip", "grouped_weights.hip"}
 
 
 def check_mfma_fences(asm_text: str, where: str, tied=None, prefix=None) -> int:

@@ -1,0 +1,312 @@
+"""Binding of the products by groups of rows (include/mfl_grouped.h): the
+places of a list of choices, one product per group with its gradients, and
+the sum of a token's results.
+
+Checks of shapes and types, allocation of outputs and workspaces; every step
+of the operators runs in the HIP kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from ._attention import BF16, _dtype, _ptr, _Run
+
+GROUPED_ALGOS = {"auto": 0, "few": 1, "tile128": 2, "tile256": 3}
+_NAMES = {v: k for k, v in GROUPED_ALGOS.items()}
+_F32, _I32, _I64 = 2, 4, 5
+_TYPES = {torch.float16: 1, torch.float32: _F32, torch.bfloat16: BF16}
+
+_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+
+
+class GroupRowsArgs(ctypes.Structure):
+    """mfl_group_rows_t"""
+    _fields_ = [("ids_type", _i32)] + [(n, _i64) for n in ("count", "top", "groups")]
+
+
+class GroupedArgs(ctypes.Structure):
+    """mfl_grouped_t"""
+    _fields_ = [("dtype", _i32), ("out", _i32), ("algo", _i32)] + \
+        [(n, _i64) for n in ("groups", "places", "a_rows", "n", "k", "lda", "ldb", "b_group",
+                             "ldd")]
+
+
+class GroupedGradArgs(ctypes.Structure):
+    """mfl_grouped_grad_t"""
+    _fields_ = [("f", GroupedArgs)] + [(n, _i64) for n in ("ldda", "lddb", "db_group")]
+
+
+class CombineArgs(ctypes.Structure):
+    """mfl_combine_t"""
+    _fields_ = [("dtype", _i32), ("out", _i32)] + \
+        [(n, _i64) for n in ("tokens", "top", "n", "x_rows", "ldx", "ldo")]
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Argument types of the library's functions."""
+    P = ctypes.POINTER
+    lib.group_rows.argtypes = [P(GroupRowsArgs)] + [_vp] * 5 + [_i64, _vp]
+    lib.group_rows_plan.argtypes = [P(GroupRowsArgs)] + [_vp] * 4 + [P(_i64)]
+    lib.gemm_tn_grouped.argtypes = [P(GroupedArgs)] + [_vp] * 6
+    lib.gemm_tn_grouped_plan.argtypes = [P(GroupedArgs)] + [_vp] * 5 + [P(_i32)]
+    lib.gemm_tn_grouped_backward.argtypes = [P(GroupedGradArgs)] + [_vp] * 8
+    lib.gemm_tn_grouped_backward_plan.argtypes = [P(GroupedGradArgs)] + [_vp] * 7
+    lib.combine_rows.argtypes = [P(CombineArgs)] + [_vp] * 5
+    lib.combine_rows_backward.argtypes = [P(CombineArgs), _i64] + [_vp] * 8
+    for n in ("group_rows", "group_rows_plan", "gemm_tn_grouped", "gemm_tn_grouped_plan",
+              "gemm_tn_grouped_backward", "gemm_tn_grouped_backward_plan", "combine_rows",
+              "combine_rows_backward"):
+        getattr(lib, n).restype = ctypes.c_int
+
+
+_lib = None        # the loaded library and the caller's check of its codes
+_check = None
+
+
+def bind(lib: ctypes.CDLL, check) -> None:
+    """Give the functions below their library."""
+    global _lib, _check
+    declare(lib)
+    _lib, _check = lib, check
+
+
+# ---------------------------------------------------------------- marshalling
+def _call(run: _Run, fn, *args) -> None:
+    """fn, which takes no workspace, on the tensors' device."""
+    if torch.cuda.current_device() != run.device.index:
+        with torch.cuda.device(run.device):
+            rc = fn(*args, run.handle)
+    else:
+        rc = fn(*args, run.handle)
+    if rc:
+        _check(rc)
+
+
+def _matrix(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return t.stride(0) if r > 1 else c
+
+
+def _matrices(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """Row and matrix stride of a 3-D tensor with contiguous rows."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    g, r, c = t.shape
+    if c > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return (t.stride(1) if r > 1 else c), (t.stride(0) if g > 1 else 0)
+
+
+def _numbers(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) -> None:
+    if t is None:
+        return
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.dim() != 1 or (t.shape[0] > 1 and t.stride(0) != 1) or \
+            (count is not None and t.shape[0] != count):
+        raise ValueError(f"{name} must be contiguous" +
+                         ("" if count is None else f", of {count} entries"))
+
+
+def _type(dtype, given: torch.dtype, name: str) -> int:
+    """Code of an output's type: the operands' own or float32."""
+    dtype = given if dtype is None else dtype
+    if dtype not in (given, torch.float32):
+        raise TypeError(f"{name} must be of the operands' type or float32")
+    return _TYPES[dtype]
+
+
+def _grouped_args(A, B, offsets, rows, out: int, algo: str, places: int, ldd: int):
+    code = _dtype("A and B", A, B)
+    lda = _matrix(A, "A")
+    ldb, b_group = _matrices(B, "B")
+    groups, n, k = B.shape
+    if A.shape[1] != k:
+        raise ValueError("A and B disagree on K")
+    _numbers(offsets, "offsets", groups + 1)
+    _numbers(rows, "rows")
+    return GroupedArgs(code, out, GROUPED_ALGOS[algo], groups, places, A.shape[0], n, k, lda, ldb,
+                       b_group, ldd)
+
+
+# ------------------------------------------------------------------ functions
+def group_rows(ids: torch.Tensor, groups: int, *, stream=None):
+    """The rows of every group, from a list of choices, on the GPU.
+
+    ids (tokens,) or (tokens, top), int32 or int64, contiguous: the groups that
+    each token goes to, as a router's top-k or a batch's adapters; numbers
+    outside 0 .. groups - 1 are of no group.  Sorted by group, a group's
+    choices in their own order and those of no group behind, the choices take
+    places 0, 1, ...  Returns (int32, on the device)
+
+      rows     (tokens * top,)  the token of each place
+      offsets  (groups + 1,)    the first place of each group
+      slots    ids' shape       the place of each choice, -1 for no group
+
+    as gemm_grouped, combine_rows and gemm_adapters take them.  At most 4096
+    groups."""
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be int32 or int64")
+    if ids.dim() not in (1, 2):
+        raise ValueError("ids must be (tokens,) or (tokens, top)")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    top = ids.shape[1] if ids.dim() == 2 else 1
+    a = GroupRowsArgs(_I64 if ids.dtype == torch.int64 else _I32, ids.numel(), max(top, 1), groups)
+    run = _Run([ids], stream)
+    if groups < 1:
+        raise ValueError("there must be a group")
+    rows = run.empty((ids.numel(),), torch.int32)
+    offsets = run.empty((groups + 1,), torch.int32)
+    slots = run.empty(ids.shape, torch.int32)
+    ptrs = tuple(_ptr(t) for t in (ids, rows, offsets, slots))
+
+    def need():
+        n = _i64(0)
+        _check(_lib.group_rows_plan(a, *ptrs, n))
+        return n.value
+
+    run.call(_lib.group_rows, a, ptrs, need)
+    return rows, offsets, slots
+
+
+def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, *,
+                 rows: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                 D: Optional[torch.Tensor] = None, algo: str = "auto", stream=None):
+    """D[i] = A[rows[i]] @ B[g].T for every place i of group g, on the GPU.
+
+    A (M, K) and B (groups, N, K), float16 or bfloat16 with contiguous rows,
+    16-byte aligned, N and K multiples of 8.  offsets (groups + 1, int32, on
+    the device): group g owns the places offsets[g] .. offsets[g + 1] - 1.
+    rows (int32): the row of A at each place, gathered by the kernel; without
+    it place i is row i.  D (places, N) is of A's type, or float32 with
+    out_dtype; it is allocated when not given, and its rows of no group are
+    not written.  No autograd graph is recorded: gemm_grouped_backward gives
+    the gradients.  algo chooses the kernel; by itself it follows the mean
+    number of places per group."""
+    places = A.shape[0] if rows is None else rows.shape[0]
+    n = B.shape[1] if B.dim() == 3 else 0
+    if D is not None:
+        if D.shape != (places, n):
+            raise ValueError(f"D must have shape {(places, n)}")
+        if out_dtype is not None and out_dtype != D.dtype:
+            raise TypeError("D is not of out_dtype")
+        out_dtype = D.dtype
+    out = _type(out_dtype, A.dtype, "D")
+    a = _grouped_args(A, B, offsets, rows, out, algo, places, n if D is None else _matrix(D, "D"))
+    run = _Run([t for t in (A, B, offsets, rows, D) if t is not None], stream)
+    if D is None:
+        D = run.empty((places, n), A.dtype if out_dtype is None else out_dtype)
+    _call(run, _lib.gemm_tn_grouped, a, _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), _ptr(D))
+    return D
+
+
+def gemm_grouped_plan(A, B, offsets, *, rows=None, out_dtype=None, algo="auto") -> str:
+    """The kernel gemm_grouped() takes for these tensors; their data is not
+    read."""
+    places = A.shape[0] if rows is None else rows.shape[0]
+    a = _grouped_args(A, B, offsets, rows, _type(out_dtype, A.dtype, "D"), algo, places,
+                      B.shape[1])
+    al = _i32(0)
+    _check(_lib.gemm_tn_grouped_plan(a, _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), 1 << 40, al))
+    return _NAMES[al.value]
+
+
+def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                          offsets: torch.Tensor, *, rows: Optional[torch.Tensor] = None,
+                          dB_dtype: Optional[torch.dtype] = None, algo: str = "auto",
+                          stream=None):
+    """(dA, dB) of sum(D * dD) for gemm_grouped()'s arguments.
+
+    dA (places, K) has a row per place, 0 for those of no group; where rows
+    gathers, combine_rows(dA, slots) adds the rows of each token.  dB has B's
+    shape and type, or float32 with dB_dtype; 0 for groups without places.
+    The same arguments give the same bits."""
+    places = A.shape[0] if rows is None else rows.shape[0]
+    out = _type(dB_dtype, A.dtype, "dB")
+    if dD.dtype != A.dtype:
+        raise TypeError("dD must have A's dtype")
+    if B.dim() != 3 or dD.shape != (places, B.shape[1]):
+        raise ValueError("dD must be (places, N)")
+    f = _grouped_args(A, B, offsets, rows, out, algo, places, _matrix(dD, "dD"))
+    k, n = B.shape[2], B.shape[1]
+    a = GroupedGradArgs(f, k, k, n * k)
+    run = _Run([t for t in (dD, A, B, offsets, rows) if t is not None], stream)
+    dA = run.empty((places, k), A.dtype)
+    dB = run.empty(B.shape, A.dtype if dB_dtype is None else dB_dtype)
+    _call(run, _lib.gemm_tn_grouped_backward, a, _ptr(dD), _ptr(A), _ptr(B), _ptr(offsets),
+          _ptr(rows), _ptr(dA), _ptr(dB))
+    return dA, dB
+
+
+def _combine_args(X, slots, weights, out: int, ldo: int) -> CombineArgs:
+    code = _dtype("X", X)
+    if slots.dtype != torch.int32:
+        raise TypeError("slots must be int32")
+    if slots.dim() not in (1, 2) or not slots.is_contiguous():
+        raise ValueError("slots must be (tokens,) or (tokens, top), contiguous")
+    if weights is not None:
+        if weights.dtype != torch.float32:
+            raise TypeError("weights must be float32")
+        if weights.shape != slots.shape or not weights.is_contiguous():
+            raise ValueError("weights must have slots' shape, contiguous")
+    ldx = _matrix(X, "X")
+    top = slots.shape[1] if slots.dim() == 2 else 1
+    return CombineArgs(code, out, slots.shape[0], top, X.shape[1], X.shape[0], ldx, ldo)
+
+
+def combine_rows(X: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
+                 out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                 stream=None):
+    """out[t] = sum over j of weights[t, j] * X[slots[t, j]], on the GPU.
+
+    X (places, N), float16 or bfloat16 with contiguous rows, N a multiple of
+    8; slots (tokens,) or (tokens, top <= 64) int32, as group_rows gives them:
+    one outside X's rows adds nothing.  weights: slots' shape, float32; 1
+    without them.  out (tokens, N) is of X's type, or float32 with out_dtype.
+    Sums are float32, in the order of j."""
+    n = X.shape[1] if X.dim() == 2 else 0
+    if out is not None:
+        if out.shape != (slots.shape[0], n):
+            raise ValueError(f"out must have shape {(slots.shape[0], n)}")
+        if out_dtype is not None and out_dtype != out.dtype:
+            raise TypeError("out is not of out_dtype")
+        out_dtype = out.dtype
+    a = _combine_args(X, slots, weights, _type(out_dtype, X.dtype, "out"),
+                      n if out is None else _matrix(out, "out"))
+    run = _Run([t for t in (X, slots, weights, out) if t is not None], stream)
+    if out is None:
+        out = run.empty((slots.shape[0], n), X.dtype if out_dtype is None else out_dtype)
+    _call(run, _lib.combine_rows, a, _ptr(X), _ptr(slots), _ptr(weights), _ptr(out))
+    return out
+
+
+def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tensor,
+                          weights: Optional[torch.Tensor] = None, *, rows: torch.Tensor,
+                          stream=None):
+    """(dX, dweights) of sum(out * dout) for combine_rows()'s arguments.
+
+    rows (places,) int32: each place's token, as group_rows gives it with
+    slots.  dX has X's shape; a place that no choice of its token leads to has
+    gradient 0, and so has the weight of a choice without a place.  dweights is
+    None without weights."""
+    if dout.dtype != X.dtype:
+        raise TypeError("dout must have X's dtype")
+    if X.dim() != 2 or dout.shape != (slots.shape[0], X.shape[1]):
+        raise ValueError("dout must be (tokens, N)")
+    a = _combine_args(X, slots, weights, _TYPES.get(X.dtype, 0), _matrix(dout, "dout"))
+    _numbers(rows, "rows", X.shape[0])
+    run = _Run([t for t in (dout, X, slots, weights, rows) if t is not None], stream)
+    dX = run.empty(X.shape, X.dtype)
+    dw = None if weights is None else run.empty(weights.shape, torch.float32)
+    _call(run, _lib.combine_rows_backward, a, X.shape[1], _ptr(dout), _ptr(X), _ptr(slots),
+          _ptr(rows), _ptr(weights), _ptr(dX), _ptr(dw))
+    return dX, dw

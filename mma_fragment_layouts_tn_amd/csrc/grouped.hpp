@@ -1,0 +1,669 @@
+// Products whose weights are chosen per row: experts' layers (grouped by
+// expert, forward and both gradients) and low-rank adapters beside a shared
+// projection.
+//
+// Every kernel here computes, on a tile of m x n,
+//
+//   D(m, n) = sum_c Q(m, c) P(n, c)
+//
+// and issues the matrix instruction with P first, so that lane l's four
+// accumulators of an atom are four adjacent columns n = 4 (l / 16) + v of row
+// m = l % 16: results leave the registers as vectors along D's rows.
+//
+//            D                       Q                       P
+//   rows     D, a row per place      A rows (gathered), c=k  B[g], c = k
+//   dA       dA, a row per place     dD rows, c = n          B[g], c = n, transposed
+//   dB       dB[g], m = n, n = k     dD, c = place, transp.  A (gathered), c = place, transp.
+//
+// Transposed: the contraction is the strided direction in memory.  Such a
+// tile lies in LDS as it does in memory (a row per c) and its fragments come
+// from the transposing LDS read, so no operand is rearranged anywhere.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <type_traits>
+
+#include "attention.hpp"
+#include "grouped_launch.hpp"
+
+namespace mfl {
+namespace grp {
+
+using att::barrier;
+using att::BoolC;
+using att::Elem;
+using att::floatx4;
+using att::lds_c;
+using att::lds_s4;
+using att::lds_t;
+using att::shortx4;
+using att::Span;
+using att::span_of;
+using att::uniform;
+using att::Vec8;
+
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr unsigned kOutside = 0x80000000u;   // a lane's offset beyond any descriptor's range
+constexpr int kWhole = 0x7fffffff;
+
+// acc += P Q^T on one atom, the accumulator tied to one AGPR tuple (with the
+// builtin the compiler rotates a wave's tuples through copies in the loop).
+// It sees no hazards through the statement: two wait states ahead of it cover
+// operands assembled by vector instructions, settle() what follows the last.
+template <class T>
+struct Mma;
+template <>
+struct Mma<_Float16> {
+  static __device__ __forceinline__ void run(const Vec8<_Float16>& p, const Vec8<_Float16>& q,
+                                             floatx4& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
+  }
+};
+template <>
+struct Mma<__bf16> {
+  static __device__ __forceinline__ void run(const Vec8<__bf16>& p, const Vec8<__bf16>& q,
+                                             floatx4& c) {
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
+  }
+};
+
+// A tile of BM x BN by WM x WN waves, BC contraction elements per step, two
+// stages.  Each wave 16 RM x 64.
+template <int BM_, int BN_, int WM_, int WN_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BC = 64;
+  static constexpr int W = WM * WN, T = 64 * W;
+  static constexpr int RM = BM / WM / 16, RN = BN / WN / 16;
+  static constexpr int P_BYTES = BN * BC * 2, Q_BYTES = BM * BC * 2;
+  static constexpr int STAGE = P_BYTES + Q_BYTES;
+  static constexpr int NP = P_BYTES / 1024 / W, NQ = Q_BYTES / 1024 / W, NI = NP + NQ;
+  static_assert(RN == 4, "the order of P's rows in LDS is made for 64 columns per wave");
+  static_assert(NP * W * 1024 == P_BYTES && NQ * W * 1024 == Q_BYTES, "loads divide over waves");
+  static_assert(BM % 128 == 0 && BN % 128 == 0, "swizzle of transposed tiles");
+  static_assert(2 * STAGE <= 160 * 1024, "two stages fit LDS");
+};
+
+// 8 waves of 128 x 64, two per SIMD; 4 waves of 64 x 64, two workgroups per CU
+using Tile256 = Tile<256, 256, 2, 4>;
+using Tile128 = Tile<128, 128, 2, 2>;
+
+// P's rows in LDS (contraction contiguous): row 16 j + 4 q + v of a wave's 64
+// holds column 16 q + 4 j + v, so the four atoms' accumulators of a lane are
+// 16 adjacent columns.  Its own inverse.
+MFL_HD constexpr int perm64(int r) {
+  return (r & ~63) | ((r >> 2) & 3) << 4 | ((r >> 4) & 3) << 2 | (r & 3);
+}
+
+// ------------------------------------------------------- fragment reads
+// Contraction-contiguous tile, rows of 64 elements (lds_offset<64>): the
+// fragment of rows 16 i + l % 16, sub-step kk.
+template <class T>
+struct Straight {
+  unsigned at;
+  static __device__ __forceinline__ Straight of(int row0, int lane) {
+    const int r = lane & 15;
+    return Straight{2u * lds_offset<64>(row0 + r, 8 * (lane >> 4))};
+  }
+  __device__ __forceinline__ Vec8<T> read(lds_c stage, int i, int kk) const {
+    using ptr = const __attribute__((address_space(3))) Vec8<T>*;
+    return *(ptr)(stage + ((at ^ (64u * kk)) + 2048u * i));
+  }
+};
+constexpr bool straight_addresses_hold() {
+  for (int r = 0; r < 16; ++r)
+    for (int c = 0; c < 4; ++c)
+      for (int i = 0; i < 8; ++i)
+        for (int kk = 0; kk < 2; ++kk)
+          if (2 * lds_offset<64>(16 * i + r, 32 * kk + 8 * c) !=
+              ((2 * lds_offset<64>(r, 8 * c)) ^ (64 * kk)) + 2048 * i)
+            return false;
+  return true;
+}
+static_assert(straight_addresses_hold(), "sub-steps by XOR, atoms by offset");
+
+// Transposed tile, 64 rows (one per c) of R elements (lds_offset_mn<R>): two
+// reads of four rows each fill the fragment.
+template <class T, int R>
+struct Transposed {
+  unsigned at;
+  static __device__ __forceinline__ Transposed of(int row0, int lane) {
+    const int s = lane & 15, blk = lane >> 4;
+    return Transposed{2u * lds_offset_mn<R>(row0 + 4 * (s & 3), 8 * blk + (s >> 2))};
+  }
+  __device__ __forceinline__ Vec8<T> read(lds_c stage, int i, int kk) const {
+    const lds_c a = stage + ((at ^ (32u * i)) + 64u * R * kk);
+    const shortx4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)a);
+    const shortx4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(a + 8 * R));
+    return __builtin_bit_cast(Vec8<T>, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+};
+template <int R>
+constexpr bool transposed_addresses_hold() {
+  for (int row0 = 0; row0 < R; row0 += 64)
+    for (int s = 0; s < 4; ++s)
+      for (int k = 0; k < 32; ++k)
+        for (int i = 0; i < (R - row0 >= 128 && row0 % 128 == 0 ? 8 : 4); ++i)
+          for (int kk = 0; kk < 2; ++kk)
+            if (2 * lds_offset_mn<R>(row0 + 16 * i + 4 * s, 32 * kk + k) !=
+                ((2 * lds_offset_mn<R>(row0 + 4 * s, k)) ^ (32 * i)) + 64 * R * kk)
+              return false;
+  return true;
+}
+static_assert(transposed_addresses_hold<128>() && transposed_addresses_hold<256>(),
+              "atoms by XOR, sub-steps by offset");
+
+template <class T, int R, bool TR>
+struct ReaderOf {
+  using type = Straight<T>;
+};
+template <class T, int R>
+struct ReaderOf<T, R, true> {
+  using type = Transposed<T, R>;
+};
+
+// ------------------------------------------------------------ pipeline
+// `steps` steps of 64 contraction elements into acc.  issue(kt, i, stage)
+// sends load i (of the wave's NI) of step kt into the stage at `stage`;
+// ahead(kt) is called a step before the loads of step kt are issued.
+//
+// A step is two sub-steps of 32.  The first one's matrix instructions run
+// while the second one's fragments are read; then every wave has its loads of
+// the next step and is done with this stage (the barrier); the second one's
+// run while the next stage's first fragments are read and the loads of the
+// step after that go into this stage, one by one between the instructions.
+template <class T, class C, bool PT, bool QT, class Source>
+__device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
+                                        floatx4 (&acc)[C::RM][C::RN], int w, int lane) {
+  constexpr int RM = C::RM, RN = C::RN, NI = C::NI;
+  const typename ReaderOf<T, C::BN, PT>::type rp =
+      ReaderOf<T, C::BN, PT>::type::of((w / C::WM) * (C::BN / C::WN), lane);
+  const typename ReaderOf<T, C::BM, QT>::type rq =
+      ReaderOf<T, C::BM, QT>::type::of((w % C::WM) * (C::BM / C::WM), lane);
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  asm volatile("s_nop 4" ::);
+  if (steps > 0) {
+    Vec8<T> fp[2][RN], fq[2][RM];
+    // fragment read r in the order the instructions take them
+    auto read = [&](int r, int buf, int kk, lds_c stage) {
+      if (r == 0)
+        fq[buf][0] = rq.read(stage + C::P_BYTES, 0, kk);
+      else if (r <= RN)
+        fp[buf][r - 1] = rp.read(stage, r - 1, kk);
+      else
+        fq[buf][r - RN] = rq.read(stage + C::P_BYTES, r - RN, kk);
+    };
+    constexpr int kReads = RM + RN, kMma = RM * RN, kSlots = kMma / 2;
+    auto group = [&](int buf, auto reads, lds_c stage, auto loads, int kt, lds_c to) {
+#pragma unroll
+      for (int g = 0; g < kMma; ++g) {
+        if (C::W > 4) {           // two waves of the workgroup per SIMD take turns
+          if (g == 0) __builtin_amdgcn_s_setprio(1);
+          if (g == kMma / 2) __builtin_amdgcn_s_setprio(0);
+        }
+        Mma<T>::run(fp[buf][g % RN], fq[buf][g / RN], acc[g / RN][g % RN]);
+        if constexpr (decltype(reads)::value)
+          if (g < kSlots)
+#pragma unroll
+            for (int r = g * kReads / kSlots; r < (g + 1) * kReads / kSlots; ++r)
+              read(r, 1 - buf, 1 - buf, stage);
+        if constexpr (decltype(loads)::value)
+#pragma unroll
+          for (int i = g * NI / kMma; i < (g + 1) * NI / kMma; ++i) src.issue(kt, i, to);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using Yes = BoolC<true>;
+    using No = BoolC<false>;
+    // the stage read now, the next one, and where the loads go: distinct for
+    // the compiler, which otherwise lets every transposing read wait for them
+    auto step = [&](int kt, lds_c __restrict__ from, lds_c __restrict__ next,
+                    lds_c __restrict__ to, auto has_next, auto has_load) {
+      group(0, Yes(), from, No(), 0, to);
+      att::wait_vm<0>();
+      barrier();
+      group(1, has_next, next, has_load, kt + 2, to);
+      if constexpr (decltype(has_load)::value) src.ahead(kt + 3);
+    };
+    src.ahead(0);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) src.issue(0, i, ring);
+    src.ahead(1);
+    if (steps > 1) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) src.issue(1, i, ring + C::STAGE);
+      src.ahead(2);
+      att::wait_vm<NI + Source::kAhead>();
+    } else {
+      att::wait_vm<0>();
+    }
+    barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read(r, 0, 0, ring);
+    int kt = 0;
+    for (; kt + 2 < steps; ++kt) {
+      const lds_c a = ring + (kt & 1) * C::STAGE, b = ring + (1 - (kt & 1)) * C::STAGE;
+      step(kt, a, b, a, Yes(), Yes());
+    }
+    if (kt + 1 < steps) {
+      const lds_c a = ring + (kt & 1) * C::STAGE, b = ring + (1 - (kt & 1)) * C::STAGE;
+      step(kt, a, b, a, Yes(), No());
+      ++kt;
+    }
+    step(kt, ring + (kt & 1) * C::STAGE, ring, ring, No(), No());
+  }
+  att::settle();
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+// ---------------------------------------------------- where loads come from
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, lds_c to, unsigned lane_off,
+                                         int off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_t)to, 16, lane_off, off, 0, 0);
+}
+
+// R rows with the contraction contiguous, `k` elements of it: LDS run j holds
+// rows 8 j .. 8 j + 7.  at(row): byte offset of a row, or kOutside.
+template <int N>
+struct RowLoads {
+  __amdgpu_buffer_rsrc_t r;
+  unsigned off[N];
+  int col;           // of the even runs; 32 further or nearer in the odd ones
+  int k, run0;
+  template <class At>
+  __device__ __forceinline__ void init(const void* base, int k_, int w, int lane, At at) {
+    r = buffer(base, kWhole);
+    k = k_;
+    run0 = w * N;
+    col = 8 * ((lane & 7) ^ ((lane >> 4) & 3));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int row = 8 * (run0 + i) + (lane >> 3);
+      const unsigned x = at(row);
+      off[i] = x == kOutside ? x : x + 2u * column(i);
+    }
+  }
+  // (swz<8> of a row is its bits 1 - 3, bit 3 of them the run's parity)
+  __device__ __forceinline__ int column(int i) const { return col ^ (((run0 + i) & 1) * 32); }
+  __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    const unsigned x = column(i) < k - 64 * kt ? off[i] : kOutside;
+    load_lds(r, to + (run0 + i) * 1024, x, 128 * kt);
+  }
+};
+
+// A transposed tile of R columns from column col0 on (of `width`): LDS run j
+// holds 512 / R rows.
+template <int R, int N>
+struct ColumnLoads {
+  static constexpr int RUN = 512 / R, CPR = R / 8;
+  unsigned off[N];   // column's byte offset within a row, kOutside past the width
+  int row0;          // the lane's row within run 0 of the wave
+  int run0;
+  __device__ __forceinline__ void init(int col0, int width, int w, int lane) {
+    run0 = w * N;
+    row0 = RUN * run0 + lane / CPR;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = col0 + 8 * ((lane % CPR) ^ mn_swz(row0 + RUN * i));
+      off[i] = c < width ? 2u * c : kOutside;
+    }
+  }
+};
+
+// rows follow each other, `count` of them, `ld` elements apart
+template <int R, int N>
+struct PlainColumns : ColumnLoads<R, N> {
+  using Base = ColumnLoads<R, N>;
+  const char* base;
+  int64_t count;
+  int ld, width;
+  __device__ __forceinline__ void init(const void* b, int64_t n, int ld_, int col0, int width_,
+                                       int w, int lane) {
+    Base::init(col0, width_, w, lane);
+    base = (const char*)b;
+    count = n;
+    ld = ld_;
+    width = width_;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (this->off[i] != kOutside) this->off[i] += 2u * (this->row0 + Base::RUN * i) * ld;
+  }
+  __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    const int64_t left = count - 64 * (int64_t)kt;
+    const int rows = left < 64 ? (int)left : 64;
+    const __amdgpu_buffer_rsrc_t r = buffer(base + (int64_t)kt * 128 * ld,
+                                            rows > 0 ? 2 * ((rows - 1) * ld + width) : 0);
+    load_lds(r, to + (this->run0 + i) * 1024, this->off[i], 0);
+  }
+};
+
+// the rows index[0] .. index[count - 1] of `total` rows; a number outside
+// counts as a row of zeros
+template <int R, int N>
+struct GatheredColumns : ColumnLoads<R, N> {
+  using Base = ColumnLoads<R, N>;
+  __amdgpu_buffer_rsrc_t r, list;
+  int ld, total, count;
+  int next[N];       // indices of the step whose loads are issued next
+  __device__ __forceinline__ void init(const void* b, const int* index, int n, int ld_, int total_,
+                                       int col0, int width, int w, int lane) {
+    Base::init(col0, width, w, lane);
+    r = buffer(b, kWhole);
+    list = buffer(index, 4 * min(n, 1 << 28));
+    ld = ld_;
+    total = total_;
+    count = n;
+  }
+  __device__ __forceinline__ void ahead(int kt) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      next[i] = __builtin_amdgcn_raw_buffer_load_b32(
+          list, 4 * (64 * kt + this->row0 + Base::RUN * i), 0, 0);
+  }
+  __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    const int row = next[i];
+    const bool ok = 64 * kt + this->row0 + Base::RUN * i < count && (unsigned)row < (unsigned)total &&
+                    this->off[i] != kOutside;
+    unsigned x = 2u * row * ld + this->off[i];
+    asm volatile("" : "+v"(x));     // (else formed in a branch of its own)
+    load_lds(r, to + (this->run0 + i) * 1024, ok ? x : kOutside, 0);
+  }
+};
+
+// ---------------------------------------------------------- rows of groups
+// Tiles of `bm` places, none across two groups: slot of a tile as attention
+// finds those of its sequences.  The places behind the last group are a group
+// of their own.
+struct Place {
+  int group, first, count;    // the tile's first place, its places (<= bm)
+};
+__device__ __forceinline__ Place place_of(const GroupedParams& p, int slot, int bm) {
+  auto first = [&](int g) { return min(max(p.offsets[g], 0), p.places) / bm + g; };
+  const int g = att::find_sequence(p.groups + 1, slot, first);
+  const int a = min(max(p.offsets[g], 0), p.places),
+            b = g < p.groups ? min(max(p.offsets[g + 1], 0), p.places) : p.places;
+  const Span s{uniform(a), uniform(max(b - a, 0))};
+  const int t = slot - uniform(s.begin / bm + g);
+  Place r;
+  r.group = g;
+  r.first = s.begin + t * bm;
+  r.count = t < 0 ? 0 : min(s.len - t * bm, bm);
+  return r;
+}
+
+template <class O>
+struct Out;
+template <>
+struct Out<float> {
+  static __device__ __forceinline__ void store4(float* p, const floatx4& x) { *(floatx4*)p = x; }
+};
+template <class O>
+struct Out {
+  typedef O vec4 __attribute__((ext_vector_type(4)));
+  static __device__ __forceinline__ void store4(O* p, const floatx4& x) {
+    *(vec4*)p = vec4{(O)x[0], (O)x[1], (O)x[2], (O)x[3]};
+  }
+};
+
+// D's columns of a lane: atom j's four from column(j) on.
+template <bool PERM>
+__device__ __forceinline__ int column_of(int lane, int j) {
+  return PERM ? 16 * (lane >> 4) + 4 * j : 16 * j + 4 * (lane >> 4);
+}
+
+// the tile's rows (base + row ld) < rows and columns < width
+template <class O, class C, bool PERM>
+__device__ __forceinline__ void store_tile(O* base, int64_t ld, int rows, int col0, int width,
+                                           const floatx4 (&acc)[C::RM][C::RN], int w, int lane) {
+  const int wm = w % C::WM, wn = w / C::WM;
+#pragma unroll
+  for (int i = 0; i < C::RM; ++i) {
+    const int m = wm * (C::BM / C::WM) + 16 * i + (lane & 15);
+    if (m >= rows) continue;
+    O* row = base + (int64_t)m * ld;
+#pragma unroll
+    for (int j = 0; j < C::RN; ++j) {
+      const int n = col0 + wn * 64 + column_of<PERM>(lane, j);
+      if (n < width) Out<O>::store4(row + n, acc[i][j]);
+    }
+  }
+}
+
+template <class O, class C>
+__device__ __forceinline__ void zero_tile(O* base, int64_t ld, int rows, int col0, int width,
+                                          int tid) {
+  for (int x = tid; x < rows * (C::BN / 4); x += C::T) {
+    const int m = x / (C::BN / 4), n = col0 + 4 * (x % (C::BN / 4));
+    if (n < width) Out<O>::store4(base + (int64_t)m * ld + n, floatx4{0.0f, 0.0f, 0.0f, 0.0f});
+  }
+}
+
+template <class C, bool PT>
+struct RowsSource {
+  static constexpr int kAhead = 0;    // loads of ahead()
+  RowLoads<C::NQ> q;
+  typename std::conditional<PT, PlainColumns<C::BN, C::NP>, RowLoads<C::NP>>::type p;
+  __device__ __forceinline__ void ahead(int) {}
+  __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    if (i < C::NP)
+      p.issue(kt, i, to);
+    else
+      q.issue(kt, i - C::NP, to + C::P_BYTES);
+  }
+};
+
+// D = A B[g]^T (PT false) or dA = dD B[g] (PT true): a tile of places of one
+// group.
+template <class T, class O, class C, bool PT>
+__global__ void __launch_bounds__(C::T, 1) grouped_rows(const GroupedParams p) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
+  const Place at = place_of(p, ti.tm, C::BM);
+  if (at.count <= 0) return;
+  const int n0 = ti.tn * C::BN;
+  O* D = (O*)p.d + (int64_t)at.first * p.ldd;
+  if (at.group == p.groups) {       // of no group: no result, or no gradient
+    if constexpr (PT) zero_tile<O, C>(D, p.ldd, at.count, n0, p.n, tid);
+    return;
+  }
+  const T* P = (const T*)p.p + at.group * p.p_group;
+  RowsSource<C, PT> src;
+  if (p.rows)
+    src.q.init(p.q, p.k, w, lane, [&](int row) {
+      const int a = p.rows[at.first + min(row, at.count - 1)];
+      return row < at.count && (unsigned)a < (unsigned)p.q_rows ? 2u * (unsigned)a * p.ldq : kOutside;
+    });
+  else
+    src.q.init((const T*)p.q + (int64_t)at.first * p.ldq, p.k, w, lane, [&](int row) {
+      return row < at.count ? 2u * row * p.ldq : kOutside;
+    });
+  if constexpr (PT)
+    src.p.init(P, p.k, p.ldp, n0, p.n, w, lane);
+  else
+    src.p.init(P + (int64_t)n0 * p.ldp, p.k, w, lane, [&](int row) {
+      const int n = perm64(row);
+      return n0 + n < p.n ? 2u * n * p.ldp : kOutside;
+    });
+  floatx4 acc[C::RM][C::RN];
+  product<T, C, PT, false>((lds_c)smem, (p.k + 63) / 64, src, acc, w, lane);
+  store_tile<O, C, !PT>(D, p.ldd, at.count, n0, p.n, acc, w, lane);
+}
+
+template <class C, bool GATHER>
+struct WeightsSource {
+  static constexpr int kAhead = GATHER ? C::NP : 0;
+  typename std::conditional<GATHER, GatheredColumns<C::BN, C::NP>,
+                            PlainColumns<C::BN, C::NP>>::type p;
+  PlainColumns<C::BM, C::NQ> q;
+  __device__ __forceinline__ void ahead(int kt) {
+    if constexpr (GATHER) p.ahead(kt);
+  }
+  __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    if (i < C::NP)
+      p.issue(kt, i, to);
+    else
+      q.issue(kt, i - C::NP, to + C::P_BYTES);
+  }
+};
+
+// dB[g] = sum over the group's places of dD^T A: a tile of it.
+template <class T, class O, class C, bool GATHER>
+__global__ void __launch_bounds__(C::T, 1) grouped_weights(const GroupedParams p) {
+  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  // slots: tiles of one group's rows times groups
+  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
+  const int per = p.slots / p.groups, g = ti.tm / per;
+  const int m0 = (ti.tm - g * per) * C::BM, n0 = ti.tn * C::BN;
+  const Span s = span_of(p.offsets, g, p.places);
+  WeightsSource<C, GATHER> src;
+  if constexpr (GATHER)
+    src.p.init(p.p, p.rows + s.begin, s.len, p.ldp, p.p_rows, n0, p.n, w, lane);
+  else
+    src.p.init((const T*)p.p + (int64_t)s.begin * p.ldp, s.len, p.ldp, n0, p.n, w, lane);
+  src.q.init((const T*)p.q + (int64_t)s.begin * p.ldq, s.len, p.ldq, m0, p.m, w, lane);
+  floatx4 acc[C::RM][C::RN];
+  product<T, C, true, true>((lds_c)smem, (s.len + 63) / 64, src, acc, w, lane);
+  store_tile<O, C, false>((O*)p.d + g * p.d_group + (int64_t)m0 * p.ldd, p.ldd, p.m - m0, n0, p.n,
+                          acc, w, lane);
+}
+
+// ------------------------------------------------------------- few rows
+// Tiles of 16 RM places by 16 RN columns for groups of few rows, where the
+// weights' bytes are the work: no LDS stages, every fragment straight from
+// memory.  The workgroup's eight waves share the contraction, U sub-steps of
+// 32 a time (64 U consecutive bytes of each row per wave); their sums are
+// added through LDS in the order of the waves.
+constexpr int kFewWaves = 8, kFewDepth = 4;
+
+template <int RM, int RN>
+struct FewTile {
+  static constexpr int BM = 16 * RM, BN = 16 * RN, T = 64 * kFewWaves;
+};
+
+__device__ __forceinline__ att::Vec8<_Float16> as16(const u32x4_t& u, _Float16) {
+  return __builtin_bit_cast(att::Vec8<_Float16>, u);
+}
+__device__ __forceinline__ att::Vec8<__bf16> as16(const u32x4_t& u, __bf16) {
+  return __builtin_bit_cast(att::Vec8<__bf16>, u);
+}
+
+// q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
+// sums[(i RN + j) * 64 + lane] holds the four values of atom (i, j).
+template <class T, int RM, int RN>
+__device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const unsigned (&q_off)[RM],
+                                            __amdgpu_buffer_rsrc_t rp, const unsigned (&p_off)[RN],
+                                            int k, floatx4* sums, int w, int lane) {
+  constexpr int U = kFewDepth, W = kFewWaves;
+  floatx4 acc[RM][RN];
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  struct Part {
+    u32x4_t p[U][RN], q[U][RM];
+  };
+  auto load = [&](Part& x, int k0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = k0 + 32 * u + 8 * (lane >> 4) < k;
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+        x.p[u][j] = __builtin_amdgcn_raw_buffer_load_b128(
+            rp, in ? p_off[j] : kOutside, 2 * k0 + 64 * u, 0);
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+        x.q[u][i] = __builtin_amdgcn_raw_buffer_load_b128(
+            rq, in ? q_off[i] : kOutside, 2 * k0 + 64 * u, 0);
+    }
+  };
+  auto use = [&](const Part& x) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < RM; ++i)
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+          acc[i][j] = Elem<T>::mma16(as16(x.p[u][j], T()), as16(x.q[u][i], T()), acc[i][j]);
+  };
+  // two parts in turn, so that one is on its way while the other is used
+  Part a, b;
+  const int step = 32 * U * W;
+  int k0 = 32 * U * w;
+  if (k0 < k) {
+    load(a, k0);
+    for (; k0 + step < k; k0 += 2 * step) {
+      load(b, k0 + step);
+      use(a);
+      if (k0 + 2 * step < k) load(a, k0 + 2 * step);
+      use(b);
+    }
+    if (k0 < k) use(a);
+  }
+#pragma unroll
+  for (int i = 0; i < RM; ++i)
+#pragma unroll
+    for (int j = 0; j < RN; ++j) sums[((w * RM + i) * RN + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int x = threadIdx.x; x < RM * RN * 64; x += 64 * W) {
+    floatx4 t = sums[x];
+#pragma unroll
+    for (int v = 1; v < W; ++v) t += sums[v * RM * RN * 64 + x];
+    sums[x] = t;
+  }
+}
+
+// D = A B[g]^T, groups of few rows
+template <class T, class O, int RM, int RN>
+__global__ void __launch_bounds__(64 * kFewWaves, 1) grouped_few(const GroupedParams p) {
+  using F = FewTile<RM, RN>;
+  __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
+  const Place at = place_of(p, ti.tm, F::BM);
+  if (at.count <= 0 || at.group == p.groups) return;
+  const int n0 = ti.tn * F::BN, r = lane & 15;
+  unsigned q_off[RM], p_off[RN];
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int row = 16 * i + r;
+    if (p.rows) {
+      const int a = p.rows[at.first + min(row, at.count - 1)];
+      q_off[i] = row < at.count && (unsigned)a < (unsigned)p.q_rows
+                     ? 2u * (unsigned)a * p.ldq + 16u * (lane >> 4) : kOutside;
+    } else {
+      q_off[i] = row < at.count ? 2u * row * p.ldq + 16u * (lane >> 4) : kOutside;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RN; ++j)
+    p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + 16u * (lane >> 4) : kOutside;
+  few_product<T, RM, RN>(
+      buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
+      buffer((const T*)p.p + at.group * p.p_group + (int64_t)n0 * p.ldp, kWhole), p_off, p.k, sums,
+      w, lane);
+  // (a thread stores what it added itself)
+  for (int x = tid; x < RM * RN * 64; x += F::T) {
+    const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;
+    const int m = 16 * i + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
+    if (m < at.count && n < p.n)
+      Out<O>::store4((O*)p.d + (int64_t)(at.first + m) * p.ldd + n, sums[x]);
+  }
+}
+
+}  // namespace grp
+}  // namespace mfl

@@ -1,0 +1,389 @@
+// C ABI of the products by groups of rows (mfl_grouped.h): argument checks,
+// choice of kernel, launches.
+#include <hip/hip_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "../../include/mfl_grouped.h"
+#include "grouped_launch.hpp"
+
+namespace {
+
+using namespace mfl::grp;
+
+constexpr int64_t kMaxCount = (int64_t)INT_MAX - (1 << 16);
+constexpr int64_t kMaxExtent = (int64_t)1 << 21;     // n, k, strides between rows
+constexpr int64_t kMaxGroupStride = (int64_t)1 << 42;
+constexpr int64_t kMaxGather = ((int64_t)1 << 30) - 1;   // elements a gathered operand spans
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
+constexpr int64_t kFill = 256;     // workgroups that occupy every CU
+
+bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
+bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool half_type(int32_t t) { return t == MFL_F16 || t == MFL_BF16; }
+
+int launch(const KernelRef& k, int64_t blocks, void* params, void* stream) {
+  if (blocks == 0) return MFL_OK;
+  if (blocks > kMaxBlocks) return MFL_E_TOO_LARGE;
+  void* args[] = {params};
+  const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
+                                       (hipStream_t)stream);
+  return e == hipSuccess ? MFL_OK : MFL_E_LAUNCH;
+}
+
+// a stride between rows of `width` elements
+int check_stride(int64_t ld, int64_t width) {
+  if (ld < 0 || ld < width) return MFL_E_LEADING_DIM;
+  if (ld > kMaxExtent) return MFL_E_TOO_LARGE;
+  return ld % 8 ? MFL_E_MISALIGNED : MFL_OK;
+}
+// between the groups' matrices of rows x width elements; an output's do not overlap
+int check_group_stride(int64_t s, int64_t rows, int64_t ld, int64_t width, int64_t groups,
+                       bool output) {
+  if (s < 0) return MFL_E_LEADING_DIM;
+  if (s > kMaxGroupStride) return MFL_E_TOO_LARGE;
+  if (s % 8) return MFL_E_MISALIGNED;
+  if (output && groups > 1 && rows > 0 && s < (rows - 1) * ld + width) return MFL_E_ALIAS;
+  return MFL_OK;
+}
+
+int check_places(int64_t groups, int64_t places) {
+  if (groups < 0 || places < 0) return MFL_E_NEGATIVE_DIM;
+  if (groups == 0) return MFL_E_UNSUPPORTED;
+  if (groups > kMaxGroups || places > kMaxCount) return MFL_E_TOO_LARGE;
+  return MFL_OK;
+}
+
+int check_grouped(const mfl_grouped_t& a, const void* A, const void* B, const int32_t* offsets,
+                  const int32_t* rows, const void* D) {
+  if (a.a_rows < 0 || a.n < 0 || a.k < 0) return MFL_E_NEGATIVE_DIM;
+  int rc = check_places(a.groups, a.places);
+  if (rc) return rc;
+  if (!half_type(a.dtype) || (a.out != a.dtype && a.out != MFL_F32) || a.algo < MFL_GROUPED_AUTO ||
+      a.algo > MFL_GROUPED_TILE_256)
+    return MFL_E_UNSUPPORTED;
+  if (a.n == 0 || a.k == 0) return MFL_E_UNSUPPORTED;
+  if (a.a_rows > kMaxCount || a.n > kMaxExtent || a.k > kMaxExtent) return MFL_E_TOO_LARGE;
+  if (a.n % 8 || a.k % 8) return MFL_E_MISALIGNED;
+  if (!rows && a.a_rows < a.places) return MFL_E_UNSUPPORTED;
+  if (!offsets || !B || (a.places > 0 && (!A || !D))) return MFL_E_NULL_POINTER;
+  if ((rc = check_stride(a.lda, a.k)) || (rc = check_stride(a.ldb, a.k)) ||
+      (rc = check_stride(a.ldd, a.n)) ||
+      (rc = check_group_stride(a.b_group, a.n, a.ldb, a.k, a.groups, false)))
+    return rc;
+  if (rows && a.a_rows * a.lda > kMaxGather) return MFL_E_TOO_LARGE;
+  if (!aligned(A) || !aligned(B) || !aligned(D) || !aligned4(offsets) || !aligned4(rows))
+    return MFL_E_MISALIGNED;
+  if (D && (D == A || D == B)) return MFL_E_ALIAS;
+  return MFL_OK;
+}
+
+// slots of `bm`-place tiles over the groups and what is behind them
+int64_t tile_slots(int64_t places, int64_t groups, int64_t bm) { return places / bm + groups + 1; }
+
+struct Choice {
+  int algo;
+  KernelRef kernel;
+  int64_t slots, tiles_n;
+  int64_t blocks() const { return slots * tiles_n; }
+};
+
+Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
+  return {algo, k, tile_slots(a.places, a.groups, k.bm), ceil_div(n, k.bn)};
+}
+
+// Square tile for groups of `mean` rows.
+int square_tile(int64_t mean, int64_t places, int64_t n) {
+  return mean >= 192 && ceil_div(places, 256) * ceil_div(n, 256) >= 192 ? kTile256 : kTile128;
+}
+
+Choice choose(const mfl_grouped_t& a) {
+  const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
+  const int64_t mean = ceil_div(a.places, a.groups);
+  int algo = a.algo;
+  if (algo == kAuto) algo = mean <= 64 ? kFew : square_tile(mean, a.places, a.n);
+  if (algo != kFew) return with(rows_kernel(bf16, f32, algo), algo, a, a.n);
+  const int rm = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
+  const int64_t held = a.places < a.groups ? a.places : a.groups;
+  const int rn = held * ceil_div(a.n, 32) >= 2 * kFill ? 2 : 1;
+  return with(few_kernel(bf16, f32, rm, rn), algo, a, a.n);
+}
+
+// the walk over tiles: bands of this many slots (tile_of_block).  FEW: the
+// tiles of one group, which read the same weights, follow each other.
+int band_of(const Choice& c) {
+  return c.algo == kFew ? (int)c.slots : c.algo == kTile256 ? 4 : 8;
+}
+
+void place(GroupedParams& p, const Choice& c) {
+  p.slots = (int)c.slots;
+  p.tiles_n = (int)c.tiles_n;
+  p.band = band_of(c);
+}
+
+struct Backward {
+  Choice da, db;
+};
+Backward choose_backward(const mfl_grouped_t& f, bool gathered) {
+  const bool bf16 = f.dtype == MFL_BF16, f32 = f.out == MFL_F32;
+  const int64_t mean = ceil_div(f.places, f.groups);
+  Backward r;
+  const int a = f.algo ? f.algo : square_tile(mean, f.places, f.k);
+  r.da = with(input_grad_kernel(bf16, a), a, f, f.k);
+  const int b = f.algo ? f.algo
+                : f.groups * ceil_div(f.n, 256) * ceil_div(f.k, 256) >= 192 ? kTile256 : kTile128;
+  r.db.algo = b;
+  r.db.kernel = weight_grad_kernel(bf16, f32, b, gathered);
+  r.db.slots = f.groups * ceil_div(f.n, r.db.kernel.bm);
+  r.db.tiles_n = ceil_div(f.k, r.db.kernel.bn);
+  return r;
+}
+
+int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, const void* B,
+                   const int32_t* offsets, const int32_t* rows, const void* dA, const void* dB) {
+  const mfl_grouped_t& f = a.f;
+  int rc = check_grouped(f, A, B, offsets, rows, dD);
+  if (rc) return rc;
+  if (f.algo == MFL_GROUPED_FEW) return MFL_E_ALGO_CASE;
+  if ((rc = check_stride(a.ldda, f.k)) || (rc = check_stride(a.lddb, f.k)) ||
+      (rc = check_group_stride(a.db_group, f.n, a.lddb, f.k, f.groups, true)))
+    return rc;
+  if (!aligned(dA) || !aligned(dB)) return MFL_E_MISALIGNED;
+  const void* in[3] = {dD, A, B};
+  for (const void* x : in)
+    if ((dA && dA == x) || (dB && dB == x)) return MFL_E_ALIAS;
+  if (dA && dA == dB) return MFL_E_ALIAS;
+  const Backward r = choose_backward(f, rows != nullptr);
+  if (r.da.blocks() > kMaxBlocks || r.db.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  return MFL_OK;
+}
+
+struct SortPlan {
+  int64_t chunk, blocks, bytes;
+};
+SortPlan plan_sort(const mfl_group_rows_t& a) {
+  SortPlan r;
+  const int64_t per = ceil_div(a.count, 128);
+  r.chunk = ceil_div(a.count <= 4096 ? a.count : per > 4096 ? per : 4096, 512) * 512;
+  if (r.chunk == 0) r.chunk = 512;
+  r.blocks = a.count ? ceil_div(a.count, r.chunk) : 1;
+  r.bytes = r.blocks > 1 ? 4 * r.blocks * (a.groups + 1) : 0;
+  return r;
+}
+
+int check_sort(const mfl_group_rows_t& a, const void* ids, const int32_t* rows,
+               const int32_t* offsets, const int32_t* slots) {
+  if (a.top < 0) return MFL_E_NEGATIVE_DIM;
+  const int rc = check_places(a.groups, a.count);
+  if (rc) return rc;
+  if (a.ids_type != MFL_I32 && a.ids_type != MFL_I64) return MFL_E_UNSUPPORTED;
+  if (a.top == 0 || a.count % a.top) return MFL_E_UNSUPPORTED;
+  if (!offsets || (a.count > 0 && (!ids || !rows || !slots))) return MFL_E_NULL_POINTER;
+  if ((uintptr_t)ids % (a.ids_type == MFL_I64 ? 8 : 4) || !aligned4(rows) || !aligned4(offsets) ||
+      !aligned4(slots))
+    return MFL_E_MISALIGNED;
+  if (rows && (rows == ids || rows == offsets || rows == slots)) return MFL_E_ALIAS;
+  if (slots && (slots == ids || slots == offsets)) return MFL_E_ALIAS;
+  return offsets == ids ? MFL_E_ALIAS : MFL_OK;
+}
+
+int check_combine(const mfl_combine_t& a, const void* X, const int32_t* slots,
+                  const float* weights, const void* out) {
+  if (a.tokens < 0 || a.top < 0 || a.n < 0 || a.x_rows < 0) return MFL_E_NEGATIVE_DIM;
+  if (!half_type(a.dtype) || (a.out != a.dtype && a.out != MFL_F32)) return MFL_E_UNSUPPORTED;
+  if (a.n == 0 || a.top > 64) return MFL_E_UNSUPPORTED;
+  if (a.tokens > kMaxCount || a.x_rows > kMaxCount || a.tokens * a.top > kMaxCount ||
+      a.n > kMaxExtent)
+    return MFL_E_TOO_LARGE;
+  if (a.n % 8) return MFL_E_MISALIGNED;
+  if (a.tokens > 0 && (!out || (a.top > 0 && !slots))) return MFL_E_NULL_POINTER;
+  if (a.tokens > 0 && a.x_rows > 0 && !X) return MFL_E_NULL_POINTER;
+  int rc;
+  if ((rc = check_stride(a.ldx, a.n)) || (rc = check_stride(a.ldo, a.n))) return rc;
+  if (!aligned(X) || !aligned(out) || !aligned4(slots) || !aligned4(weights))
+    return MFL_E_MISALIGNED;
+  if (out && out == X) return MFL_E_ALIAS;
+  return ceil_div(a.tokens * (a.n / 8), 256) > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
+}
+
+CombineRows combine_params(const mfl_combine_t& a, const void* X, const int32_t* slots,
+                           const float* weights) {
+  CombineRows p{};
+  p.x = X;
+  p.slots = slots;
+  p.weights = weights;
+  p.tokens = a.tokens;
+  p.ldx = a.ldx;
+  p.ldo = a.ldo;
+  p.top = (int)a.top;
+  p.n = (int)a.n;
+  p.x_rows = (int)a.x_rows;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int group_rows_plan(const mfl_group_rows_t* a, const void* ids, const int32_t* rows,
+                    const int32_t* offsets, const int32_t* slots, int64_t* workspace_bytes) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_sort(*a, ids, rows, offsets, slots);
+  if (rc) return rc;
+  if (workspace_bytes) *workspace_bytes = plan_sort(*a).bytes;
+  return MFL_OK;
+}
+
+int group_rows(const mfl_group_rows_t* a, const void* ids, int32_t* rows, int32_t* offsets,
+               int32_t* slots, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_sort(*a, ids, rows, offsets, slots);
+  if (rc) return rc;
+  const SortPlan plan = plan_sort(*a);
+  if (plan.bytes > 0 && (!workspace || !aligned(workspace) || workspace_bytes < plan.bytes))
+    return MFL_E_WORKSPACE;
+  SortParams p{};
+  p.ids = ids;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.slots = slots;
+  p.table = (int*)workspace;
+  p.count = a->count;
+  p.chunk = plan.chunk;
+  p.top = (int)a->top;
+  p.groups = (int)a->groups;
+  while (p.groups >> p.bits) ++p.bits;
+  const bool i64 = a->ids_type == MFL_I64;
+  if (plan.blocks > 1 && (rc = launch(count_kernel(i64, p.groups), plan.blocks, &p, stream)))
+    return rc;
+  return launch(place_kernel(i64, p.groups), plan.blocks, &p, stream);
+}
+
+int gemm_tn_grouped_plan(const mfl_grouped_t* a, const void* A, const void* B,
+                         const int32_t* offsets, const int32_t* rows, const void* D,
+                         int32_t* algo) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_grouped(*a, A, B, offsets, rows, D);
+  if (rc) return rc;
+  const Choice c = choose(*a);
+  if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (algo) *algo = c.algo;
+  return MFL_OK;
+}
+
+int gemm_tn_grouped(const mfl_grouped_t* a, const void* A, const void* B, const int32_t* offsets,
+                    const int32_t* rows, void* D, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_grouped(*a, A, B, offsets, rows, D);
+  if (rc) return rc;
+  const Choice c = choose(*a);
+  if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (a->places == 0) return MFL_OK;
+  GroupedParams p{};
+  p.p = B;
+  p.q = A;
+  p.d = D;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.groups = (int)a->groups;
+  p.places = (int)a->places;
+  p.n = (int)a->n;
+  p.k = (int)a->k;
+  p.ldp = (int)a->ldb;
+  p.ldq = (int)a->lda;
+  p.ldd = (int)a->ldd;
+  p.q_rows = (int)a->a_rows;
+  p.p_group = a->b_group;
+  place(p, c);
+  return launch(c.kernel, c.blocks(), &p, stream);
+}
+
+int gemm_tn_grouped_backward_plan(const mfl_grouped_grad_t* a, const void* dD, const void* A,
+                                  const void* B, const int32_t* offsets, const int32_t* rows,
+                                  const void* dA, const void* dB) {
+  if (!a) return MFL_E_NULL_POINTER;
+  return check_backward(*a, dD, A, B, offsets, rows, dA, dB);
+}
+
+int gemm_tn_grouped_backward(const mfl_grouped_grad_t* a, const void* dD, const void* A,
+                             const void* B, const int32_t* offsets, const int32_t* rows, void* dA,
+                             void* dB, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_backward(*a, dD, A, B, offsets, rows, dA, dB);
+  if (rc) return rc;
+  const mfl_grouped_t& f = a->f;
+  const Backward r = choose_backward(f, rows != nullptr);
+  GroupedParams p{};
+  p.offsets = offsets;
+  p.groups = (int)f.groups;
+  p.places = (int)f.places;
+  if (dA && f.places > 0) {
+    GroupedParams x = p;
+    x.p = B;
+    x.q = dD;
+    x.d = dA;
+    x.n = (int)f.k;
+    x.k = (int)f.n;
+    x.ldp = (int)f.ldb;
+    x.ldq = (int)f.ldd;
+    x.ldd = (int)a->ldda;
+    x.p_group = f.b_group;
+    place(x, r.da);
+    rc = launch(r.da.kernel, r.da.blocks(), &x, stream);
+    if (rc) return rc;
+  }
+  if (!dB) return MFL_OK;
+  p.p = A;
+  p.q = dD;
+  p.d = dB;
+  p.rows = rows;
+  p.m = (int)f.n;
+  p.n = (int)f.k;
+  p.ldp = (int)f.lda;
+  p.ldq = (int)f.ldd;
+  p.ldd = (int)a->lddb;
+  p.p_rows = (int)f.a_rows;
+  p.d_group = a->db_group;
+  place(p, r.db);
+  return launch(r.db.kernel, r.db.blocks(), &p, stream);
+}
+
+int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,
+                 const float* weights, void* out, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_combine(*a, X, slots, weights, out);
+  if (rc) return rc;
+  CombineRows p = combine_params(*a, X, slots, weights);
+  p.out = out;
+  return launch(combine_kernel(a->dtype == MFL_BF16, a->out == MFL_F32),
+                ceil_div(a->tokens * (a->n / 8), 256), &p, stream);
+}
+
+int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout, const void* X,
+                          const int32_t* slots, const int32_t* rows, const float* weights,
+                          void* dX, float* dw, void* stream) {
+  if (!a) return MFL_E_NULL_POINTER;
+  int rc = check_combine(*a, X, slots, weights, dout);
+  if (rc) return rc;
+  if (a->out != a->dtype) return MFL_E_UNSUPPORTED;
+  if (a->x_rows > 0 && (!rows || !dX)) return MFL_E_NULL_POINTER;
+  if (dw && !weights) return MFL_E_UNSUPPORTED;
+  rc = check_stride(lddx, a->n);
+  if (rc) return rc;
+  if (!aligned(dX) || !aligned4(rows) || !aligned4(dw)) return MFL_E_MISALIGNED;
+  if (dX && (dX == X || dX == dout)) return MFL_E_ALIAS;
+  if (dw && dw == weights) return MFL_E_ALIAS;
+  CombineRows p = combine_params(*a, X, slots, weights);
+  p.dout = dout;
+  p.rows = rows;
+  p.dx = dX;
+  p.dw = dw;
+  p.lddx = lddx;
+  const int64_t choices = a->tokens * a->top, waves = a->x_rows > choices ? a->x_rows : choices;
+  return launch(combine_grad_kernel(a->dtype == MFL_BF16), ceil_div(waves, 4), &p, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,66 @@
+// Kernel arguments and instances of the products by groups of rows.
+#pragma once
+
+#include <stdint.h>
+
+namespace mfl {
+namespace grp {
+
+// D(m, n) = sum_c Q(m, c) P(n, c), see grouped.hpp.  Strides in elements.
+struct GroupedParams {
+  const void* p;
+  const void* q;
+  void* d;
+  const int* offsets;          // groups + 1 places
+  const int* rows;             // row of each place, or null
+  int groups, places;
+  int m, n, k;                 // extents; m or k is the group's places
+  int ldp, ldq, ldd;
+  int p_rows, q_rows;          // rows that a gathered operand has
+  int slots, tiles_n, band;    // tiles along m (of all groups), along n; order
+  int64_t p_group, d_group;
+};
+
+struct SortParams {
+  const void* ids;
+  int* rows;
+  int* offsets;
+  int* slots;
+  int* table;                  // choices of each group in each chunk
+  int64_t count, chunk;
+  int top, groups, bits;       // bits: of the numbers 0 .. groups
+};
+
+struct CombineRows {
+  const void* x;
+  const void* dout;
+  const int* slots;
+  const int* rows;
+  const float* weights;
+  void* out;
+  void* dx;
+  float* dw;
+  int64_t tokens, ldx, ldo, lddx;
+  int top, n, x_rows;
+};
+
+constexpr int kMaxGroups = 4096;
+
+struct KernelRef {
+  const void* fn;
+  int threads, bm, bn;
+};
+
+// kernels by type and size of tile, each in a source of its own
+enum Algo { kAuto, kFew, kTile128, kTile256 };
+KernelRef rows_kernel(bool bf16, bool f32, int algo);                   // D
+KernelRef few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
+KernelRef input_grad_kernel(bool bf16, int algo);                       // dA
+KernelRef weight_grad_kernel(bool bf16, bool f32, int algo, bool gathered);   // dB
+KernelRef count_kernel(bool i64, int groups);
+KernelRef place_kernel(bool i64, int groups);
+KernelRef combine_kernel(bool bf16, bool f32);
+KernelRef combine_grad_kernel(bool bf16);
+
+}  // namespace grp
+}  // namespace mfl

@@ -1,0 +1,29 @@
+// Kernels of the gradients of the groups' matrices: their sums are tied by
+// hand, and the build checks every access to them in the generated code.
+#include <hip/hip_runtime.h>
+
+#include "grouped.hpp"
+
+namespace mfl {
+namespace grp {
+namespace {
+template <class T, class O, class C>
+KernelRef ref(bool gathered) {
+  return {gathered ? (const void*)grouped_weights<T, O, C, true>
+                   : (const void*)grouped_weights<T, O, C, false>,
+          C::T, C::BM, C::BN};
+}
+template <class T, class O>
+KernelRef by_tile(int algo, bool gathered) {
+  return algo == kTile256 ? ref<T, O, Tile256>(gathered) : ref<T, O, Tile128>(gathered);
+}
+}  // namespace
+
+KernelRef weight_grad_kernel(bool bf16, bool f32, int algo, bool gathered) {
+  if (f32)
+    return bf16 ? by_tile<__bf16, float>(algo, gathered) : by_tile<_Float16, float>(algo, gathered);
+  return bf16 ? by_tile<__bf16, __bf16>(algo, gathered)
+              : by_tile<_Float16, _Float16>(algo, gathered);
+}
+}  // namespace grp
+}  // namespace mfl
