@@ -7,6 +7,8 @@
  *   group_rows        places: the choices in the order of their groups
  *   gemm_tn_grouped   D(i, n) = sum_k A(r_i, k) B(g, n, k)   for every place i of group g
  *   combine_rows      out(t, c) = sum_j w(t, j) X(slot(t, j), c)
+ *   gemm_tn_adapters  D(r, n) = sum_k x(r, k) W(n, k) + the low-rank term of the
+ *                     group that row r's place belongs to
  *
  * Places.  offsets holds groups + 1 numbers in device memory, the first of
  * them 0, growing: group g owns the places offsets[g] .. offsets[g + 1] - 1;
@@ -23,7 +25,7 @@
  * n ldb + k], D(i, n) = D[i ldd + n].  n, k and every stride are multiples of
  * 8 and every matrix is 16-byte aligned (else MFL_E_MISALIGNED); strides reach
  * past a row (MFL_E_LEADING_DIM); n, k and the strides between rows are at
- * most 2^21, and where rows are gathered A spans less than 2 GiB
+ * most 2^21, and where rows are gathered A (x) spans less than 2 GiB
  * (MFL_E_TOO_LARGE).  At most 4096 groups.
  *
  * Values of one group's rows and of its matrix never reach another group's
@@ -140,6 +142,39 @@ int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,
 int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout, const void* X,
                           const int32_t* slots, const int32_t* rows, const float* weights,
                           void* dX, float* dw, void* stream);
+
+/* A shared projection with low-rank adapters, every place i of group g:
+ *   D(r_i, n) = sum_k x(r_i, k) W(n, k) + s_g sum_j h(i, j) B(g, n, j)
+ *   h(i, j)   = sum_k x(r_i, k) A(g, j, k),  j < rank
+ * and for places of no group the first sum alone.  scale holds s (fp32, one
+ * per group), NULL for 1.  x, W, A and B are all MFL_F16 or all MFL_BF16, D
+ * also MFL_F32.  rank is a multiple of 8.
+ *
+ * rows holds each row of x and D at most once, NULL: places are rows; rows of
+ * D that no place leads to stay as they were.  s_g h is held to fp32's
+ * accuracy (in fp16, beyond 65504 it becomes infinite), sums are fp32, D is
+ * rounded once.  The values of an adapter reach its own rows alone, whatever
+ * they are.
+ *
+ * Kernels as above: FEW adds the low-rank terms row by row, the TILEs by runs
+ * of one group.  The workspace: 4 bytes per place, up to 16 for alignment, and
+ * places x rank numbers of 4 bytes (6 for TILE with an fp32 D). */
+typedef struct {
+  int32_t dtype, out, algo;
+  int64_t groups, places;
+  int64_t x_rows;              /* rows of x and D; at least places if rows is NULL */
+  int64_t n, k, rank;
+  int64_t ldx, ldw, lda, a_group, ldb, b_group, ldd;
+} mfl_adapters_t;
+
+int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, const void* A,
+                     const void* B, const int32_t* offsets, const int32_t* rows,
+                     const float* scale, void* D, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W, const void* A,
+                          const void* B, const int32_t* offsets, const int32_t* rows,
+                          const float* scale, const void* D, int32_t* algo,
+                          int64_t* workspace_bytes);
 
 #ifdef __cplusplus
 }

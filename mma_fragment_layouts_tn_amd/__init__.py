@@ -26,7 +26,8 @@ from ._attention import (ATTENTION_ALGOS, BF16, AttentionArgs, AttentionGradArgs
                          AttentionPrefixArgs, attention, attention_backward, attention_plan,
                          attention_prefix)
 from ._grouped import (GROUPED_ALGOS, combine_rows, combine_rows_backward,  # noqa: F401
-                       gemm_grouped, gemm_grouped_backward, gemm_grouped_plan, group_rows)
+                       gemm_adapters, gemm_adapters_plan, gemm_grouped, gemm_grouped_backward,
+                       gemm_grouped_plan, group_rows)
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmfl_gemm.so")
@@ -266,7 +267,7 @@ _attention.bind(_lib, _check)   # attention, attention_backward, attention_prefi
 
 
 # ---------------------------------------------- products by groups of rows
-_grouped.bind(_lib, _check)     # group_rows, gemm_grouped, combine_rows, their gradients
+_grouped.bind(_lib, _check)     # group_rows, gemm_grouped, combine_rows, gemm_adapters
 
 
 # ------------------------------------------------------- back-to-back GEMM

@@ -1,6 +1,6 @@
 """Binding of the products by groups of rows (include/mfl_grouped.h): the
-places of a list of choices, one product per group with its gradients, and
-the sum of a token's results.
+places of a list of choices, one product per group with its gradients, the sum
+of a token's results, and adapters beside a shared projection.
 
 Checks of shapes and types, allocation of outputs and workspaces; every step
 of the operators runs in the HIP kernels.
@@ -45,6 +45,13 @@ class CombineArgs(ctypes.Structure):
         [(n, _i64) for n in ("tokens", "top", "n", "x_rows", "ldx", "ldo")]
 
 
+class AdaptersArgs(ctypes.Structure):
+    """mfl_adapters_t"""
+    _fields_ = [("dtype", _i32), ("out", _i32), ("algo", _i32)] + \
+        [(n, _i64) for n in ("groups", "places", "x_rows", "n", "k", "rank", "ldx", "ldw", "lda",
+                             "a_group", "ldb", "b_group", "ldd")]
+
+
 def declare(lib: ctypes.CDLL) -> None:
     """Argument types of the library's functions."""
     P = ctypes.POINTER
@@ -56,7 +63,9 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.gemm_tn_grouped_backward_plan.argtypes = [P(GroupedGradArgs)] + [_vp] * 7
     lib.combine_rows.argtypes = [P(CombineArgs)] + [_vp] * 5
     lib.combine_rows_backward.argtypes = [P(CombineArgs), _i64] + [_vp] * 8
-    for n in ("group_rows", "group_rows_plan", "gemm_tn_grouped", "gemm_tn_grouped_plan",
+    lib.gemm_tn_adapters.argtypes = [P(AdaptersArgs)] + [_vp] * 9 + [_i64, _vp]
+    lib.gemm_tn_adapters_plan.argtypes = [P(AdaptersArgs)] + [_vp] * 8 + [P(_i32), P(_i64)]
+    for n in ("gemm_tn_adapters", "gemm_tn_adapters_plan", "group_rows", "group_rows_plan", "gemm_tn_grouped", "gemm_tn_grouped_plan",
               "gemm_tn_grouped_backward", "gemm_tn_grouped_backward_plan", "combine_rows",
               "combine_rows_backward"):
         getattr(lib, n).restype = ctypes.c_int
@@ -310,3 +319,81 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
     _call(run, _lib.combine_rows_backward, a, X.shape[1], _ptr(dout), _ptr(X), _ptr(slots),
           _ptr(rows), _ptr(weights), _ptr(dX), _ptr(dw))
     return dX, dw
+
+
+def _adapters_args(x, W, A, B, offsets, rows, scale, out: int, algo: str, ldd: int):
+    code = _dtype("x, W, A and B", x, W, A, B)
+    ldx, ldw = _matrix(x, "x"), _matrix(W, "W")
+    lda, a_group = _matrices(A, "A")
+    ldb, b_group = _matrices(B, "B")
+    (m, k), (n, kw), (groups, rank, ka) = x.shape, W.shape, A.shape
+    if kw != k or ka != k:
+        raise ValueError("x, W and A disagree on K")
+    if B.shape != (groups, n, rank):
+        raise ValueError("W, A and B disagree on the adapters, N or the rank")
+    _numbers(offsets, "offsets", groups + 1)
+    _numbers(rows, "rows")
+    if rows is not None and rows.shape[0] > m:
+        raise ValueError("rows holds each row at most once")
+    if scale is not None:
+        if scale.dtype != torch.float32:
+            raise TypeError("scale must be float32")
+        if scale.shape != (groups,) or (groups > 1 and scale.stride(0) != 1):
+            raise ValueError("scale must hold one factor per adapter, contiguous")
+    return AdaptersArgs(code, out, GROUPED_ALGOS[algo], groups,
+                        m if rows is None else rows.shape[0], m, n, k, rank, ldx, ldw, lda,
+                        a_group, ldb, b_group, ldd)
+
+
+def gemm_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
+                  offsets: torch.Tensor, *, rows: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None,
+                  out_dtype: Optional[torch.dtype] = None, D: Optional[torch.Tensor] = None,
+                  algo: str = "auto", stream=None):
+    """x @ W.T, plus scale[g] * (x @ A[g].T) @ B[g].T in the rows of adapter g,
+    on the GPU: one step of a batch whose requests use different adapters.
+
+    x (M, K), W (N, K), A (adapters, rank, K), B (adapters, N, rank), float16
+    or bfloat16 with contiguous rows, 16-byte aligned, N, K and the rank
+    multiples of 8.  offsets (adapters + 1, int32, on the device): adapter g
+    owns the places offsets[g] .. offsets[g + 1] - 1; places behind the last
+    have no adapter.  rows (int32): the row of x and of the result at each
+    place, every row at most once, as group_rows(adapter of each row, adapters)
+    gives them; without it places are rows.  scale: (adapters,) float32, 1
+    without it.  D (M, N) is of x's type, or float32 with out_dtype; it is
+    allocated when not given, and rows that no place leads to are not written.
+    An adapter's values reach its own rows alone.  No autograd graph is
+    recorded.  algo chooses the kernel."""
+    m, n = x.shape[0], W.shape[0]
+    if D is not None:
+        if D.shape != (m, n):
+            raise ValueError(f"D must have shape {(m, n)}")
+        if out_dtype is not None and out_dtype != D.dtype:
+            raise TypeError("D is not of out_dtype")
+        out_dtype = D.dtype
+    a = _adapters_args(x, W, A, B, offsets, rows, scale, _type(out_dtype, x.dtype, "D"), algo,
+                       n if D is None else _matrix(D, "D"))
+    run = _Run([t for t in (x, W, A, B, offsets, rows, scale, D) if t is not None], stream)
+    if D is None:
+        D = run.empty((m, n), x.dtype if out_dtype is None else out_dtype)
+    ptrs = tuple(_ptr(t) for t in (x, W, A, B, offsets, rows, scale, D))
+
+    def need():
+        b = _i64(0)
+        _check(_lib.gemm_tn_adapters_plan(a, *ptrs, None, b))
+        return b.value
+
+    run.call(_lib.gemm_tn_adapters, a, ptrs, need)
+    return D
+
+
+def gemm_adapters_plan(x, W, A, B, offsets, *, rows=None, scale=None, out_dtype=None,
+                       algo="auto") -> Tuple[str, int]:
+    """(kernel, workspace bytes) gemm_adapters() takes for these tensors; their
+    data is not read."""
+    a = _adapters_args(x, W, A, B, offsets, rows, scale, _type(out_dtype, x.dtype, "D"), algo,
+                       W.shape[0])
+    al, b = _i32(0), _i64(0)
+    _check(_lib.gemm_tn_adapters_plan(a, _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(offsets),
+                                      _ptr(rows), _ptr(scale), 1 << 40, al, b))
+    return _NAMES[al.value], b.value

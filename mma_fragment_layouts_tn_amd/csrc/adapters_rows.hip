@@ -1,0 +1,26 @@
+// Kernels of the shared projection with adapters on tiles through LDS: their
+// sums are tied by hand, and the build checks every access to them in the
+// generated code.
+#include <hip/hip_runtime.h>
+
+#include "adapters.hpp"
+
+namespace mfl {
+namespace grp {
+namespace {
+template <class T, class O, class C>
+KernelRef ref() {
+  return {(const void*)adapters_rows<T, O, C>, C::T, C::BM, C::BN};
+}
+template <class T, class O>
+KernelRef by_tile(int algo) {
+  return algo == kTile256 ? ref<T, O, Tile256>() : ref<T, O, Tile128>();
+}
+}  // namespace
+
+KernelRef adapters_kernel(bool bf16, bool f32, int algo) {
+  if (f32) return bf16 ? by_tile<__bf16, float>(algo) : by_tile<_Float16, float>(algo);
+  return bf16 ? by_tile<__bf16, __bf16>(algo) : by_tile<_Float16, _Float16>(algo);
+}
+}  // namespace grp
+}  // namespace mfl

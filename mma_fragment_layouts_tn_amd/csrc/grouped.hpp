@@ -95,6 +95,26 @@ MFL_HD constexpr int perm64(int r) {
   return (r & ~63) | ((r >> 2) & 3) << 4 | ((r >> 4) & 3) << 2 | (r & 3);
 }
 
+// The sums are as vector instructions wrote them, and the wait states before a
+// matrix instruction takes them have passed.
+template <class C>
+__device__ __forceinline__ void tied(floatx4 (&acc)[C::RM][C::RN]) {
+#pragma unroll
+  for (int i = 0; i < C::RM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::RN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  asm volatile("s_nop 4" ::);
+}
+// The matrix instructions' results are written: the sums may be moved or read.
+template <class C>
+__device__ __forceinline__ void settled(floatx4 (&acc)[C::RM][C::RN]) {
+  att::settle();
+#pragma unroll
+  for (int i = 0; i < C::RM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::RN; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
 // ------------------------------------------------------- fragment reads
 // Contraction-contiguous tile, rows of 64 elements (lds_offset<64>): the
 // fragment of rows 16 i + l % 16, sub-step kk.
@@ -184,11 +204,7 @@ __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
   for (int i = 0; i < RM; ++i)
 #pragma unroll
     for (int j = 0; j < RN; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < RM; ++i)
-#pragma unroll
-    for (int j = 0; j < RN; ++j) asm volatile("" : "+a"(acc[i][j]));
-  asm volatile("s_nop 4" ::);
+  tied<C>(acc);
   if (steps > 0) {
     Vec8<T> fp[2][RN], fq[2][RM];
     // fragment read r in the order the instructions take them
@@ -259,11 +275,7 @@ __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
     }
     step(kt, ring + (kt & 1) * C::STAGE, ring, ring, No(), No());
   }
-  att::settle();
-#pragma unroll
-  for (int i = 0; i < RM; ++i)
-#pragma unroll
-    for (int j = 0; j < RN; ++j) asm volatile("" : "+a"(acc[i][j]));
+  settled<C>(acc);
 }
 
 // ---------------------------------------------------- where loads come from
@@ -424,22 +436,28 @@ __device__ __forceinline__ int column_of(int lane, int j) {
   return PERM ? 16 * (lane >> 4) + 4 * j : 16 * j + 4 * (lane >> 4);
 }
 
-// the tile's rows (base + row ld) < rows and columns < width
-template <class O, class C, bool PERM>
-__device__ __forceinline__ void store_tile(O* base, int64_t ld, int rows, int col0, int width,
-                                           const floatx4 (&acc)[C::RM][C::RN], int w, int lane) {
+// the wave's rows, row_of(m) for row m of the tile (null: none), columns < width
+template <class O, class C, bool PERM, class RowOf>
+__device__ __forceinline__ void store_rows(const floatx4 (&acc)[C::RM][C::RN], int col0, int width,
+                                           int w, int lane, RowOf row_of) {
   const int wm = w % C::WM, wn = w / C::WM;
 #pragma unroll
   for (int i = 0; i < C::RM; ++i) {
-    const int m = wm * (C::BM / C::WM) + 16 * i + (lane & 15);
-    if (m >= rows) continue;
-    O* row = base + (int64_t)m * ld;
+    O* row = row_of(wm * (C::BM / C::WM) + 16 * i + (lane & 15));
+    if (!row) continue;
 #pragma unroll
     for (int j = 0; j < C::RN; ++j) {
       const int n = col0 + wn * 64 + column_of<PERM>(lane, j);
       if (n < width) Out<O>::store4(row + n, acc[i][j]);
     }
   }
+}
+// rows follow each other
+template <class O, class C, bool PERM>
+__device__ __forceinline__ void store_tile(O* base, int64_t ld, int rows, int col0, int width,
+                                           const floatx4 (&acc)[C::RM][C::RN], int w, int lane) {
+  store_rows<O, C, PERM>(acc, col0, width, w, lane,
+                         [&](int m) { return m < rows ? base + (int64_t)m * ld : nullptr; });
 }
 
 template <class O, class C>
@@ -456,6 +474,27 @@ struct RowsSource {
   static constexpr int kAhead = 0;    // loads of ahead()
   RowLoads<C::NQ> q;
   typename std::conditional<PT, PlainColumns<C::BN, C::NP>, RowLoads<C::NP>>::type p;
+  // the tile's places against columns n0 .. of the matrix P
+  template <class T>
+  __device__ __forceinline__ void init(const GroupedParams& a, const Place& at, int n0, const T* P,
+                                       int w, int lane) {
+    if (a.rows)
+      q.init(a.q, a.k, w, lane, [&](int row) {
+        const int r = a.rows[at.first + min(row, at.count - 1)];
+        return row < at.count && (unsigned)r < (unsigned)a.q_rows ? 2u * (unsigned)r * a.ldq
+                                                                  : kOutside;
+      });
+    else
+      q.init((const T*)a.q + (int64_t)at.first * a.ldq, a.k, w, lane,
+             [&](int row) { return row < at.count ? 2u * row * a.ldq : kOutside; });
+    if constexpr (PT)
+      p.init(P, a.k, a.ldp, n0, a.n, w, lane);
+    else
+      p.init(P + (int64_t)n0 * a.ldp, a.k, w, lane, [&](int row) {
+        const int n = perm64(row);
+        return n0 + n < a.n ? 2u * n * a.ldp : kOutside;
+      });
+  }
   __device__ __forceinline__ void ahead(int) {}
   __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
     if (i < C::NP)
@@ -480,24 +519,8 @@ __global__ void __launch_bounds__(C::T, 1) grouped_rows(const GroupedParams p) {
     if constexpr (PT) zero_tile<O, C>(D, p.ldd, at.count, n0, p.n, tid);
     return;
   }
-  const T* P = (const T*)p.p + at.group * p.p_group;
   RowsSource<C, PT> src;
-  if (p.rows)
-    src.q.init(p.q, p.k, w, lane, [&](int row) {
-      const int a = p.rows[at.first + min(row, at.count - 1)];
-      return row < at.count && (unsigned)a < (unsigned)p.q_rows ? 2u * (unsigned)a * p.ldq : kOutside;
-    });
-  else
-    src.q.init((const T*)p.q + (int64_t)at.first * p.ldq, p.k, w, lane, [&](int row) {
-      return row < at.count ? 2u * row * p.ldq : kOutside;
-    });
-  if constexpr (PT)
-    src.p.init(P, p.k, p.ldp, n0, p.n, w, lane);
-  else
-    src.p.init(P + (int64_t)n0 * p.ldp, p.k, w, lane, [&](int row) {
-      const int n = perm64(row);
-      return n0 + n < p.n ? 2u * n * p.ldp : kOutside;
-    });
+  src.init(p, at, n0, (const T*)p.p + at.group * p.p_group, w, lane);
   floatx4 acc[C::RM][C::RN];
   product<T, C, PT, false>((lds_c)smem, (p.k + 63) / 64, src, acc, w, lane);
   store_tile<O, C, !PT>(D, p.ldd, at.count, n0, p.n, acc, w, lane);
@@ -627,6 +650,32 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
   }
 }
 
+// the tile's places against columns n0 .. of the matrix P
+template <class T, int RM, int RN>
+__device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at, int n0,
+                                         const T* P, floatx4* sums, int w, int lane) {
+  const int r = lane & 15;
+  const unsigned c = 16u * (lane >> 4);
+  unsigned q_off[RM], p_off[RN];
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int row = 16 * i + r;
+    if (p.rows) {
+      const int a = p.rows[at.first + min(row, at.count - 1)];
+      q_off[i] = row < at.count && (unsigned)a < (unsigned)p.q_rows
+                     ? 2u * (unsigned)a * p.ldq + c : kOutside;
+    } else {
+      q_off[i] = row < at.count ? 2u * row * p.ldq + c : kOutside;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < RN; ++j)
+    p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + c : kOutside;
+  few_product<T, RM, RN>(
+      buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
+      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, p.k, sums, w, lane);
+}
+
 // D = A B[g]^T, groups of few rows
 template <class T, class O, int RM, int RN>
 __global__ void __launch_bounds__(64 * kFewWaves, 1) grouped_few(const GroupedParams p) {
@@ -636,26 +685,8 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) grouped_few(const GroupedPa
   const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
   const Place at = place_of(p, ti.tm, F::BM);
   if (at.count <= 0 || at.group == p.groups) return;
-  const int n0 = ti.tn * F::BN, r = lane & 15;
-  unsigned q_off[RM], p_off[RN];
-#pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int row = 16 * i + r;
-    if (p.rows) {
-      const int a = p.rows[at.first + min(row, at.count - 1)];
-      q_off[i] = row < at.count && (unsigned)a < (unsigned)p.q_rows
-                     ? 2u * (unsigned)a * p.ldq + 16u * (lane >> 4) : kOutside;
-    } else {
-      q_off[i] = row < at.count ? 2u * row * p.ldq + 16u * (lane >> 4) : kOutside;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < RN; ++j)
-    p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + 16u * (lane >> 4) : kOutside;
-  few_product<T, RM, RN>(
-      buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
-      buffer((const T*)p.p + at.group * p.p_group + (int64_t)n0 * p.ldp, kWhole), p_off, p.k, sums,
-      w, lane);
+  const int n0 = ti.tn * F::BN;
+  few_tile<T, RM, RN>(p, at, n0, (const T*)p.p + at.group * p.p_group, sums, w, lane);
   // (a thread stores what it added itself)
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;

@@ -161,6 +161,69 @@ int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, c
   return MFL_OK;
 }
 
+int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const void* A,
+                   const void* B, const int32_t* offsets, const int32_t* rows, const float* scale,
+                   const void* D) {
+  if (a.x_rows < 0 || a.n < 0 || a.k < 0 || a.rank < 0) return MFL_E_NEGATIVE_DIM;
+  int rc = check_places(a.groups, a.places);
+  if (rc) return rc;
+  if (!half_type(a.dtype) || (a.out != a.dtype && a.out != MFL_F32) || a.algo < MFL_GROUPED_AUTO ||
+      a.algo > MFL_GROUPED_TILE_256)
+    return MFL_E_UNSUPPORTED;
+  if (a.n == 0 || a.k == 0 || a.rank == 0) return MFL_E_UNSUPPORTED;
+  if (a.x_rows > kMaxCount || a.n > kMaxExtent || a.k > kMaxExtent || a.rank > kMaxExtent)
+    return MFL_E_TOO_LARGE;
+  if (a.n % 8 || a.k % 8 || a.rank % 8) return MFL_E_MISALIGNED;
+  if (!rows && a.x_rows < a.places) return MFL_E_UNSUPPORTED;
+  if (!offsets || !W || !A || !B || (a.places > 0 && (!x || !D))) return MFL_E_NULL_POINTER;
+  if ((rc = check_stride(a.ldx, a.k)) || (rc = check_stride(a.ldw, a.k)) ||
+      (rc = check_stride(a.lda, a.k)) || (rc = check_stride(a.ldb, a.rank)) ||
+      (rc = check_stride(a.ldd, a.n)) ||
+      (rc = check_group_stride(a.a_group, a.rank, a.lda, a.k, a.groups, false)) ||
+      (rc = check_group_stride(a.b_group, a.n, a.ldb, a.rank, a.groups, false)))
+    return rc;
+  if (rows && a.x_rows * a.ldx > kMaxGather) return MFL_E_TOO_LARGE;
+  if (!aligned(x) || !aligned(W) || !aligned(A) || !aligned(B) || !aligned(D) ||
+      !aligned4(offsets) || !aligned4(rows) || !aligned4(scale))
+    return MFL_E_MISALIGNED;
+  if (D && (D == x || D == W || D == A || D == B)) return MFL_E_ALIAS;
+  return MFL_OK;
+}
+
+// The shared product is on tiles of places whatever their group; the down
+// projection on tiles of one group.
+struct AdaptersPlan {
+  Choice down, all;
+  int pieces;                  // 0: h in fp32
+  int64_t h_at, bytes;
+};
+AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
+  const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
+  AdaptersPlan r;
+  const int64_t mean = ceil_div(a.places, a.groups);
+  const int algo = a.algo ? a.algo : a.places <= 192 ? kFew
+                   : square_tile(a.places, a.places, a.n);
+  r.all.algo = algo;
+  if (algo == kFew) {
+    const int rm = a.places <= 16 ? 1 : a.places <= 32 ? 2 : 4;
+    const int rn = ceil_div(a.places, 16 * rm) * ceil_div(a.n, 32) >= 2 * kFill ? 2 : 1;
+    r.all.kernel = adapters_few_kernel(bf16, f32, rm, rn);
+    r.pieces = 0;
+  } else {
+    r.all.kernel = adapters_kernel(bf16, f32, algo);
+    r.pieces = f32 ? 3 : 2;
+  }
+  r.all.slots = ceil_div(a.places, r.all.kernel.bm);
+  r.all.tiles_n = ceil_div(a.n, r.all.kernel.bn);
+  r.down.algo = kFew;
+  r.down.kernel = down_kernel(bf16, mean <= 10 ? 1 : mean <= 24 ? 2 : 4, a.rank <= 16 ? 1 : 2);
+  r.down.slots = tile_slots(a.places, a.groups, r.down.kernel.bm);
+  r.down.tiles_n = ceil_div(a.rank, r.down.kernel.bn);
+  r.h_at = ceil_div(4 * a.places, 16) * 16;
+  r.bytes = r.h_at + a.places * a.rank * (r.pieces ? 2 * r.pieces : 4);
+  return r;
+}
+
 struct SortPlan {
   int64_t chunk, blocks, bytes;
 };
@@ -349,6 +412,67 @@ int gemm_tn_grouped_backward(const mfl_grouped_grad_t* a, const void* dD, const 
   p.d_group = a->db_group;
   place(p, r.db);
   return launch(r.db.kernel, r.db.blocks(), &p, stream);
+}
+
+int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W, const void* A,
+                          const void* B, const int32_t* offsets, const int32_t* rows,
+                          const float* scale, const void* D, int32_t* algo,
+                          int64_t* workspace_bytes) {
+  if (!a) return MFL_E_NULL_POINTER;
+  const int rc = check_adapters(*a, x, W, A, B, offsets, rows, scale, D);
+  if (rc) return rc;
+  const AdaptersPlan r = plan_adapters(*a);
+  if (r.down.blocks() > kMaxBlocks || r.all.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (algo) *algo = r.all.algo;
+  if (workspace_bytes) *workspace_bytes = r.bytes;
+  return MFL_OK;
+}
+
+int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, const void* A,
+                     const void* B, const int32_t* offsets, const int32_t* rows,
+                     const float* scale, void* D, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  int64_t need = 0;
+  int rc = gemm_tn_adapters_plan(a, x, W, A, B, offsets, rows, scale, D, nullptr, &need);
+  if (rc) return rc;
+  if (a->places == 0) return MFL_OK;
+  if (!workspace || !aligned(workspace) || workspace_bytes < need) return MFL_E_WORKSPACE;
+  const AdaptersPlan r = plan_adapters(*a);
+  AdapterParams p{};
+  p.g.q = x;
+  p.g.d = D;
+  p.g.offsets = offsets;
+  p.g.rows = rows;
+  p.g.groups = (int)a->groups;
+  p.g.places = (int)a->places;
+  p.g.k = (int)a->k;
+  p.g.ldq = (int)a->ldx;
+  p.g.q_rows = (int)a->x_rows;
+  p.up = B;
+  p.scale = scale;
+  p.owner = (int*)workspace;
+  if (r.pieces)
+    p.hp = (char*)workspace + r.h_at;
+  else
+    p.h = (float*)((char*)workspace + r.h_at);
+  p.up_group = a->b_group;
+  p.rank = (int)a->rank;
+  p.ldup = (int)a->ldb;
+  p.pieces = r.pieces;
+  AdapterParams down = p;
+  down.g.p = A;
+  down.g.n = (int)a->rank;
+  down.g.ldp = (int)a->lda;
+  down.g.p_group = a->a_group;
+  place(down.g, r.down);
+  rc = launch(r.down.kernel, r.down.blocks(), &down, stream);
+  if (rc) return rc;
+  p.g.p = W;
+  p.g.n = (int)a->n;
+  p.g.ldp = (int)a->ldw;
+  p.g.ldd = (int)a->ldd;
+  place(p.g, r.all);
+  return launch(r.all.kernel, r.all.blocks(), &p, stream);
 }
 
 int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,

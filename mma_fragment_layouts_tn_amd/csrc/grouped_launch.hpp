@@ -21,6 +21,20 @@ struct GroupedParams {
   int64_t p_group, d_group;
 };
 
+// Adapters beside a shared projection (adapters.hpp): g is the down
+// projection's (p = A, n = rank) in the first launch, the shared product's
+// (p = W) in the second.  q = x, d = D, offsets and rows in both.
+struct AdapterParams {
+  GroupedParams g;
+  const void* up;              // B
+  const float* scale;          // of each group, or null: 1
+  int* owner;                  // workspace: the group of each place that has one,
+  float* h;                    // scale h in fp32, places x rank,
+  void* hp;                    // or as 16-bit numbers, places x pieces x rank
+  int64_t up_group;
+  int rank, ldup, pieces;
+};
+
 struct SortParams {
   const void* ids;
   int* rows;
@@ -57,6 +71,9 @@ KernelRef rows_kernel(bool bf16, bool f32, int algo);                   // D
 KernelRef few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
 KernelRef input_grad_kernel(bool bf16, int algo);                       // dA
 KernelRef weight_grad_kernel(bool bf16, bool f32, int algo, bool gathered);   // dB
+KernelRef down_kernel(bool bf16, int row_blocks, int column_blocks);
+KernelRef adapters_few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
+KernelRef adapters_kernel(bool bf16, bool f32, int algo);
 KernelRef count_kernel(bool i64, int groups);
 KernelRef place_kernel(bool i64, int groups);
 KernelRef combine_kernel(bool bf16, bool f32);

@@ -1,7 +1,7 @@
 """Products by groups of rows on the GPU against their float64 definitions
 (oracle/grouped.py): places of a list of choices (exact), the product of every
-group and its gradients, and the sum of a token's results, every element
-within the bound that fp32 sums and one rounding of the result give.
+group and its gradients, the sum of a token's results, and adapters beside a
+projection, every element within the bound that fp32 sums and one rounding of the result give.
 
 Sizes sit where the kernels change: empty groups, one row, the 16 rows of an
 atom, tiles of 16, 32, 64, 128 and 256 rows, contractions that end inside a
@@ -338,3 +338,135 @@ def test_combine_strides():
     want, tol = G.combine(f64(X[:, :40]), slots.numpy(), np.ones((4, 3)), "bf16")
     within("out", got, want, tol)
     assert bool((out[:, 40:] == 0).all())
+
+
+# ---------------------------------------------------------- gemm_adapters
+class Adapted:
+    def __init__(self, kind, m, adapters, rank, n, k, *, mode="mixed", seed=0, pad=0):
+        gen = torch.Generator().manual_seed(seed + m + rank + n + k)
+        self.kind = kind
+        ids = torch.randint(-1, adapters, (m,), generator=gen)
+        if mode == "runs":
+            ids = ids.sort().values
+        if mode == "none":
+            ids[:] = -1
+        if mode == "one":
+            ids[:] = adapters - 1
+        self.ids = ids
+        self.x = values(gen, (m, k + pad), kind)[:, :k]
+        self.W = values(gen, (n, k + pad), kind, k ** -0.5)[:, :k]
+        self.A = values(gen, (adapters, rank, k + pad), kind, k ** -0.5)[:, :, :k]
+        self.B = values(gen, (adapters, n, rank + pad), kind, rank ** -0.5)[:, :, :rank]
+        self.scale = torch.rand(adapters, generator=gen) * 2 - 0.5
+        self.adapters = adapters
+        say(f"[gpu] adapters {kind} m={m} adapters={adapters} rank={rank} n={n} k={k} {mode}")
+
+    def run(self, out="", scale=True, **kw):
+        rows, offsets, _ = mfl.group_rows(self.ids.cuda(), self.adapters)
+        self.rows, self.offsets = rows.cpu(), offsets.cpu()
+
+        def put(t):
+            c = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device="cuda")
+            return c.copy_(t)
+
+        D = mfl.gemm_adapters(put(self.x), put(self.W), put(self.A), put(self.B), offsets,
+                              rows=rows, scale=self.scale.cuda() if scale else None,
+                              out_dtype=DT[out or self.kind], **kw)
+        torch.cuda.synchronize()
+        return D
+
+    def check(self, out="", scale=True, **kw):
+        D = self.run(out, scale, **kw)
+        s = f64(self.scale) if scale else np.ones(self.adapters)
+        want, tol = G.adapters(f64(self.x), f64(self.W), f64(self.A), f64(self.B),
+                               self.offsets.numpy(), self.rows.numpy(), s, out or self.kind)
+        within("D", D, want, tol)
+        return D
+
+
+ALGOS = ["few", "tile128", "tile256"]
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("m", [1, 16, 33, 64, 130, 300])
+@pytest.mark.parametrize("mode", ["mixed", "runs", "none", "one"])
+def test_adapters_rows(m, mode, algo):
+    Adapted("bf16", m, 5, 16, 136, 200, mode=mode).check(algo=algo)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("rank", [8, 24, 32, 40, 64, 136])
+@pytest.mark.parametrize("kind,out", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"),
+                                      ("bf16", "f32")])
+def test_adapters_ranks(kind, out, rank, algo):
+    Adapted(kind, 70, 3, rank, 72, 264).check(out, scale=rank != 24, algo=algo)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+@pytest.mark.parametrize("n,k", [(8, 8), (264, 128), (512, 1000)])
+def test_adapters_sizes(n, k, algo):
+    Adapted("f16", 90, 40, 8, n, k, pad=16).check(algo=algo)
+
+
+def test_adapters_auto_and_many():
+    Adapted("bf16", 400, 100, 16, 1032, 64).check()
+    Adapted("f16", 1200, 7, 32, 1024, 72, mode="runs").check()
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_adapters_without_rows(algo):
+    """Places are rows; those behind the last adapter have the shared term
+    alone."""
+    c = Adapted("bf16", 100, 4, 16, 72, 136)
+    offsets = torch.tensor([0, 30, 30, 47, 80], dtype=torch.int32)
+    D = mfl.gemm_adapters(c.x.cuda(), c.W.cuda(), c.A.cuda(), c.B.cuda(), offsets.cuda(),
+                          algo=algo)
+    want, tol = G.adapters(f64(c.x), f64(c.W), f64(c.A), f64(c.B), offsets.numpy(), None,
+                           np.ones(4), "bf16")
+    within("D", D, want, tol)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_adapters_are_apart(algo):
+    """An adapter of infinities and NaN changes no other request's row."""
+    c = Adapted("f16", 150, 5, 16, 72, 136, seed=2)
+    clean = c.run(algo=algo)
+    c.B[2, 5:9], c.A[3] = float("nan"), float("inf")
+    c.B[2, 20, 3] = float("inf")
+    D = c.run(algo=algo)
+    others = (c.ids != 2) & (c.ids != 3)
+    assert torch.equal(D[others], clean[others])
+    mine = (c.ids == 2).nonzero().flatten()
+    rest = [n for n in range(72) if not 5 <= n < 9 and n != 20]
+    assert bool(D[mine][:, 5:9].isnan().all()) and bool((~D[mine][:, 20].isfinite()).all())
+    assert torch.equal(D[mine][:, rest], clean[mine][:, rest])
+    assert bool((~D[c.ids == 3].isfinite()).all())
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_adapters_rows_listed_in_part(algo):
+    """Rows that no place leads to stay as they were; numbers outside are
+    skipped."""
+    c = Adapted("bf16", 90, 3, 8, 64, 72, seed=4)
+    rows = torch.arange(0, 90, 2, dtype=torch.int32)
+    rows[3], rows[7] = -1, 90
+    offsets = torch.tensor([0, 10, 25, 40], dtype=torch.int32)
+    D = torch.full((90, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    mfl.gemm_adapters(c.x.cuda(), c.W.cuda(), c.A.cuda(), c.B.cuda(), offsets.cuda(),
+                      rows=rows.cuda(), D=D, algo=algo)
+    want, tol = G.adapters(f64(c.x), f64(c.W), f64(c.A), f64(c.B), offsets.numpy(), rows.numpy(),
+                           np.ones(3), "bf16")
+    kept = torch.from_numpy(np.isnan(want[:, 0]))
+    assert int(kept.sum()) == 47 and bool((D[kept] == 7).all())
+    within("D", D, want, tol)
+
+
+@pytest.mark.parametrize("algo", ALGOS)
+def test_adapters_offsets_out_of_range(algo):
+    c = Adapted("f16", 90, 3, 8, 64, 72)
+    for bad in ([-5, 30, 1 << 30, 90], [0, 80, 20, 90], [90, 90, 90, 90],
+                [2 ** 31 - 1, -2 ** 31, 50, 3]):
+        say(f"[gpu] offsets {bad}")
+        mfl.gemm_adapters(c.x.cuda(), c.W.cuda(), c.A.cuda(), c.B.cuda(),
+                          torch.tensor(bad, dtype=torch.int32).cuda(), algo=algo)
+    torch.cuda.synchronize()
