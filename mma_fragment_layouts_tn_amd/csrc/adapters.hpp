@@ -42,9 +42,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_down(const Adapter
   using F = FewTile<RM, RN>;
   __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const int slot = blockIdx.x / p.g.tiles_n, n0 = (blockIdx.x % p.g.tiles_n) * F::BN;
-  const Place at = place_of(p.g, slot, F::BM);
-  if (at.count <= 0 || at.group == p.g.groups) return;
+  const GroupSpot spot = group_spot<1>(p.g, blockIdx.x, F::BM);
+  if (spot.spot.parts == 0 || spot.at.group == p.g.groups) return;
+  const Place at = spot.at;
+  const int n0 = spot.spot.tn * F::BN;
   few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p + at.group * p.g.p_group, sums, w, lane);
   const float s = p.scale ? p.scale[at.group] : 1.0f;
   if (n0 == 0)
@@ -92,9 +93,9 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_few(const AdapterP
   using F = FewTile<RM, RN>;
   __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.g.slots, p.g.tiles_n, p.g.band);
-  const Place at{0, ti.tm * F::BM, min(p.g.places - ti.tm * F::BM, F::BM)};
-  const int n0 = ti.tn * F::BN;
+  const Spot s = spot_of<1>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.slots);
+  const Place at{0, s.tm * F::BM, min(p.g.places - s.tm * F::BM, F::BM)};
+  const int n0 = s.tn * F::BN;
   few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p, sums, w, lane);
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;
@@ -150,27 +151,27 @@ __device__ __forceinline__ floatx4 rest(const AdapterParams& p, int place, int n
 // of other groups multiply B by zeros.  What is not finite in B is left out
 // there, so that it cannot reach them, and added to its own rows at the end.
 template <class T, class O, class C>
-__global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) {
-  constexpr int NPC = pieces_of<O>(), RN = C::RN, H = C::RM / 4;
-  static_assert(C::RM % 4 == 0, "runs are found 64 rows at a time");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE];
+__device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem, int first,
+                                              int count, int n0) {
+  constexpr int NPC = pieces_of<O>(), RN = C::RN, WROWS = 16 * C::RM, H = (C::RM + 3) / 4,
+                HM = C::RM < 4 ? C::RM : 4;
+  static_assert(H * HM == C::RM, "runs are found 64 rows at a time");
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const GroupedParams& g = p.g;
-  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, g.slots, g.tiles_n, g.band);
-  const int first = ti.tm * C::BM, count = min(g.places - first, C::BM), n0 = ti.tn * C::BN;
   RowsSource<C, false> src;
   src.init(g, Place{0, first, count}, n0, (const T*)g.p, w, lane);
   floatx4 acc[C::RM][RN];
   product<T, C, false, false>((lds_c)smem, (g.k + 63) / 64, src, acc, w, lane);
 
-  const int m0 = first + (w % C::WM) * (C::BM / C::WM), nw = n0 + (w / C::WM) * 64;
+  const int m0 = first + (w % C::WM) * WROWS, nw = n0 + (w / C::WM) * 64;
   const int r = lane & 15, c8 = 8 * (lane >> 4);
   bool bad = false;       // something in B that is not finite
   tied<C>(acc);
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int at = m0 + 64 * h;
-    const int own = at + lane < first + count ? owner_of(p, at + lane) : -1;
+    const int own =
+        lane < 16 * HM && at + lane < first + count ? owner_of(p, at + lane) : -1;
     unsigned long long starts = __ballot(lane == 0 || own != __shfl_up(own, 1));
     while (starts) {
       const int a = __builtin_ctzll(starts);
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
           buffer((const T*)p.hp + (int64_t)at * NPC * p.rank, kWhole);
       for (int c0 = 0; c0 < p.rank; c0 += 32) {
         const bool in = c0 + c8 < p.rank;
-        u32x4_t fp[RN], fq[NPC][4];
+        u32x4_t fp[RN], fq[NPC][HM];
 #pragma unroll
         for (int j = 0; j < RN; ++j) {
           const int n = 16 * (r >> 2) + 4 * j + (r & 3);
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
 #pragma unroll
         for (int x = 0; x < NPC; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < HM; ++i) {
             const int m = 16 * i + r;
             fq[x][i] = __builtin_amdgcn_raw_buffer_load_b128(
                 rh, in && m >= a && m < b ? 2u * ((m * NPC + x) * p.rank + c0 + c8) : kOutside, 0,
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
 #pragma unroll
         for (int x = 0; x < NPC; ++x)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < HM; ++i)
 #pragma unroll
             for (int j = 0; j < RN; ++j)
               Mma<T>::run(as16(fp[j], T()), as16(fq[x][i], T()), acc[4 * h + i][j]);
@@ -222,7 +223,6 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
     }
   }
   settled<C>(acc);
-  const int wave_row = (w % C::WM) * (C::BM / C::WM);
   auto row_of = [&](int m) {
     const int row = m < count ? row_at(g, first + m) : -1;
     return row < 0 ? nullptr : (O*)g.d + (int64_t)row * g.ldd;
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
   // depend on the rounding of its finite part)
 #pragma unroll 1
   for (int x = 0; x < C::RM * RN; ++x) {
-    const int m = wave_row + 16 * (x / RN) + r, n = nw + column_of<true>(lane, x % RN);
+    const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of<true>(lane, x % RN);
     O* row = row_of(m);
     if (!row || n >= g.n) continue;
     floatx4 y = rest<T>(p, first + m, n, NPC);
@@ -241,6 +241,18 @@ __global__ void __launch_bounds__(C::T, 1) adapters_rows(const AdapterParams p) 
     for (int v = 0; v < 4; ++v) y[v] += (float)row[n + v];
     Out<O>::store4(row + n, y);
   }
+}
+
+template <class T, class O, class S>
+__global__ void __launch_bounds__(S::Full::T, 1) adapters_rows(const AdapterParams p) {
+  using C = typename S::Full;
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+  const Spot s = spot_of<S::kParts>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.band);
+  if (s.parts == 0) return;
+  const Place at{0, s.tm * C::BM, min(p.g.places - s.tm * C::BM, C::BM)};
+  by_rows<S>(s, at, [&](auto c, const Place& x) {
+    adapters_tile<T, O, decltype(c)>(p, smem, x.first, x.count, s.tn * C::BN);
+  });
 }
 
 }  // namespace grp

@@ -8,13 +8,13 @@
 namespace mfl {
 namespace grp {
 namespace {
-template <class T, class O, class C>
+template <class T, class O, class S>
 KernelRef ref() {
-  return {(const void*)adapters_rows<T, O, C>, C::T, C::BM, C::BN};
+  return {(const void*)adapters_rows<T, O, S>, S::Full::T, S::Full::BM, S::Full::BN, S::kParts};
 }
 template <class T, class O>
 KernelRef by_tile(int algo) {
-  return algo == kTile256 ? ref<T, O, Tile256>() : ref<T, O, Tile128>();
+  return algo == kTile256 ? ref<T, O, Tiles256>() : ref<T, O, Tiles128>();
 }
 }  // namespace
 

@@ -68,25 +68,48 @@ struct Mma<__bf16> {
   }
 };
 
-// A tile of BM x BN by WM x WN waves, BC contraction elements per step, two
+// A tile of BM x BN by WM x WN waves, BC contraction elements per step, NST
 // stages.  Each wave 16 RM x 64.
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int NST_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BC = 64;
   static constexpr int W = WM * WN, T = 64 * W;
   static constexpr int RM = BM / WM / 16, RN = BN / WN / 16;
   static constexpr int P_BYTES = BN * BC * 2, Q_BYTES = BM * BC * 2;
-  static constexpr int STAGE = P_BYTES + Q_BYTES;
+  static constexpr int NST = NST_, STAGE = P_BYTES + Q_BYTES, LDS = NST * STAGE;
   static constexpr int NP = P_BYTES / 1024 / W, NQ = Q_BYTES / 1024 / W, NI = NP + NQ;
   static_assert(RN == 4, "the order of P's rows in LDS is made for 64 columns per wave");
   static_assert(NP * W * 1024 == P_BYTES && NQ * W * 1024 == Q_BYTES, "loads divide over waves");
-  static_assert(BM % 128 == 0 && BN % 128 == 0, "swizzle of transposed tiles");
-  static_assert(2 * STAGE <= 160 * 1024, "two stages fit LDS");
+  static_assert(LDS <= 160 * 1024, "stages fit LDS");
 };
 
-// 8 waves of 128 x 64, two per SIMD; 4 waves of 64 x 64, two workgroups per CU
-using Tile256 = Tile<256, 256, 2, 4>;
-using Tile128 = Tile<128, 128, 2, 2>;
+// Tiles of 256 x 256 by 8 waves of 128 x 64, two per SIMD, one workgroup per
+// CU.  The tiles of a launch's last, incomplete round are cut in two or four,
+// one part to a workgroup, as long as those find room in the round (kParts),
+// and a tile of few rows is computed as the smaller one: 68 tiles by 8 are 2
+// rounds and a quarter, not 3.
+//
+// A smaller tile's step is over before the loads of the next have come (a
+// quarter's: 0.7 us a step with two stages, where its instructions take 0.25),
+// so it keeps as many stages as LDS holds.
+struct Tiles256 {
+  using Full = Tile<256, 256, 2, 4>;
+  using Half = Tile<128, 256, 2, 4, 3>;
+  using Quarter = Tile<64, 256, 2, 4, 4>;
+  static constexpr int kParts = 4, kLds = Quarter::LDS;
+};
+// the same where both operands are transposed
+struct Weights256 {
+  using Full = Tile<256, 256, 2, 4>;
+  using Half = Tile<128, 256, 2, 4>;
+  using Corner = Tile<128, 128, 4, 2>;
+  static constexpr int kParts = 4, kLds = Full::LDS;
+};
+// Tiles of 128 x 128 by 4 waves of 64 x 64, two workgroups per CU.
+struct Tiles128 {
+  using Full = Tile<128, 128, 2, 2>;
+  static constexpr int kParts = 1, kLds = Full::LDS;
+};
 
 // P's rows in LDS (contraction contiguous): row 16 j + 4 q + v of a wave's 64
 // holds column 16 q + 4 j + v, so the four atoms' accumulators of a lane are
@@ -191,7 +214,7 @@ struct ReaderOf<T, R, true> {
 // while the second one's fragments are read; then every wave has its loads of
 // the next step and is done with this stage (the barrier); the second one's
 // run while the next stage's first fragments are read and the loads of the
-// step after that go into this stage, one by one between the instructions.
+// step NST further go into this stage, one by one between the instructions.
 template <class T, class C, bool PT, bool QT, class Source>
 __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
                                         floatx4 (&acc)[C::RM][C::RN], int w, int lane) {
@@ -217,7 +240,7 @@ __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
         fq[buf][r - RN] = rq.read(stage + C::P_BYTES, r - RN, kk);
     };
     constexpr int kReads = RM + RN, kMma = RM * RN, kSlots = kMma / 2;
-    auto group = [&](int buf, auto reads, lds_c stage, auto loads, int kt, lds_c to) {
+    auto group = [&](int buf, lds_c stage, auto loads, int kt, lds_c to) {
 #pragma unroll
       for (int g = 0; g < kMma; ++g) {
         if (C::W > 4) {           // two waves of the workgroup per SIMD take turns
@@ -225,11 +248,10 @@ __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
           if (g == kMma / 2) __builtin_amdgcn_s_setprio(0);
         }
         Mma<T>::run(fp[buf][g % RN], fq[buf][g / RN], acc[g / RN][g % RN]);
-        if constexpr (decltype(reads)::value)
-          if (g < kSlots)
+        if (g < kSlots)
 #pragma unroll
-            for (int r = g * kReads / kSlots; r < (g + 1) * kReads / kSlots; ++r)
-              read(r, 1 - buf, 1 - buf, stage);
+          for (int r = g * kReads / kSlots; r < (g + 1) * kReads / kSlots; ++r)
+            read(r, 1 - buf, 1 - buf, stage);
         if constexpr (decltype(loads)::value)
 #pragma unroll
           for (int i = g * NI / kMma; i < (g + 1) * NI / kMma; ++i) src.issue(kt, i, to);
@@ -240,42 +262,39 @@ __device__ __forceinline__ void product(lds_c ring, int steps, Source& src,
     using No = BoolC<false>;
     // the stage read now, the next one, and where the loads go: distinct for
     // the compiler, which otherwise lets every transposing read wait for them
+    constexpr int NST = C::NST, HEAD = Source::kAhead;
+    static_assert(HEAD == 0 || NST == 2, "ahead() reaches one step");
     auto step = [&](int kt, lds_c __restrict__ from, lds_c __restrict__ next,
-                    lds_c __restrict__ to, auto has_next, auto has_load) {
-      group(0, Yes(), from, No(), 0, to);
-      att::wait_vm<0>();
+                    lds_c __restrict__ to) {
+      group(0, from, No(), 0, to);
+      att::wait_vm<(NST - 2) * NI>();
       barrier();
-      group(1, has_next, next, has_load, kt + 2, to);
-      if constexpr (decltype(has_load)::value) src.ahead(kt + 3);
+      group(1, next, Yes(), kt + NST, to);
+      src.ahead(kt + NST + 1);
     };
-    src.ahead(0);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) src.issue(0, i, ring);
-    src.ahead(1);
-    if (steps > 1) {
+    for (int st = 0; st < NST; ++st) {
+      src.ahead(st);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) src.issue(1, i, ring + C::STAGE);
-      src.ahead(2);
-      att::wait_vm<NI + Source::kAhead>();
-    } else {
-      att::wait_vm<0>();
+      for (int i = 0; i < NI; ++i) src.issue(st, i, ring + st * C::STAGE);
     }
+    src.ahead(NST);
+    att::wait_vm<(NST - 1) * NI + HEAD>();
     barrier();
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(r, 0, 0, ring);
-    int kt = 0;
-    for (; kt + 2 < steps; ++kt) {
-      const lds_c a = ring + (kt & 1) * C::STAGE, b = ring + (1 - (kt & 1)) * C::STAGE;
-      step(kt, a, b, a, Yes(), Yes());
+    // One body for every step (several would need the sums at the same
+    // registers where they meet): the loads behind the last step are out of
+    // range and move nothing, the fragments read behind it are not used.
+    lds_c from = ring, last = ring + (NST - 1) * C::STAGE;
+    for (int kt = 0; kt < steps; ++kt) {
+      const lds_c next = from == last ? ring : from + C::STAGE;
+      step(kt, from, next, from);
+      from = next;
     }
-    if (kt + 1 < steps) {
-      const lds_c a = ring + (kt & 1) * C::STAGE, b = ring + (1 - (kt & 1)) * C::STAGE;
-      step(kt, a, b, a, Yes(), No());
-      ++kt;
-    }
-    step(kt, ring + (kt & 1) * C::STAGE, ring, ring, No(), No());
+    att::wait_vm<0>();
+    settled<C>(acc);       // (inside the condition: where the paths meet is too late)
   }
-  settled<C>(acc);
 }
 
 // ---------------------------------------------------- where loads come from
@@ -396,23 +415,117 @@ struct GatheredColumns : ColumnLoads<R, N> {
 };
 
 // ---------------------------------------------------------- rows of groups
-// Tiles of `bm` places, none across two groups: slot of a tile as attention
-// finds those of its sequences.  The places behind the last group are a group
-// of their own.
 struct Place {
-  int group, first, count;    // the tile's first place, its places (<= bm)
+  int group, first, count;    // the tile's first place, its places
 };
-__device__ __forceinline__ Place place_of(const GroupedParams& p, int slot, int bm) {
-  auto first = [&](int g) { return min(max(p.offsets[g], 0), p.places) / bm + g; };
-  const int g = att::find_sequence(p.groups + 1, slot, first);
-  const int a = min(max(p.offsets[g], 0), p.places),
-            b = g < p.groups ? min(max(p.offsets[g + 1], 0), p.places) : p.places;
-  const Span s{uniform(a), uniform(max(b - a, 0))};
-  const int t = slot - uniform(s.begin / bm + g);
-  Place r;
-  r.group = g;
-  r.first = s.begin + t * bm;
-  r.count = t < 0 ? 0 : min(s.len - t * bm, bm);
+
+// Workgroups go to the 8 XCDs in turn; renumbered, each XCD has a run of
+// consecutive numbers (as tile_of_block).
+__device__ __forceinline__ int in_runs(int id, int n) {
+  const int q = n / 8, r = n % 8, x = id % 8;
+  return x * q + min(x, r) + id / 8;
+}
+// number -> tile, in bands `band` tiles tall
+__device__ __forceinline__ TileIndex tile_at(int lin, int tiles_m, int tiles_n, int band) {
+  const int g = lin / (band * tiles_n), in = lin - g * band * tiles_n;
+  const int rows = min(tiles_m - g * band, band);
+  return TileIndex{g * band + in % rows, in / rows};
+}
+
+// A workgroup's tile of `tiles_m` x `tiles_n`, or its part of one: those of
+// the last round of kFill workgroups are cut into up to PARTS.
+struct Spot {
+  int tm, tn, part, parts;    // parts 0: nothing to do
+};
+template <int PARTS>
+__device__ __forceinline__ Spot spot_of(int id, int tiles_m, int tiles_n, int band) {
+  const int n = tiles_m * tiles_n;
+  int whole = n, parts = 1;
+  if constexpr (PARTS > 1) {
+    const int rest = n % kFill;
+    parts = rest == 0 ? 1 : rest * 4 <= kFill && PARTS >= 4 ? 4 : rest * 2 <= kFill ? 2 : 1;
+    if (parts > 1) whole = n - rest;
+  }
+  int lin, part = 0;
+  if (id < whole) {
+    lin = in_runs(id, whole);
+    parts = 1;
+  } else {
+    const int cut = (n - whole) * parts;
+    if (id - whole >= cut) return Spot{0, 0, 0, 0};
+    const int x = in_runs(id - whole, cut);
+    lin = whole + x / parts;
+    part = x % parts;
+  }
+  const TileIndex t = tile_at(lin, tiles_m, tiles_n, band);
+  return Spot{t.tm, t.tn, part, parts};
+}
+
+// Tiles of `bm` places, none across two groups; the places behind the last
+// group are a group of their own (group == p.groups).
+//
+// Up to kExact - 1 groups every wave counts the tiles of all of them, 64
+// groups a time, so that the tiles are numbered without gaps and the launch's
+// workgroups beyond them are the last ones.  (With the numbering below, 4096
+// rows in one group left two of 18 slots empty, which made one of the 8 XCDs
+// idle and the others run a second round: 793 TFLOP/s where it gives 1,270.)
+// For more groups, group g takes the numbers from start(g) / bm + g on, as
+// attention's tiles of sequences, some of them empty.
+struct GroupSpot {
+  Spot spot;
+  Place at;
+};
+template <int PARTS>
+__device__ __forceinline__ GroupSpot group_spot(const GroupedParams& p, int id, int bm) {
+  auto held = [&](int g) { return min(max(p.offsets[g], 0), p.places); };
+  GroupSpot r;
+  if (p.groups >= kExact) {
+    r.spot = spot_of<1>(id, p.slots, p.tiles_n, p.band ? p.band : p.slots);
+    if (r.spot.parts == 0) return r;
+    auto first = [&](int g) { return held(g) / bm + g; };
+    const int g = att::find_sequence(p.groups + 1, r.spot.tm, first);
+    const int a = uniform(held(g)), b = uniform(g < p.groups ? held(g + 1) : p.places);
+    const int t = r.spot.tm - (a / bm + g);
+    r.at = Place{g, a + t * bm, t < 0 ? 0 : min(max(b - a, 0) - t * bm, bm)};
+    if (r.at.count <= 0) r.spot.parts = 0;
+    return r;
+  }
+  constexpr int NB = kExact / 64;
+  const int lane = threadIdx.x & 63;
+  int start[NB], len[NB], before[NB], total = 0;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int g = 64 * b + lane;
+    start[b] = g <= p.groups ? held(g) : 0;
+    const int end = g < p.groups ? held(g + 1) : p.places;
+    len[b] = g <= p.groups ? max(end - start[b], 0) : 0;
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (64 * b > p.groups) break;
+    const int mine = (len[b] + bm - 1) / bm;
+    int scan = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int t = __shfl_up(scan, d);
+      if (lane >= d) scan += t;
+    }
+    before[b] = total + scan - mine;
+    total += __builtin_amdgcn_readlane(scan, 63);
+  }
+  r.spot = spot_of<PARTS>(id, total, p.tiles_n,
+                          p.band ? p.band : max(total, 1));
+  if (r.spot.parts == 0) return r;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (64 * b > p.groups) break;
+    const unsigned long long m = __ballot(len[b] > 0 && before[b] <= r.spot.tm);
+    if (!m) continue;
+    const int l = 63 - __builtin_clzll(m);
+    const int t = r.spot.tm - __builtin_amdgcn_readlane(before[b], l);
+    r.at = Place{64 * b + l, __builtin_amdgcn_readlane(start[b], l) + t * bm,
+                 min(__builtin_amdgcn_readlane(len[b], l) - t * bm, bm)};
+  }
   return r;
 }
 
@@ -504,16 +617,11 @@ struct RowsSource {
   }
 };
 
-// D = A B[g]^T (PT false) or dA = dD B[g] (PT true): a tile of places of one
-// group.
+// a tile of places of one group against columns n0 ..
 template <class T, class O, class C, bool PT>
-__global__ void __launch_bounds__(C::T, 1) grouped_rows(const GroupedParams p) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE];
+__device__ __forceinline__ void rows_tile(const GroupedParams& p, char* smem, const Place& at,
+                                          int n0) {
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
-  const Place at = place_of(p, ti.tm, C::BM);
-  if (at.count <= 0) return;
-  const int n0 = ti.tn * C::BN;
   O* D = (O*)p.d + (int64_t)at.first * p.ldd;
   if (at.group == p.groups) {       // of no group: no result, or no gradient
     if constexpr (PT) zero_tile<O, C>(D, p.ldd, at.count, n0, p.n, tid);
@@ -524,6 +632,38 @@ __global__ void __launch_bounds__(C::T, 1) grouped_rows(const GroupedParams p) {
   floatx4 acc[C::RM][C::RN];
   product<T, C, PT, false>((lds_c)smem, (p.k + 63) / 64, src, acc, w, lane);
   store_tile<O, C, !PT>(D, p.ldd, at.count, n0, p.n, acc, w, lane);
+}
+
+// a part of a tile's rows; f with the tile that fits them
+template <class S, class F>
+__device__ __forceinline__ void by_rows(const Spot& spot, Place at, F f) {
+  using C = typename S::Full;
+  if constexpr (S::kParts == 1) {
+    f(C(), at);
+  } else {
+    const int rows = C::BM / spot.parts;
+    at.first += spot.part * rows;
+    at.count = min(at.count - spot.part * rows, rows);
+    if (at.count <= 0) return;
+    if (at.count <= S::Quarter::BM)
+      f(typename S::Quarter(), at);
+    else if (at.count <= S::Half::BM)
+      f(typename S::Half(), at);
+    else
+      f(C(), at);
+  }
+}
+
+// D = A B[g]^T (PT false) or dA = dD B[g] (PT true)
+template <class T, class O, class S, bool PT>
+__global__ void __launch_bounds__(S::Full::T, 1) grouped_rows(const GroupedParams p) {
+  using C = typename S::Full;
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+  const GroupSpot x = group_spot<S::kParts>(p, blockIdx.x, C::BM);
+  if (x.spot.parts == 0) return;
+  by_rows<S>(x.spot, x.at, [&](auto c, const Place& at) {
+    rows_tile<T, O, decltype(c), PT>(p, smem, at, x.spot.tn * C::BN);
+  });
 }
 
 template <class C, bool GATHER>
@@ -543,15 +683,12 @@ struct WeightsSource {
   }
 };
 
-// dB[g] = sum over the group's places of dD^T A: a tile of it.
 template <class T, class O, class C, bool GATHER>
-__global__ void __launch_bounds__(C::T, 1) grouped_weights(const GroupedParams p) {
-  __shared__ __attribute__((aligned(1024))) char smem[2 * C::STAGE];
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  // slots: tiles of one group's rows times groups
-  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
-  const int per = p.slots / p.groups, g = ti.tm / per;
-  const int m0 = (ti.tm - g * per) * C::BM, n0 = ti.tn * C::BN;
+__device__ __forceinline__ void weights_tile(const GroupedParams& p, char* smem, int g, int m0,
+                                             int n0) {
+  static_assert(C::BM % 128 == 0 && C::BN % 128 == 0, "swizzle of transposed tiles");
+  if (m0 >= p.m || n0 >= p.n) return;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   const Span s = span_of(p.offsets, g, p.places);
   WeightsSource<C, GATHER> src;
   if constexpr (GATHER)
@@ -563,6 +700,27 @@ __global__ void __launch_bounds__(C::T, 1) grouped_weights(const GroupedParams p
   product<T, C, true, true>((lds_c)smem, (s.len + 63) / 64, src, acc, w, lane);
   store_tile<O, C, false>((O*)p.d + g * p.d_group + (int64_t)m0 * p.ldd, p.ldd, p.m - m0, n0, p.n,
                           acc, w, lane);
+}
+
+// dB[g] = sum over the group's places of dD^T A
+template <class T, class O, class S, bool GATHER>
+__global__ void __launch_bounds__(S::Full::T, 1) grouped_weights(const GroupedParams p) {
+  using C = typename S::Full;
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+  // slots: tiles of one group's rows times groups
+  const Spot x = spot_of<S::kParts>(blockIdx.x, p.slots, p.tiles_n, p.band);
+  if (x.parts == 0) return;
+  const int per = p.slots / p.groups, g = x.tm / per;
+  const int m0 = (x.tm - g * per) * C::BM, n0 = x.tn * C::BN;
+  if constexpr (S::kParts > 1) {
+    if (x.parts == 4)
+      return weights_tile<T, O, typename S::Corner, GATHER>(
+          p, smem, g, m0 + (x.part >> 1) * S::Corner::BM, n0 + (x.part & 1) * S::Corner::BN);
+    if (x.parts == 2)
+      return weights_tile<T, O, typename S::Half, GATHER>(p, smem, g, m0 + x.part * S::Half::BM,
+                                                          n0);
+  }
+  weights_tile<T, O, C, GATHER>(p, smem, g, m0, n0);
 }
 
 // ------------------------------------------------------------- few rows
@@ -682,10 +840,10 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) grouped_few(const GroupedPa
   using F = FewTile<RM, RN>;
   __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const TileIndex ti = tile_of_block(blockIdx.x, gridDim.x, p.slots, p.tiles_n, p.band);
-  const Place at = place_of(p, ti.tm, F::BM);
-  if (at.count <= 0 || at.group == p.groups) return;
-  const int n0 = ti.tn * F::BN;
+  const GroupSpot s = group_spot<1>(p, blockIdx.x, F::BM);
+  if (s.spot.parts == 0 || s.at.group == p.groups) return;
+  const Place at = s.at;
+  const int n0 = s.spot.tn * F::BN;
   few_tile<T, RM, RN>(p, at, n0, (const T*)p.p + at.group * p.p_group, sums, w, lane);
   // (a thread stores what it added itself)
   for (int x = tid; x < RM * RN * 64; x += F::T) {

@@ -18,7 +18,6 @@ constexpr int64_t kMaxExtent = (int64_t)1 << 21;     // n, k, strides between ro
 constexpr int64_t kMaxGroupStride = (int64_t)1 << 42;
 constexpr int64_t kMaxGather = ((int64_t)1 << 30) - 1;   // elements a gathered operand spans
 constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
-constexpr int64_t kFill = 256;     // workgroups that occupy every CU
 
 bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
 bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
@@ -81,14 +80,20 @@ int check_grouped(const mfl_grouped_t& a, const void* A, const void* B, const in
   return MFL_OK;
 }
 
-// slots of `bm`-place tiles over the groups and what is behind them
-int64_t tile_slots(int64_t places, int64_t groups, int64_t bm) { return places / bm + groups + 1; }
+// `bm`-place tiles over the groups and what is behind them, at most; the
+// kernels number the tiles of few groups without gaps, those of more with
+// empty ones between (group_spot)
+int64_t tile_slots(int64_t places, int64_t groups, int64_t bm) {
+  const int64_t held = groups < kExact && places < groups + 1 ? places : groups + 1;
+  return places / bm + held;
+}
 
 struct Choice {
   int algo;
   KernelRef kernel;
   int64_t slots, tiles_n;
-  int64_t blocks() const { return slots * tiles_n; }
+  // workgroups; cutting the last round's tiles adds less than a round
+  int64_t blocks() const { return slots * tiles_n + (kernel.parts > 1 ? kFill : 0); }
 };
 
 Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
@@ -112,16 +117,13 @@ Choice choose(const mfl_grouped_t& a) {
   return with(few_kernel(bf16, f32, rm, rn), algo, a, a.n);
 }
 
-// the walk over tiles: bands of this many slots (tile_of_block).  FEW: the
-// tiles of one group, which read the same weights, follow each other.
-int band_of(const Choice& c) {
-  return c.algo == kFew ? (int)c.slots : c.algo == kTile256 ? 4 : 8;
-}
-
+// The walk over tiles: bands of this many slots.  FEW goes down each column,
+// so that the tiles of one group, which read the same weights, follow each
+// other.
 void place(GroupedParams& p, const Choice& c) {
   p.slots = (int)c.slots;
   p.tiles_n = (int)c.tiles_n;
-  p.band = band_of(c);
+  p.band = c.algo == kFew ? 0 : c.algo == kTile256 ? 4 : 8;
 }
 
 struct Backward {

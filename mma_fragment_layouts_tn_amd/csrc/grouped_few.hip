@@ -30,25 +30,25 @@ KernelRef count_kernel(bool i64, int groups) {
                                       : (const void*)group_count<int32_t, 256>
                   : i64         ? (const void*)group_count<int64_t, kMaxGroups>
                                 : (const void*)group_count<int32_t, kMaxGroups>;
-  return {f, kSortThreads, 0, 0};
+  return {f, kSortThreads};
 }
 KernelRef place_kernel(bool i64, int groups) {
   const void* f = groups <= 256 ? i64 ? (const void*)group_place<int64_t, 256>
                                       : (const void*)group_place<int32_t, 256>
                   : i64         ? (const void*)group_place<int64_t, kMaxGroups>
                                 : (const void*)group_place<int32_t, kMaxGroups>;
-  return {f, kSortThreads, 0, 0};
+  return {f, kSortThreads};
 }
 KernelRef combine_kernel(bool bf16, bool f32) {
   const void* f = f32 ? bf16 ? (const void*)combine_sum<__bf16, float>
                              : (const void*)combine_sum<_Float16, float>
                   : bf16 ? (const void*)combine_sum<__bf16, __bf16>
                          : (const void*)combine_sum<_Float16, _Float16>;
-  return {f, kCombineThreads, 0, 0};
+  return {f, kCombineThreads};
 }
 KernelRef combine_grad_kernel(bool bf16) {
   return {bf16 ? (const void*)combine_gradient<__bf16> : (const void*)combine_gradient<_Float16>,
-          kCombineThreads, 0, 0};
+          kCombineThreads};
 }
 }  // namespace grp
 }  // namespace mfl

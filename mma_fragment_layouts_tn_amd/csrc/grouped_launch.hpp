@@ -17,7 +17,8 @@ struct GroupedParams {
   int m, n, k;                 // extents; m or k is the group's places
   int ldp, ldq, ldd;
   int p_rows, q_rows;          // rows that a gathered operand has
-  int slots, tiles_n, band;    // tiles along m (of all groups), along n; order
+  int slots, tiles_n, band;    // tiles along m (of all groups, at most), along n; order (0: down
+                               // each column)
   int64_t p_group, d_group;
 };
 
@@ -59,10 +60,13 @@ struct CombineRows {
 };
 
 constexpr int kMaxGroups = 4096;
+constexpr int kExact = 256;    // groups whose tiles are numbered without gaps, fewer than
+constexpr int kFill = 256;     // workgroups that occupy every CU
 
 struct KernelRef {
   const void* fn;
-  int threads, bm, bn;
+  int threads, bm = 0, bn = 0;
+  int parts = 1;               // that a tile may be cut into
 };
 
 // kernels by type and size of tile, each in a source of its own

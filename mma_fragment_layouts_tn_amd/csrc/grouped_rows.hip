@@ -7,13 +7,14 @@
 namespace mfl {
 namespace grp {
 namespace {
-template <class T, class O, class C, bool PT>
+template <class T, class O, class S, bool PT>
 KernelRef ref() {
-  return {(const void*)grouped_rows<T, O, C, PT>, C::T, C::BM, C::BN};
+  return {(const void*)grouped_rows<T, O, S, PT>, S::Full::T, S::Full::BM, S::Full::BN,
+          S::kParts};
 }
 template <class T, class O, bool PT>
 KernelRef by_tile(int algo) {
-  return algo == kTile256 ? ref<T, O, Tile256, PT>() : ref<T, O, Tile128, PT>();
+  return algo == kTile256 ? ref<T, O, Tiles256, PT>() : ref<T, O, Tiles128, PT>();
 }
 }  // namespace
 

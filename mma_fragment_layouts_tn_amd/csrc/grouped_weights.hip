@@ -7,15 +7,15 @@
 namespace mfl {
 namespace grp {
 namespace {
-template <class T, class O, class C>
+template <class T, class O, class S>
 KernelRef ref(bool gathered) {
-  return {gathered ? (const void*)grouped_weights<T, O, C, true>
-                   : (const void*)grouped_weights<T, O, C, false>,
-          C::T, C::BM, C::BN};
+  return {gathered ? (const void*)grouped_weights<T, O, S, true>
+                   : (const void*)grouped_weights<T, O, S, false>,
+          S::Full::T, S::Full::BM, S::Full::BN, S::kParts};
 }
 template <class T, class O>
 KernelRef by_tile(int algo, bool gathered) {
-  return algo == kTile256 ? ref<T, O, Tile256>(gathered) : ref<T, O, Tile128>(gathered);
+  return algo == kTile256 ? ref<T, O, Weights256>(gathered) : ref<T, O, Tiles128>(gathered);
 }
 }  // namespace
 
