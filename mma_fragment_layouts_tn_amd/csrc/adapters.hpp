@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_few(const AdapterP
   using F = FewTile<RM, RN>;
   __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const Spot s = spot_of<1>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.slots);
+  const Spot s = spot_of<1>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.slots, INT_MAX);
   const Place at{0, s.tm * F::BM, min(p.g.places - s.tm * F::BM, F::BM)};
   const int n0 = s.tn * F::BN;
   few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p, sums, w, lane);
@@ -247,7 +247,7 @@ template <class T, class O, class S>
 __global__ void __launch_bounds__(S::Full::T, 1) adapters_rows(const AdapterParams p) {
   using C = typename S::Full;
   __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
-  const Spot s = spot_of<S::kParts>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.band);
+  const Spot s = spot_of<S::kParts>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.band, INT_MAX);
   if (s.parts == 0) return;
   const Place at{0, s.tm * C::BM, min(p.g.places - s.tm * C::BM, C::BM)};
   by_rows<S>(s, at, [&](auto c, const Place& x) {

@@ -231,9 +231,10 @@ struct SortPlan {
 };
 SortPlan plan_sort(const mfl_group_rows_t& a) {
   SortPlan r;
-  const int64_t per = ceil_div(a.count, 128);
-  r.chunk = ceil_div(a.count <= 4096 ? a.count : per > 4096 ? per : 4096, 512) * 512;
-  if (r.chunk == 0) r.chunk = 512;
+  // 16 waves of up to 256 choices, or 4 for many groups (sort_waves)
+  const int64_t wide = a.groups <= 256 ? 1024 : 256, unit = 4 * wide;
+  r.chunk = a.count <= unit ? ceil_div(a.count > 0 ? a.count : 1, wide) * wide
+                            : unit * (a.count > 256 * unit ? ceil_div(a.count, 256 * unit) : 1);
   r.blocks = a.count ? ceil_div(a.count, r.chunk) : 1;
   r.bytes = r.blocks > 1 ? 4 * r.blocks * (a.groups + 1) : 0;
   return r;

@@ -30,14 +30,14 @@ KernelRef count_kernel(bool i64, int groups) {
                                       : (const void*)group_count<int32_t, 256>
                   : i64         ? (const void*)group_count<int64_t, kMaxGroups>
                                 : (const void*)group_count<int32_t, kMaxGroups>;
-  return {f, kSortThreads};
+  return {f, 64 * sort_waves(groups)};
 }
 KernelRef place_kernel(bool i64, int groups) {
   const void* f = groups <= 256 ? i64 ? (const void*)group_place<int64_t, 256>
                                       : (const void*)group_place<int32_t, 256>
                   : i64         ? (const void*)group_place<int64_t, kMaxGroups>
                                 : (const void*)group_place<int32_t, kMaxGroups>;
-  return {f, kSortThreads};
+  return {f, 64 * sort_waves(groups)};
 }
 KernelRef combine_kernel(bool bf16, bool f32) {
   const void* f = f32 ? bf16 ? (const void*)combine_sum<__bf16, float>

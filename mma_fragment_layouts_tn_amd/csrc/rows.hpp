@@ -12,14 +12,22 @@ namespace grp {
 
 // ------------------------------------------------------------ group_rows
 // A stable counting sort.  Choices go to workgroups in chunks, within one to
-// its eight waves in runs, so that (group, workgroup, wave, position) is the
-// order of the places: every wave counts its run, the counts before its own
-// in that order are where its first choice of each group goes, and a second
-// walk over the run gives each choice the number of equal ones before it.
-// Nothing depends on the order that waves run in.  Memory traffic is the
-// choices twice and the results once (524,288 of them: 8 MB); what bounds it
-// is the walk, 64 choices per wave at a time.
-constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
+// its W waves in runs, so that (group, workgroup, wave, position) is the order
+// of the places: every wave counts its run, the counts before its own in that
+// order are where its first choice of each group goes, and a second walk over
+// the run gives each choice the number of equal ones before it.  Nothing
+// depends on the order that waves run in.  Up to one chunk that is one launch;
+// more chunks are counted by a launch before.
+//
+// Memory traffic is the choices twice and the results once (524,288 of them:
+// 8 MB, 2 us); what bounds it is latency, of the walks (64 choices per wave at
+// a time, their loads eight times that) and of the sums over chunks (every
+// workgroup's, kSumAhead chunks at a time).
+constexpr int kWalk = 8;          // loads of 64 choices under way
+constexpr int kSumAhead = 16;
+
+// waves of a workgroup: their counts of G groups fit LDS
+constexpr int sort_waves(int G) { return G <= 256 ? 16 : 4; }
 
 template <class I>
 __device__ __forceinline__ int key_of(const void* ids, int64_t c, int groups) {
@@ -27,73 +35,109 @@ __device__ __forceinline__ int key_of(const void* ids, int64_t c, int groups) {
   return x >= 0 && x < groups ? (int)x : groups;
 }
 
+// f(first choice of 64, the lane's key) over [a, b), 64 apart
+template <class I, class F>
+__device__ __forceinline__ void walk(const SortParams& p, int64_t a, int64_t b, int lane, F f) {
+  for (int64_t c = a; c < b; c += 64 * kWalk) {
+    int key[kWalk];
+#pragma unroll
+    for (int s = 0; s < kWalk; ++s) {
+      const int64_t x = c + 64 * s + lane;
+      key[s] = x < b ? key_of<I>(p.ids, x, p.groups) : 0;
+    }
+#pragma unroll
+    for (int s = 0; s < kWalk; ++s)
+      if (c + 64 * s < b) f(c + 64 * s, key[s]);
+  }
+}
+
 struct Run {
   int64_t first, end;     // this wave's choices
 };
+template <int W>
 __device__ __forceinline__ Run run_of(const SortParams& p, int w) {
   const int64_t a = (int64_t)blockIdx.x * p.chunk, b = min(a + p.chunk, p.count);
-  const int64_t per = p.chunk / kSortWaves;
+  const int64_t per = p.chunk / W;
   return Run{min(a + w * per, b), min(a + (w + 1) * per, b)};
 }
 
 // counts of a chunk, per group (the last: no group)
-template <class I, int G>
-__global__ void __launch_bounds__(kSortThreads) group_count(const SortParams p) {
+template <class I, int G, int W = sort_waves(G)>
+__global__ void __launch_bounds__(64 * W) group_count(const SortParams p) {
   __shared__ int hist[G + 1];
-  const int tid = threadIdx.x;
-  for (int g = tid; g <= p.groups; g += kSortThreads) hist[g] = 0;
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int g = tid; g <= p.groups; g += 64 * W) hist[g] = 0;
   __syncthreads();
-  const int64_t a = (int64_t)blockIdx.x * p.chunk, b = min(a + p.chunk, p.count);
-  for (int64_t c = a + tid; c < b; c += kSortThreads)
-    atomicAdd(&hist[key_of<I>(p.ids, c, p.groups)], 1);
+  const Run run = run_of<W>(p, tid >> 6);
+  walk<I>(p, run.first, run.end, lane, [&](int64_t c, int key) {
+    if (c + lane < run.end) atomicAdd(&hist[key], 1);
+  });
   __syncthreads();
-  for (int g = tid; g <= p.groups; g += kSortThreads)
+  for (int g = tid; g <= p.groups; g += 64 * W)
     p.table[(int64_t)blockIdx.x * (p.groups + 1) + g] = hist[g];
 }
 
-template <class I, int G>
-__global__ void __launch_bounds__(kSortThreads) group_place(const SortParams p) {
+template <class I, int G, int W = sort_waves(G)>
+__global__ void __launch_bounds__(64 * W) group_place(const SortParams p) {
+  constexpr int T = 64 * W;
   // hist[w][g]: wave w's choices of group g, then the place of its next one
-  __shared__ int hist[kSortWaves][G + 1];
-  __shared__ int start[G + 1];
-  __shared__ int sums[kSortWaves];
+  __shared__ int hist[W][G + 1];
+  __shared__ int before[G + 1], all[G + 1];   // in the chunks before, in all of them
+  __shared__ int sums[W];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = p.groups + 1;
-  for (int g = tid; g < n; g += kSortThreads)
+  for (int g = tid; g < n; g += T) {
+    before[g] = all[g] = 0;
 #pragma unroll
-    for (int v = 0; v < kSortWaves; ++v) hist[v][g] = 0;
+    for (int v = 0; v < W; ++v) hist[v][g] = 0;
+  }
   __syncthreads();
-  const Run run = run_of(p, w);
-  for (int64_t c = run.first + lane; c < run.end; c += 64)
-    atomicAdd(&hist[w][key_of<I>(p.ids, c, p.groups)], 1);
+  const Run run = run_of<W>(p, w);
+  walk<I>(p, run.first, run.end, lane, [&](int64_t c, int key) {
+    if (c + lane < run.end) atomicAdd(&hist[w][key], 1);
+  });
+  if (gridDim.x > 1) {
+    // the threads as rows of columns of the table, as many rows as there are
+    const int wide = (n + 63) / 64 * 64, rows = T / wide > 1 ? T / wide : 1;
+    const int blocks = gridDim.x, me = blockIdx.x;
+    for (int g = tid % wide; g < n && tid < rows * wide; g += T) {
+      int sum = 0, mine = 0;
+      for (int b0 = tid / wide; b0 < blocks; b0 += rows * kSumAhead) {
+        int t[kSumAhead];
+#pragma unroll
+        for (int x = 0; x < kSumAhead; ++x) {
+          const int b = b0 + x * rows;
+          t[x] = p.table[(int64_t)min(b, blocks - 1) * n + g];
+          t[x] = b < blocks ? t[x] : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kSumAhead; ++x) {
+          sum += t[x];
+          mine += b0 + x * rows < me ? t[x] : 0;
+        }
+      }
+      atomicAdd(&all[g], sum);
+      atomicAdd(&before[g], mine);
+    }
+  }
   __syncthreads();
-  // start[g]: choices of the groups before g; before: those of g in earlier
-  // chunks.  Groups in runs of consecutive ones per thread, then a scan over
-  // the threads.
-  const int per = (n + kSortThreads - 1) / kSortThreads;
+  // Groups in runs of consecutive ones per thread, then a scan over the
+  // threads: the places of the groups before.
+  const int per = (n + T - 1) / T;
   int mine = 0;
   for (int x = 0; x < per; ++x) {
     const int g = tid * per + x;
     if (g >= n) break;
-    int before = 0, all = 0;
-    if (gridDim.x == 1) {
-#pragma unroll
-      for (int v = 0; v < kSortWaves; ++v) all += hist[v][g];
-    } else {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int t = p.table[(int64_t)b * n + g];
-        all += t;
-        before += b < (int)blockIdx.x ? t : 0;
-      }
-    }
-    start[g] = mine;        // within the thread's run, so far
-    mine += all;
+    int at = before[g], count = all[g];
     // this chunk's waves in turn
 #pragma unroll
-    for (int v = 0; v < kSortWaves; ++v) {
+    for (int v = 0; v < W; ++v) {
       const int t = hist[v][g];
-      hist[v][g] = before;
-      before += t;
+      hist[v][g] = at;
+      at += t;
     }
+    if (gridDim.x == 1) count = at;
+    before[g] = mine;       // from here on: within the thread's run, so far
+    mine += count;
   }
   int scan = mine;          // inclusive over the wave's lanes
 #pragma unroll
@@ -108,17 +152,16 @@ __global__ void __launch_bounds__(kSortThreads) group_place(const SortParams p) 
   for (int x = 0; x < per; ++x) {
     const int g = tid * per + x;
     if (g >= n) break;
-    const int s = start[g] + base;
+    const int s = before[g] + base;
     if (blockIdx.x == 0) p.offsets[g] = s;
 #pragma unroll
-    for (int v = 0; v < kSortWaves; ++v) hist[v][g] += s;
+    for (int v = 0; v < W; ++v) hist[v][g] += s;
   }
   __syncthreads();
   volatile int* next = hist[w];
-  for (int64_t c0 = run.first; c0 < run.end; c0 += 64) {
+  walk<I>(p, run.first, run.end, lane, [&](int64_t c0, int key) {
     const int64_t c = c0 + lane;
     const bool in = c < run.end;
-    const int key = in ? key_of<I>(p.ids, c, p.groups) : 0;
     // lanes of the same key
     unsigned long long same = __ballot(in);
     for (int bit = 0; bit < p.bits; ++bit) {
@@ -126,16 +169,16 @@ __global__ void __launch_bounds__(kSortThreads) group_place(const SortParams p) 
       const unsigned long long m = __ballot(set);
       same &= set ? m : ~m;
     }
-    const int before = __popcll(same & ((1ull << lane) - 1));
-    const int at = in ? next[key] + before : 0;
+    const int earlier = __popcll(same & ((1ull << lane) - 1));
+    const int at = in ? next[key] + earlier : 0;
     // (a wave's LDS operations are done in order: the read above, this write,
     // the next round's read)
-    if (in && before == 0) next[key] = at + __popcll(same);
+    if (in && earlier == 0) next[key] = at + __popcll(same);
     if (in) {
-      p.rows[at] = (int)(c / p.top);
+      p.rows[at] = (int)((unsigned)c / (unsigned)p.top);
       p.slots[c] = key < p.groups ? at : -1;
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------- combine_rows
