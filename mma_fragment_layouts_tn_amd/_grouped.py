@@ -83,9 +83,13 @@ def bind(lib: ctypes.CDLL, check) -> None:
 
 
 # ---------------------------------------------------------------- marshalling
+def _run(stream, *tensors) -> _Run:
+    return _Run([t for t in tensors if t is not None], stream)
+
+
 def _call(run: _Run, fn, *args) -> None:
     """fn, which takes no workspace, on the tensors' device."""
-    if torch.cuda.current_device() != run.device.index:
+    if torch._C._cuda_getDevice() != run.device.index:
         with torch.cuda.device(run.device):
             rc = fn(*args, run.handle)
     else:
@@ -94,33 +98,47 @@ def _call(run: _Run, fn, *args) -> None:
         _check(rc)
 
 
+def _call_with(run: _Run, fn, need: int, *args) -> None:
+    """The same for a function with a workspace of `need` bytes."""
+    ws = run.empty((need,), torch.uint8, result=False) if need else None
+    _call(run, fn, *args, None if ws is None else ws.data_ptr(), need)
+
+
+def _new(run: _Run, like: torch.Tensor, shape, dtype: Optional[torch.dtype]) -> torch.Tensor:
+    """A new tensor of `like`'s type, or of dtype."""
+    if run.other is not None:
+        return run.empty(shape, like.dtype if dtype is None else dtype)
+    return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+
+
 def _matrix(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2:
+    s = t.stride()
+    if len(s) != 2:
         raise ValueError(f"{name} must be 2-D")
     r, c = t.shape
-    if c > 1 and t.stride(1) != 1:
+    if s[1] != 1 and c > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t.stride(0) if r > 1 else c
+    return s[0] if r > 1 else c
 
 
 def _matrices(t: torch.Tensor, name: str) -> Tuple[int, int]:
     """Row and matrix stride of a 3-D tensor with contiguous rows."""
-    if t.dim() != 3:
+    s = t.stride()
+    if len(s) != 3:
         raise ValueError(f"{name} must be 3-D")
     g, r, c = t.shape
-    if c > 1 and t.stride(2) != 1:
+    if s[2] != 1 and c > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return (t.stride(1) if r > 1 else c), (t.stride(0) if g > 1 else 0)
+    return (s[1] if r > 1 else c), (s[0] if g > 1 else 0)
 
 
 def _numbers(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) -> None:
     if t is None:
         return
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be int32")
-    if t.dim() != 1 or (t.shape[0] > 1 and t.stride(0) != 1) or \
-            (count is not None and t.shape[0] != count):
+    if t.dim() != 1 or not t.is_contiguous() or (count is not None and t.shape[0] != count):
         raise ValueError(f"{name} must be contiguous" +
                          ("" if count is None else f", of {count} entries"))
 
@@ -170,20 +188,22 @@ def group_rows(ids: torch.Tensor, groups: int, *, stream=None):
         raise ValueError("ids must be contiguous")
     top = ids.shape[1] if ids.dim() == 2 else 1
     a = GroupRowsArgs(_I64 if ids.dtype == torch.int64 else _I32, ids.numel(), max(top, 1), groups)
-    run = _Run([ids], stream)
     if groups < 1:
         raise ValueError("there must be a group")
-    rows = run.empty((ids.numel(),), torch.int32)
-    offsets = run.empty((groups + 1,), torch.int32)
-    slots = run.empty(ids.shape, torch.int32)
-    ptrs = tuple(_ptr(t) for t in (ids, rows, offsets, slots))
-
-    def need():
-        n = _i64(0)
-        _check(_lib.group_rows_plan(a, *ptrs, n))
-        return n.value
-
-    run.call(_lib.group_rows, a, ptrs, need)
+    run = _Run([ids], stream)
+    # (one allocation: it takes longer than the kernels for a few choices)
+    n = ids.numel()
+    rows, offsets, slots = run.empty((2 * n + groups + 1,), torch.int32).split_with_sizes(
+        (n, groups + 1, n))
+    if ids.dim() == 2:
+        slots = slots.view(ids.shape)
+    ptrs = _ptr(ids), _ptr(rows), _ptr(offsets), _ptr(slots)
+    need = 0
+    if n > 1024:                  # (up to as many one workgroup does without)
+        b = _i64(0)
+        _check(_lib.group_rows_plan(a, *ptrs, b))
+        need = b.value
+    _call_with(run, _lib.group_rows, need, a, *ptrs)
     return rows, offsets, slots
 
 
@@ -211,9 +231,9 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, *,
         out_dtype = D.dtype
     out = _type(out_dtype, A.dtype, "D")
     a = _grouped_args(A, B, offsets, rows, out, algo, places, n if D is None else _matrix(D, "D"))
-    run = _Run([t for t in (A, B, offsets, rows, D) if t is not None], stream)
+    run = _run(stream, A, B, offsets, rows, D)
     if D is None:
-        D = run.empty((places, n), A.dtype if out_dtype is None else out_dtype)
+        D = _new(run, A, (places, n), out_dtype)
     _call(run, _lib.gemm_tn_grouped, a, _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), _ptr(D))
     return D
 
@@ -248,9 +268,9 @@ def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     f = _grouped_args(A, B, offsets, rows, out, algo, places, _matrix(dD, "dD"))
     k, n = B.shape[2], B.shape[1]
     a = GroupedGradArgs(f, k, k, n * k)
-    run = _Run([t for t in (dD, A, B, offsets, rows) if t is not None], stream)
-    dA = run.empty((places, k), A.dtype)
-    dB = run.empty(B.shape, A.dtype if dB_dtype is None else dB_dtype)
+    run = _run(stream, dD, A, B, offsets, rows)
+    dA = _new(run, A, (places, k), None)
+    dB = _new(run, B, B.shape, dB_dtype)
     _call(run, _lib.gemm_tn_grouped_backward, a, _ptr(dD), _ptr(A), _ptr(B), _ptr(offsets),
           _ptr(rows), _ptr(dA), _ptr(dB))
     return dA, dB
@@ -291,9 +311,9 @@ def combine_rows(X: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.T
         out_dtype = out.dtype
     a = _combine_args(X, slots, weights, _type(out_dtype, X.dtype, "out"),
                       n if out is None else _matrix(out, "out"))
-    run = _Run([t for t in (X, slots, weights, out) if t is not None], stream)
+    run = _run(stream, X, slots, weights, out)
     if out is None:
-        out = run.empty((slots.shape[0], n), X.dtype if out_dtype is None else out_dtype)
+        out = _new(run, X, (slots.shape[0], n), out_dtype)
     _call(run, _lib.combine_rows, a, _ptr(X), _ptr(slots), _ptr(weights), _ptr(out))
     return out
 
@@ -313,9 +333,9 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
         raise ValueError("dout must be (tokens, N)")
     a = _combine_args(X, slots, weights, _TYPES.get(X.dtype, 0), _matrix(dout, "dout"))
     _numbers(rows, "rows", X.shape[0])
-    run = _Run([t for t in (dout, X, slots, weights, rows) if t is not None], stream)
-    dX = run.empty(X.shape, X.dtype)
-    dw = None if weights is None else run.empty(weights.shape, torch.float32)
+    run = _run(stream, dout, X, slots, weights, rows)
+    dX = _new(run, X, X.shape, None)
+    dw = None if weights is None else _new(run, weights, weights.shape, None)
     _call(run, _lib.combine_rows_backward, a, X.shape[1], _ptr(dout), _ptr(X), _ptr(slots),
           _ptr(rows), _ptr(weights), _ptr(dX), _ptr(dw))
     return dX, dw
@@ -373,17 +393,15 @@ def gemm_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Te
         out_dtype = D.dtype
     a = _adapters_args(x, W, A, B, offsets, rows, scale, _type(out_dtype, x.dtype, "D"), algo,
                        n if D is None else _matrix(D, "D"))
-    run = _Run([t for t in (x, W, A, B, offsets, rows, scale, D) if t is not None], stream)
+    run = _run(stream, x, W, A, B, offsets, rows, scale, D)
     if D is None:
-        D = run.empty((m, n), x.dtype if out_dtype is None else out_dtype)
-    ptrs = tuple(_ptr(t) for t in (x, W, A, B, offsets, rows, scale, D))
-
-    def need():
-        b = _i64(0)
-        _check(_lib.gemm_tn_adapters_plan(a, *ptrs, None, b))
-        return b.value
-
-    run.call(_lib.gemm_tn_adapters, a, ptrs, need)
+        D = _new(run, x, (m, n), out_dtype)
+    ptrs = (_ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), _ptr(scale), _ptr(D))
+    b = _i64(0)
+    rc = _lib.gemm_tn_adapters_plan(a, *ptrs, None, b)
+    if rc:
+        _check(rc)
+    _call_with(run, _lib.gemm_tn_adapters, b.value, a, *ptrs)
     return D
 
 

@@ -36,43 +36,51 @@ constexpr int pieces_of() {
   return sizeof(O) == 4 ? 3 : 2;
 }
 
-// s_g h of a tile of one group's places.  p.g: q = x, p = A, n = rank.
+// Four values of s_g h of a place, columns n .. n + 3, and the place's group.
+template <class T>
+__device__ __forceinline__ void keep(const AdapterParams& p, int place, int group, int n,
+                                     floatx4 h) {
+  h *= p.scale ? p.scale[group] : 1.0f;
+  if (n == 0) p.owner[place] = group;
+  if (p.h) {
+    *(floatx4*)(p.h + (int64_t)place * p.rank + n) = h;
+    return;
+  }
+  typedef T vec4 __attribute__((ext_vector_type(4)));
+  for (int c = 0; c < p.pieces; ++c) {
+    vec4 y;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      y[v] = (T)h[v];
+      const float z = (float)y[v];
+      h[v] = not_finite(z) ? 0.0f : h[v] - z;
+    }
+    *(vec4*)((T*)p.hp + ((int64_t)place * p.pieces + c) * p.rank + n) = y;
+  }
+}
+
+// h of a tile of one group's places, few rows
 template <class T, int RM, int RN>
-__global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_down(const AdapterParams p) {
+__device__ __forceinline__ void down_few(const AdapterParams& p, floatx4* sums, int id) {
   using F = FewTile<RM, RN>;
-  __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const GroupSpot spot = group_spot<1>(p.g, blockIdx.x, F::BM);
-  if (spot.spot.parts == 0 || spot.at.group == p.g.groups) return;
+  const GroupSpot spot = group_spot<1>(p.down, id, F::BM);
+  if (spot.spot.parts == 0 || spot.at.group == p.down.groups) return;
   const Place at = spot.at;
   const int n0 = spot.spot.tn * F::BN;
-  few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p + at.group * p.g.p_group, sums, w, lane);
-  const float s = p.scale ? p.scale[at.group] : 1.0f;
-  if (n0 == 0)
-    for (int m = tid; m < at.count; m += F::T) p.owner[at.first + m] = at.group;
+  few_tile<T, RM, RN>(p.down, at, n0, (const T*)p.down.p + at.group * p.down.p_group, 0, p.down.k,
+                      sums, w, lane);
   // (a thread reads what it added itself)
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;
     const int m = 16 * i + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
-    if (m >= at.count || n >= p.rank) continue;
-    floatx4 h = sums[x] * s;
-    const int64_t place = at.first + m;
-    if (p.h) {
-      *(floatx4*)(p.h + place * p.rank + n) = h;
-      continue;
-    }
-    typedef T vec4 __attribute__((ext_vector_type(4)));
-    for (int c = 0; c < p.pieces; ++c) {
-      vec4 y;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        y[v] = (T)h[v];
-        const float z = (float)y[v];
-        h[v] = not_finite(z) ? 0.0f : h[v] - z;
-      }
-      *(vec4*)((T*)p.hp + (place * p.pieces + c) * p.rank + n) = y;
-    }
+    if (m < at.count && n < p.rank) keep<T>(p, at.first + m, at.group, n, sums[x]);
   }
+}
+template <class T, int RM, int RN>
+__global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_down(const AdapterParams p) {
+  __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
+  down_few<T, RM, RN>(p, sums, blockIdx.x);
 }
 
 // the group of a place that has one, else -1
@@ -86,41 +94,65 @@ __device__ __forceinline__ int row_at(const GroupedParams& p, int place) {
   return (unsigned)r < (unsigned)p.q_rows ? r : -1;
 }
 
-// Few rows: every thread adds its own results' low-rank terms, rank
-// multiplications each.
-template <class T, class O, int RM, int RN>
-__global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_few(const AdapterParams p) {
+// Few rows, first launch: the workgroups of the down projection, and those of
+// the shared product, which depend on nothing of theirs.  A tile's contraction
+// is shared out to `splits` workgroups, so that W is read by all CUs in wide
+// tiles (with a quarter of the columns per workgroup instead x is read four
+// times as often, and bounds the launch: 48 rows by 4096 x 4096 20 us).
+template <class T, int RM, int RN>
+__global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_first(const AdapterParams p) {
   using F = FewTile<RM, RN>;
   __shared__ floatx4 sums[kFewWaves * RM * RN * 64];
+  if ((int)blockIdx.x < p.down_blocks) return down_few<T, 1, 1>(p, sums, blockIdx.x);
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const Spot s = spot_of<1>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.slots, INT_MAX);
-  const Place at{0, s.tm * F::BM, min(p.g.places - s.tm * F::BM, F::BM)};
-  const int n0 = s.tn * F::BN;
-  few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p, sums, w, lane);
+  const int id = blockIdx.x - p.down_blocks, split = id % p.splits;
+  const int slot = id / p.splits % p.g.slots, n0 = id / p.splits / p.g.slots * F::BN;
+  const Place at{0, slot * F::BM, min(p.g.places - slot * F::BM, F::BM)};
+  const int from = split * p.part_k;
+  few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p, from, min(from + p.part_k, p.g.k), sums, w,
+                      lane);
+  float* part = p.part + (int64_t)split * p.g.places * p.g.n;
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;
     const int m = 16 * i + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
-    if (m >= at.count || n >= p.g.n) continue;
-    const int place = at.first + m, g = owner_of(p, place), row = row_at(p.g, place);
-    floatx4 y = sums[x];
-    if (g >= 0) {
-      const float* h = p.h + (int64_t)place * p.rank;
-      const T* b = (const T*)p.up + g * p.up_group + (int64_t)n * p.ldup;
-      floatx4 low{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int c = 0; c < p.rank; c += 8) {
-        const floatx4 h0 = *(const floatx4*)(h + c), h1 = *(const floatx4*)(h + c + 4);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const Vec8<T> bv = att::load8(b + v * p.ldup + c);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            low[v] = __builtin_fmaf(e < 4 ? h0[e % 4] : h1[e % 4], (float)bv[e], low[v]);
-        }
-      }
-      y += low;
-    }
-    if (row >= 0) Out<O>::store4((O*)p.g.d + (int64_t)row * p.g.ldd + n, y);
+    if (m < at.count && n < p.g.n)
+      *(floatx4*)(part + (int64_t)(at.first + m) * p.g.n + n) = sums[x];
   }
+}
+
+// Second launch: a thread adds the parts of four results in order, and their
+// low-rank terms, rank multiplications each.
+constexpr int kJoinThreads = 256;
+template <class T, class O>
+__global__ void __launch_bounds__(kJoinThreads) adapters_join(const AdapterParams p) {
+  const int64_t x = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  const int wide = p.g.n / 4, place = (int)(x / wide), n = 4 * (int)(x - (int64_t)place * wide);
+  if (place >= p.g.places) return;
+  const int64_t plane = (int64_t)p.g.places * p.g.n;
+  const float* part = p.part + (int64_t)place * p.g.n + n;
+  floatx4 y{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) y += *(const floatx4*)(part + s * plane);
+  const int g = owner_of(p, place), row = row_at(p.g, place);
+  if (row < 0) return;
+  if (g >= 0) {
+    const float* h = p.h + (int64_t)place * p.rank;
+    const T* b = (const T*)p.up + g * p.up_group + (int64_t)n * p.ldup;
+    floatx4 low{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+    for (int c = 0; c < p.rank; c += 8) {
+      const floatx4 h0 = *(const floatx4*)(h + c), h1 = *(const floatx4*)(h + c + 4);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const Vec8<T> bv = att::load8(b + v * p.ldup + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          low[v] = __builtin_fmaf(e < 4 ? h0[e % 4] : h1[e % 4], (float)bv[e], low[v]);
+      }
+    }
+    y += low;
+  }
+  Out<O>::store4((O*)p.g.d + (int64_t)row * p.g.ldd + n, y);
 }
 
 // what adapters_rows leaves out: the pairs of B's numbers of which one is not
@@ -145,6 +177,52 @@ __device__ __forceinline__ floatx4 rest(const AdapterParams& p, int place, int n
   return low;
 }
 
+// h of a tile of one group's places, many rows: x is read once per 64 columns
+// of the rank, and reading it is the work.  What bounds it is the latency of
+// what a CU can have under way (its LDS), so the tiles are small, to go to more
+// CUs, and the contraction is shared by kDownParts sets of two waves with
+// stages of their own.  5,001 rows of 4096, rank 64: 16 us; with 64 rows per
+// tile 19 (two sets) to 24 (four), straight from memory (down_few) 29.
+constexpr int kDownParts = 4;
+using DownTile = Tile<32, 64, 2, 1, 3>;
+template <class T>
+__global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_rows(
+    const AdapterParams p) {
+  using C = DownTile;
+  __shared__ __attribute__((aligned(1024))) char smem[kDownParts * C::LDS];
+  const int lane = threadIdx.x & 63, part = uniform(threadIdx.x / C::T),
+            w = uniform(threadIdx.x >> 6) % C::W;
+  const GroupSpot x = group_spot<1>(p.down, blockIdx.x, C::BM);
+  if (x.spot.parts == 0 || x.at.group == p.down.groups) return;
+  const int n0 = x.spot.tn * C::BN;
+  const int steps = ((p.down.k + 63) / 64 + kDownParts - 1) / kDownParts;
+  const int from = 64 * steps * part;         // (beyond k: out of range, zeros)
+  GroupedParams d = p.down;
+  d.k -= from;
+  d.q = (const T*)d.q + from;
+  RowsSource<C, false> src;
+  src.init(d, x.at, n0, (const T*)d.p + x.at.group * d.p_group + from, w, lane);
+  floatx4 acc[C::RM][C::RN];
+  product<T, C, false, false>((lds_c)smem + part * C::LDS, steps, src, acc, w, lane);
+  floatx4* sums = (floatx4*)smem;
+  __syncthreads();
+  if (part > 0)
+#pragma unroll
+    for (int j = 0; j < C::RN; ++j)
+      sums[(((part - 1) * C::W + w) * C::RN + j) * 64 + lane] = acc[0][j];
+  __syncthreads();
+  const int m = 16 * w + (lane & 15);
+  if (part > 0 || m >= x.at.count) return;
+#pragma unroll
+  for (int j = 0; j < C::RN; ++j) {
+    floatx4 h = acc[0][j];
+#pragma unroll
+    for (int v = 1; v < kDownParts; ++v) h += sums[(((v - 1) * C::W + w) * C::RN + j) * 64 + lane];
+    const int n = n0 + column_of<true>(lane, j);
+    if (n < p.rank) keep<T>(p, x.at.first + m, x.at.group, n, h);
+  }
+}
+
 // Tiles through LDS.  The low-rank term of each run of places of one group is
 // a few matrix instructions more into the same sums, on fragments straight
 // from memory (a few KB that every workgroup of a row of tiles reads): rows
@@ -160,65 +238,103 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   const GroupedParams& g = p.g;
   RowsSource<C, false> src;
   src.init(g, Place{0, first, count}, n0, (const T*)g.p, w, lane);
+  // the groups of the wave's places, 64 a time (asked for ahead of the product)
+  const int m0 = first + (w % C::WM) * WROWS, nw = n0 + (w / C::WM) * 64;
+  int own[H];
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const int at = m0 + 64 * h + lane;
+    own[h] = lane < 16 * HM && at < first + count ? owner_of(p, at) : -1;
+  }
   floatx4 acc[C::RM][RN];
   product<T, C, false, false>((lds_c)smem, (g.k + 63) / 64, src, acc, w, lane);
 
-  const int m0 = first + (w % C::WM) * WROWS, nw = n0 + (w / C::WM) * 64;
   const int r = lane & 15, c8 = 8 * (lane >> 4);
   bool bad = false;       // something in B that is not finite
   tied<C>(acc);
+  // A run's operands for 32 columns of the rank: those of the next are on
+  // their way while one's are multiplied (where the registers hold two).
+  struct Operands {
+    u32x4_t b[RN], h[NPC][HM];
+  };
+  struct Step {
+    int a, b, group, c;   // places a .. b - 1 of 64, columns c ..; group < 0: none
+    unsigned long long starts;
+  };
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int at = m0 + 64 * h;
-    const int own =
-        lane < 16 * HM && at + lane < first + count ? owner_of(p, at + lane) : -1;
-    unsigned long long starts = __ballot(lane == 0 || own != __shfl_up(own, 1));
-    while (starts) {
-      const int a = __builtin_ctzll(starts);
-      starts &= starts - 1;
-      const int b = starts ? __builtin_ctzll(starts) : 64;
-      const int grp = __builtin_amdgcn_readlane(own, a);
-      if (grp < 0) continue;
+    const __amdgpu_buffer_rsrc_t rh =
+        buffer((const T*)p.hp + (int64_t)at * NPC * p.rank, kWhole);
+    auto load = [&](const Step& s) {
+      Operands x;
       const __amdgpu_buffer_rsrc_t rb =
-          buffer((const T*)p.up + grp * p.up_group + (int64_t)nw * p.ldup, kWhole);
-      const __amdgpu_buffer_rsrc_t rh =
-          buffer((const T*)p.hp + (int64_t)at * NPC * p.rank, kWhole);
-      for (int c0 = 0; c0 < p.rank; c0 += 32) {
-        const bool in = c0 + c8 < p.rank;
-        u32x4_t fp[RN], fq[NPC][HM];
+          buffer((const T*)p.up + max(s.group, 0) * p.up_group + (int64_t)nw * p.ldup, kWhole);
+      const int c = s.group < 0 ? p.rank : s.c + c8;
 #pragma unroll
-        for (int j = 0; j < RN; ++j) {
-          const int n = 16 * (r >> 2) + 4 * j + (r & 3);
-          fp[j] = __builtin_amdgcn_raw_buffer_load_b128(
-              rb, in && nw + n < g.n ? 2u * (n * p.ldup + c0 + c8) : kOutside, 0, 0);
+      for (int j = 0; j < RN; ++j) {
+        const int n = 16 * (r >> 2) + 4 * j + (r & 3);
+        x.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
+            rb, c < p.rank && nw + n < g.n ? 2u * (n * p.ldup + c) : kOutside, 0, 0);
+      }
+#pragma unroll
+      for (int v = 0; v < NPC; ++v)
+#pragma unroll
+        for (int i = 0; i < HM; ++i) {
+          const int m = 16 * i + r;
+          x.h[v][i] = __builtin_amdgcn_raw_buffer_load_b128(
+              rh,
+              c < p.rank && m >= s.a && m < s.b ? 2u * ((m * NPC + v) * p.rank + c) : kOutside, 0,
+              0);
+        }
+      return x;
+    };
+    auto use = [&](Operands& x) {
+#pragma unroll
+      for (int j = 0; j < RN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const unsigned u = x.b[j][e];
+          const bool z = not_finite<T>(u);
+          x.b[j][e] = z ? 0u : u;
+          bad |= z;
         }
 #pragma unroll
-        for (int x = 0; x < NPC; ++x)
+      for (int v = 0; v < NPC; ++v)
 #pragma unroll
-          for (int i = 0; i < HM; ++i) {
-            const int m = 16 * i + r;
-            fq[x][i] = __builtin_amdgcn_raw_buffer_load_b128(
-                rh, in && m >= a && m < b ? 2u * ((m * NPC + x) * p.rank + c0 + c8) : kOutside, 0,
-                0);
-          }
-        bool out = false;
+        for (int i = 0; i < HM; ++i)
 #pragma unroll
-        for (int j = 0; j < RN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const unsigned u = fp[j][e];
-            const bool z = not_finite<T>(u);
-            fp[j][e] = z ? 0u : u;
-            out |= z;
-          }
-        bad |= out;
-#pragma unroll
-        for (int x = 0; x < NPC; ++x)
-#pragma unroll
-          for (int i = 0; i < HM; ++i)
-#pragma unroll
-            for (int j = 0; j < RN; ++j)
-              Mma<T>::run(as16(fp[j], T()), as16(fq[x][i], T()), acc[4 * h + i][j]);
+          for (int j = 0; j < RN; ++j)
+            Mma<T>::run(as16(x.b[j], T()), as16(x.h[v][i], T()), acc[4 * h + i][j]);
+    };
+    auto advance = [&](Step s) {
+      if (s.group >= 0 && (s.c += 32) < p.rank) return s;
+      s.c = 0;
+      do {
+        if (!s.starts) {
+          s.group = -1;
+          return s;
+        }
+        s.a = __builtin_ctzll(s.starts);
+        s.starts &= s.starts - 1;
+        s.b = s.starts ? __builtin_ctzll(s.starts) : 64;
+        s.group = __builtin_amdgcn_readlane(own[h], s.a);
+      } while (s.group < 0);
+      return s;
+    };
+    Step s = advance(Step{0, 0, -1, 0, __ballot(lane == 0 || own[h] != __shfl_up(own[h], 1))});
+    if constexpr (NPC == 2) {
+      Operands x = load(s);
+      while (s.group >= 0) {
+        s = advance(s);
+        const Operands y = load(s);    // (of no step: nothing is read)
+        use(x);
+        x = y;
+      }
+    } else {
+      for (; s.group >= 0; s = advance(s)) {
+        Operands x = load(s);
+        use(x);
       }
     }
   }

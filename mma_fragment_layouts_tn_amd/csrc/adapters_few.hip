@@ -17,24 +17,29 @@ KernelRef down_by_size(int rm, int rn) {
   if (rn == 1) return rm == 4 ? down<T, 4, 1>() : rm == 2 ? down<T, 2, 1>() : down<T, 1, 1>();
   return rm == 4 ? down<T, 4, 2>() : rm == 2 ? down<T, 2, 2>() : down<T, 1, 2>();
 }
-template <class T, class O, int RM, int RN>
-KernelRef few() {
-  using F = FewTile<RM, RN>;
-  return {(const void*)adapters_few<T, O, RM, RN>, F::T, F::BM, F::BN};
+template <class T, int RM>
+KernelRef first() {
+  using F = FewTile<RM, 4>;
+  return {(const void*)adapters_first<T, RM, 4>, F::T, F::BM, F::BN};
 }
-template <class T, class O>
-KernelRef few_by_size(int rm, int rn) {
-  if (rn == 1) return rm == 4 ? few<T, O, 4, 1>() : rm == 2 ? few<T, O, 2, 1>() : few<T, O, 1, 1>();
-  return rm == 4 ? few<T, O, 4, 2>() : rm == 2 ? few<T, O, 2, 2>() : few<T, O, 1, 2>();
+template <class T>
+KernelRef first_by_size(int rm) {
+  return rm == 4 ? first<T, 4>() : rm == 2 ? first<T, 2>() : first<T, 1>();
 }
 }  // namespace
 
 KernelRef down_kernel(bool bf16, int rm, int rn) {
   return bf16 ? down_by_size<__bf16>(rm, rn) : down_by_size<_Float16>(rm, rn);
 }
-KernelRef adapters_few_kernel(bool bf16, bool f32, int rm, int rn) {
-  if (f32) return bf16 ? few_by_size<__bf16, float>(rm, rn) : few_by_size<_Float16, float>(rm, rn);
-  return bf16 ? few_by_size<__bf16, __bf16>(rm, rn) : few_by_size<_Float16, _Float16>(rm, rn);
+KernelRef adapters_first_kernel(bool bf16, int rm) {
+  return bf16 ? first_by_size<__bf16>(rm) : first_by_size<_Float16>(rm);
+}
+KernelRef adapters_join_kernel(bool bf16, bool f32) {
+  const void* f = f32 ? bf16 ? (const void*)adapters_join<__bf16, float>
+                             : (const void*)adapters_join<_Float16, float>
+                  : bf16 ? (const void*)adapters_join<__bf16, __bf16>
+                         : (const void*)adapters_join<_Float16, _Float16>;
+  return {f, kJoinThreads};
 }
 }  // namespace grp
 }  // namespace mfl

@@ -18,6 +18,11 @@ KernelRef by_tile(int algo) {
 }
 }  // namespace
 
+KernelRef down_rows_kernel(bool bf16) {
+  using C = DownTile;
+  return {bf16 ? (const void*)adapters_down_rows<__bf16> : (const void*)adapters_down_rows<_Float16>,
+          kDownParts * C::T, C::BM, C::BN};
+}
 KernelRef adapters_kernel(bool bf16, bool f32, int algo) {
   if (f32) return bf16 ? by_tile<__bf16, float>(algo) : by_tile<_Float16, float>(algo);
   return bf16 ? by_tile<__bf16, __bf16>(algo) : by_tile<_Float16, _Float16>(algo);

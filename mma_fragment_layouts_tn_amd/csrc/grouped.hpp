@@ -735,7 +735,9 @@ __global__ void __launch_bounds__(S::Full::T, 1) grouped_weights(const GroupedPa
 // memory.  The workgroup's eight waves share the contraction, U sub-steps of
 // 32 a time (64 U consecutive bytes of each row per wave); their sums are
 // added through LDS in the order of the waves.
-constexpr int kFewWaves = 8, kFewDepth = 4;
+constexpr int kFewWaves = 8;
+// sub-steps a time: two of those are in registers beside the sums
+constexpr int few_depth(int rm, int rn) { return rm + rn > 6 ? 2 : 4; }
 
 template <int RM, int RN>
 struct FewTile {
@@ -749,13 +751,13 @@ __device__ __forceinline__ att::Vec8<__bf16> as16(const u32x4_t& u, __bf16) {
   return __builtin_bit_cast(att::Vec8<__bf16>, u);
 }
 
-// q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
+// The contraction from `from` to k.  q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
 // sums[(i RN + j) * 64 + lane] holds the four values of atom (i, j).
 template <class T, int RM, int RN>
 __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const unsigned (&q_off)[RM],
                                             __amdgpu_buffer_rsrc_t rp, const unsigned (&p_off)[RN],
-                                            int k, floatx4* sums, int w, int lane) {
-  constexpr int U = kFewDepth, W = kFewWaves;
+                                            int from, int k, floatx4* sums, int w, int lane) {
+  constexpr int U = few_depth(RM, RN), W = kFewWaves;
   floatx4 acc[RM][RN];
 #pragma unroll
   for (int i = 0; i < RM; ++i)
@@ -790,7 +792,7 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
   // two parts in turn, so that one is on its way while the other is used
   Part a, b;
   const int step = 32 * U * W;
-  int k0 = 32 * U * w;
+  int k0 = from + 32 * U * w;
   if (k0 < k) {
     load(a, k0);
     for (; k0 + step < k; k0 += 2 * step) {
@@ -817,7 +819,8 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
 // the tile's places against columns n0 .. of the matrix P
 template <class T, int RM, int RN>
 __device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at, int n0,
-                                         const T* P, floatx4* sums, int w, int lane) {
+                                         const T* P, int from, int k, floatx4* sums, int w,
+                                         int lane) {
   const int r = lane & 15;
   const unsigned c = 16u * (lane >> 4);
   unsigned q_off[RM], p_off[RN];
@@ -837,7 +840,7 @@ __device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at
     p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + c : kOutside;
   few_product<T, RM, RN>(
       buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
-      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, p.k, sums, w, lane);
+      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, from, k, sums, w, lane);
 }
 
 // D = A B[g]^T, groups of few rows
@@ -850,7 +853,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) grouped_few(const GroupedPa
   if (s.spot.parts == 0 || s.at.group == p.groups) return;
   const Place at = s.at;
   const int n0 = s.spot.tn * F::BN;
-  few_tile<T, RM, RN>(p, at, n0, (const T*)p.p + at.group * p.p_group, sums, w, lane);
+  few_tile<T, RM, RN>(p, at, n0, (const T*)p.p + at.group * p.p_group, 0, p.k, sums, w, lane);
   // (a thread stores what it added itself)
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;

@@ -197,33 +197,49 @@ int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const 
 struct AdaptersPlan {
   Choice down, all;
   int pieces;                  // 0: h in fp32
-  int64_t h_at, bytes;
+  int64_t splits, part_k;      // FEW: parts of the contraction
+  int64_t h_at, part_at, bytes;
+  int64_t join_blocks;
 };
 AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
   const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
-  AdaptersPlan r;
+  AdaptersPlan r{};
   const int64_t mean = ceil_div(a.places, a.groups);
   const int algo = a.algo ? a.algo : a.places <= 192 ? kFew
                    : square_tile(a.places, a.places, a.n);
   r.all.algo = algo;
+  r.down.algo = kFew;
   if (algo == kFew) {
-    const int rm = a.places <= 16 ? 1 : a.places <= 32 ? 2 : 4;
-    const int rn = ceil_div(a.places, 16 * rm) * ceil_div(a.n, 32) >= 2 * kFill ? 2 : 1;
-    r.all.kernel = adapters_few_kernel(bf16, f32, rm, rn);
-    r.pieces = 0;
+    r.all.kernel = adapters_first_kernel(bf16, a.places <= 16 ? 1 : a.places <= 32 ? 2 : 4);
+    r.down.kernel = down_kernel(bf16, 1, 1);
   } else {
     r.all.kernel = adapters_kernel(bf16, f32, algo);
+    r.down.kernel = mean > 24 ? down_rows_kernel(bf16)
+                              : down_kernel(bf16, mean <= 10 ? 1 : 2, a.rank <= 16 ? 1 : 2);
     r.pieces = f32 ? 3 : 2;
   }
   r.all.slots = ceil_div(a.places, r.all.kernel.bm);
   r.all.tiles_n = ceil_div(a.n, r.all.kernel.bn);
-  r.down.algo = kFew;
-  r.down.kernel = down_kernel(bf16, mean <= 10 ? 1 : mean <= 24 ? 2 : 4, a.rank <= 16 ? 1 : 2);
   r.down.slots = tile_slots(a.places, a.groups, r.down.kernel.bm);
   r.down.tiles_n = ceil_div(a.rank, r.down.kernel.bn);
   r.h_at = ceil_div(4 * a.places, 16) * 16;
-  r.bytes = r.h_at + a.places * a.rank * (r.pieces ? 2 * r.pieces : 4);
+  r.part_at = r.h_at + ceil_div(a.places * a.rank * (r.pieces ? 2 * r.pieces : 4), 16) * 16;
+  if (algo == kFew) {
+    // one round of the chip (a workgroup per CU) with the down projection's,
+    // 256 of the contraction each at least
+    const int64_t tiles = r.all.slots * r.all.tiles_n, most = ceil_div(a.k, 256),
+                  free = kFill - r.down.blocks();
+    r.splits = tiles > 0 && free > tiles ? free / tiles : 1;
+    if (r.splits > most) r.splits = most;
+    r.part_k = ceil_div(ceil_div(a.k, r.splits), 32) * 32;
+    r.splits = ceil_div(a.k, r.part_k);
+    r.join_blocks = ceil_div(a.places * (a.n / 4), 256);
+  }
+  r.bytes = r.part_at + 4 * r.splits * a.places * a.n;
   return r;
+}
+int64_t first_blocks(const AdaptersPlan& r) {
+  return r.all.algo == kFew ? r.down.blocks() + r.all.blocks() * r.splits : r.all.blocks();
 }
 
 struct SortPlan {
@@ -425,7 +441,8 @@ int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W,
   const int rc = check_adapters(*a, x, W, A, B, offsets, rows, scale, D);
   if (rc) return rc;
   const AdaptersPlan r = plan_adapters(*a);
-  if (r.down.blocks() > kMaxBlocks || r.all.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (r.down.blocks() > kMaxBlocks || first_blocks(r) > kMaxBlocks || r.join_blocks > kMaxBlocks)
+    return MFL_E_TOO_LARGE;
   if (algo) *algo = r.all.algo;
   if (workspace_bytes) *workspace_bytes = r.bytes;
   return MFL_OK;
@@ -443,7 +460,6 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   const AdaptersPlan r = plan_adapters(*a);
   AdapterParams p{};
   p.g.q = x;
-  p.g.d = D;
   p.g.offsets = offsets;
   p.g.rows = rows;
   p.g.groups = (int)a->groups;
@@ -451,6 +467,18 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   p.g.k = (int)a->k;
   p.g.ldq = (int)a->ldx;
   p.g.q_rows = (int)a->x_rows;
+  p.down = p.g;
+  p.down.p = A;
+  p.down.n = (int)a->rank;
+  p.down.ldp = (int)a->lda;
+  p.down.p_group = a->a_group;
+  place(p.down, r.down);
+  p.g.p = W;
+  p.g.d = D;
+  p.g.n = (int)a->n;
+  p.g.ldp = (int)a->ldw;
+  p.g.ldd = (int)a->ldd;
+  place(p.g, r.all);
   p.up = B;
   p.scale = scale;
   p.owner = (int*)workspace;
@@ -458,24 +486,21 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
     p.hp = (char*)workspace + r.h_at;
   else
     p.h = (float*)((char*)workspace + r.h_at);
+  p.part = (float*)((char*)workspace + r.part_at);
   p.up_group = a->b_group;
   p.rank = (int)a->rank;
   p.ldup = (int)a->ldb;
   p.pieces = r.pieces;
-  AdapterParams down = p;
-  down.g.p = A;
-  down.g.n = (int)a->rank;
-  down.g.ldp = (int)a->lda;
-  down.g.p_group = a->a_group;
-  place(down.g, r.down);
-  rc = launch(r.down.kernel, r.down.blocks(), &down, stream);
-  if (rc) return rc;
-  p.g.p = W;
-  p.g.n = (int)a->n;
-  p.g.ldp = (int)a->ldw;
-  p.g.ldd = (int)a->ldd;
-  place(p.g, r.all);
-  return launch(r.all.kernel, r.all.blocks(), &p, stream);
+  if (r.all.algo == kFew) {
+    p.down_blocks = (int)r.down.blocks();
+    p.splits = (int)r.splits;
+    p.part_k = (int)r.part_k;
+    rc = launch(r.all.kernel, first_blocks(r), &p, stream);
+    return rc ? rc : launch(adapters_join_kernel(a->dtype == MFL_BF16, a->out == MFL_F32),
+                            r.join_blocks, &p, stream);
+  }
+  rc = launch(r.down.kernel, r.down.blocks(), &p, stream);
+  return rc ? rc : launch(r.all.kernel, r.all.blocks(), &p, stream);
 }
 
 int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,

@@ -22,18 +22,20 @@ struct GroupedParams {
   int64_t p_group, d_group;
 };
 
-// Adapters beside a shared projection (adapters.hpp): g is the down
-// projection's (p = A, n = rank) in the first launch, the shared product's
-// (p = W) in the second.  q = x, d = D, offsets and rows in both.
+// Adapters beside a shared projection (adapters.hpp): g is the shared product
+// (p = W), down the down projection (p = A, n = rank); q = x, offsets and rows
+// in both.
 struct AdapterParams {
-  GroupedParams g;
+  GroupedParams g, down;
   const void* up;              // B
   const float* scale;          // of each group, or null: 1
   int* owner;                  // workspace: the group of each place that has one,
   float* h;                    // scale h in fp32, places x rank,
-  void* hp;                    // or as 16-bit numbers, places x pieces x rank
+  void* hp;                    // or as 16-bit numbers, places x pieces x rank,
+  float* part;                 // sums over parts of the contraction, splits x places x n
   int64_t up_group;
   int rank, ldup, pieces;
+  int down_blocks, splits, part_k;
 };
 
 struct SortParams {
@@ -76,7 +78,9 @@ KernelRef few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
 KernelRef input_grad_kernel(bool bf16, int algo);                       // dA
 KernelRef weight_grad_kernel(bool bf16, bool f32, int algo, bool gathered);   // dB
 KernelRef down_kernel(bool bf16, int row_blocks, int column_blocks);
-KernelRef adapters_few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
+KernelRef down_rows_kernel(bool bf16);
+KernelRef adapters_first_kernel(bool bf16, int row_blocks);
+KernelRef adapters_join_kernel(bool bf16, bool f32);
 KernelRef adapters_kernel(bool bf16, bool f32, int algo);
 KernelRef count_kernel(bool i64, int groups);
 KernelRef place_kernel(bool i64, int groups);
