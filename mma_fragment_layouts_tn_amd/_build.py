@@ -25,7 +25,7 @@ SOURCES = ["gemm_inst_256.hip", "gemm_inst_256w4.hip", "gemm_inst_128.hip",
            "gemm_inst_128w1.hip", "gemm_inst_splitk.hip", "gemm_inst_256w4x16.hip",
            "gemm_inst_256x16.hip", "gemm_inst_128x16.hip", "gemm_inst_splitk16.hip", "chain_inst.hip", "attention_fwd.hip",
            "attention_bwd.hip", "attention_dkv.hip", "attention_capi.hip",
-           "grouped_rows.hip", "grouped_weights.hip", "grouped_few.hip", "adapters_rows.hip",
+           "grouped_rows.hip", "grouped_backward.hip", "grouped_few.hip", "adapters_rows.hip",
            "adapters_few.hip", "grouped_capi.hip",
            "gemm_dispatch.hip", "probe_kernels.hip", "microbench.hip", "probe_dump.hip", "capi.cpp"]
 FLAGS = [
@@ -107,7 +107,7 @@ def _blocks(lines):
 
 # sources whose kernels tie accumulators to other instructions by hand: every
 # matrix instruction is taken for one of them
-TIED_SOURCES = {"attention_dkv.hip", "grouped_rows.hip", "grouped_weights.hip",
+TIED_SOURCES = {"attention_dkv.hip", "grouped_rows.hip", "grouped_backward.hip",
                 "adapters_rows.hip"}
 
 

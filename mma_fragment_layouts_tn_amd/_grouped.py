@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._attention import BF16, _dtype, _ptr, _Run
+from ._attention import _DTYPES, BF16, _ptr, _Run
 
 GROUPED_ALGOS = {"auto": 0, "few": 1, "tile128": 2, "tile256": 3}
 _NAMES = {v: k for k, v in GROUPED_ALGOS.items()}
@@ -20,6 +20,8 @@ _F32, _I32, _I64 = 2, 4, 5
 _TYPES = {torch.float16: 1, torch.float32: _F32, torch.bfloat16: BF16}
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_int32, _float32 = torch.int32, torch.float32
+_raw_stream, _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class GroupRowsArgs(ctypes.Structure):
@@ -83,13 +85,30 @@ def bind(lib: ctypes.CDLL, check) -> None:
 
 
 # ---------------------------------------------------------------- marshalling
-def _run(stream, *tensors) -> _Run:
-    return _Run([t for t in tensors if t is not None], stream)
+class _Here(_Run):
+    """_Run of the tensors given, None left out, with less to do where they are
+    on one device and the stream is the current one."""
+
+    __slots__ = ("index",)
+
+    def __init__(self, stream, *tensors):
+        i = tensors[0].get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != i:
+                i = -1
+        if i < 0 or stream is not None:
+            super().__init__([t for t in tensors if t is not None], stream)
+            i = self.device.index
+        else:
+            self.device = tensors[0].device
+            self.handle = _raw_stream(i)
+            self.other = None
+        self.index = i
 
 
-def _call(run: _Run, fn, *args) -> None:
+def _call(run: _Here, fn, *args) -> None:
     """fn, which takes no workspace, on the tensors' device."""
-    if torch._C._cuda_getDevice() != run.device.index:
+    if _current() != run.index:
         with torch.cuda.device(run.device):
             rc = fn(*args, run.handle)
     else:
@@ -98,13 +117,15 @@ def _call(run: _Run, fn, *args) -> None:
         _check(rc)
 
 
-def _call_with(run: _Run, fn, need: int, *args) -> None:
+def _call_with(run: _Here, fn, need: int, *args) -> None:
     """The same for a function with a workspace of `need` bytes."""
-    ws = run.empty((need,), torch.uint8, result=False) if need else None
-    _call(run, fn, *args, None if ws is None else ws.data_ptr(), need)
+    if need == 0:
+        return _call(run, fn, *args, None, 0)
+    ws = run.empty((need,), torch.uint8, result=False)
+    _call(run, fn, *args, ws.data_ptr(), need)
 
 
-def _new(run: _Run, like: torch.Tensor, shape, dtype: Optional[torch.dtype]) -> torch.Tensor:
+def _new(run: _Here, like: torch.Tensor, shape, dtype: Optional[torch.dtype]) -> torch.Tensor:
     """A new tensor of `like`'s type, or of dtype."""
     if run.other is not None:
         return run.empty(shape, like.dtype if dtype is None else dtype)
@@ -136,7 +157,7 @@ def _matrices(t: torch.Tensor, name: str) -> Tuple[int, int]:
 def _numbers(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) -> None:
     if t is None:
         return
-    if t.dtype is not torch.int32:
+    if t.dtype is not _int32:
         raise TypeError(f"{name} must be int32")
     if t.dim() != 1 or not t.is_contiguous() or (count is not None and t.shape[0] != count):
         raise ValueError(f"{name} must be contiguous" +
@@ -145,14 +166,27 @@ def _numbers(t: Optional[torch.Tensor], name: str, count: Optional[int] = None) 
 
 def _type(dtype, given: torch.dtype, name: str) -> int:
     """Code of an output's type: the operands' own or float32."""
-    dtype = given if dtype is None else dtype
-    if dtype not in (given, torch.float32):
+    if dtype is None or dtype is given:
+        return _TYPES.get(given, 0)       # (0: refused with the operands)
+    if dtype is not _float32:
         raise TypeError(f"{name} must be of the operands' type or float32")
-    return _TYPES[dtype]
+    return _F32
+
+
+def _code(names: str, first: torch.Tensor, *others) -> int:
+    """Code of the operands' one type."""
+    dt = first.dtype
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"{names} must be float16 or bfloat16")
+    for t in others:
+        if t.dtype is not dt:
+            raise TypeError(f"{names} must have one dtype")
+    return code
 
 
 def _grouped_args(A, B, offsets, rows, out: int, algo: str, places: int, ldd: int):
-    code = _dtype("A and B", A, B)
+    code = _code("A and B", A, B)
     lda = _matrix(A, "A")
     ldb, b_group = _matrices(B, "B")
     groups, n, k = B.shape
@@ -180,17 +214,18 @@ def group_rows(ids: torch.Tensor, groups: int, *, stream=None):
 
     as gemm_grouped, combine_rows and gemm_adapters take them.  At most 4096
     groups."""
-    if ids.dtype not in (torch.int32, torch.int64):
+    dtype = ids.dtype
+    if dtype is not torch.int64 and dtype is not _int32:
         raise TypeError("ids must be int32 or int64")
     if ids.dim() not in (1, 2):
         raise ValueError("ids must be (tokens,) or (tokens, top)")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
     top = ids.shape[1] if ids.dim() == 2 else 1
-    a = GroupRowsArgs(_I64 if ids.dtype == torch.int64 else _I32, ids.numel(), max(top, 1), groups)
+    a = GroupRowsArgs(_I32 if dtype is _int32 else _I64, ids.numel(), max(top, 1), groups)
     if groups < 1:
         raise ValueError("there must be a group")
-    run = _Run([ids], stream)
+    run = _Here(stream, ids)
     # (one allocation: it takes longer than the kernels for a few choices)
     n = ids.numel()
     rows, offsets, slots = run.empty((2 * n + groups + 1,), torch.int32).split_with_sizes(
@@ -231,7 +266,7 @@ def gemm_grouped(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, *,
         out_dtype = D.dtype
     out = _type(out_dtype, A.dtype, "D")
     a = _grouped_args(A, B, offsets, rows, out, algo, places, n if D is None else _matrix(D, "D"))
-    run = _run(stream, A, B, offsets, rows, D)
+    run = _Here(stream, A, B, offsets, rows, D)
     if D is None:
         D = _new(run, A, (places, n), out_dtype)
     _call(run, _lib.gemm_tn_grouped, a, _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), _ptr(D))
@@ -268,7 +303,7 @@ def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     f = _grouped_args(A, B, offsets, rows, out, algo, places, _matrix(dD, "dD"))
     k, n = B.shape[2], B.shape[1]
     a = GroupedGradArgs(f, k, k, n * k)
-    run = _run(stream, dD, A, B, offsets, rows)
+    run = _Here(stream, dD, A, B, offsets, rows)
     dA = _new(run, A, (places, k), None)
     dB = _new(run, B, B.shape, dB_dtype)
     _call(run, _lib.gemm_tn_grouped_backward, a, _ptr(dD), _ptr(A), _ptr(B), _ptr(offsets),
@@ -277,19 +312,20 @@ def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
 
 
 def _combine_args(X, slots, weights, out: int, ldo: int) -> CombineArgs:
-    code = _dtype("X", X)
-    if slots.dtype != torch.int32:
+    code = _code("X", X)
+    if slots.dtype is not _int32:
         raise TypeError("slots must be int32")
-    if slots.dim() not in (1, 2) or not slots.is_contiguous():
+    shape = slots.shape
+    if len(shape) not in (1, 2) or not slots.is_contiguous():
         raise ValueError("slots must be (tokens,) or (tokens, top), contiguous")
     if weights is not None:
-        if weights.dtype != torch.float32:
+        if weights.dtype is not _float32:
             raise TypeError("weights must be float32")
-        if weights.shape != slots.shape or not weights.is_contiguous():
+        if weights.shape != shape or not weights.is_contiguous():
             raise ValueError("weights must have slots' shape, contiguous")
     ldx = _matrix(X, "X")
-    top = slots.shape[1] if slots.dim() == 2 else 1
-    return CombineArgs(code, out, slots.shape[0], top, X.shape[1], X.shape[0], ldx, ldo)
+    rows, n = X.shape
+    return CombineArgs(code, out, shape[0], shape[1] if len(shape) == 2 else 1, n, rows, ldx, ldo)
 
 
 def combine_rows(X: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
@@ -311,7 +347,7 @@ def combine_rows(X: torch.Tensor, slots: torch.Tensor, weights: Optional[torch.T
         out_dtype = out.dtype
     a = _combine_args(X, slots, weights, _type(out_dtype, X.dtype, "out"),
                       n if out is None else _matrix(out, "out"))
-    run = _run(stream, X, slots, weights, out)
+    run = _Here(stream, X, slots, weights, out)
     if out is None:
         out = _new(run, X, (slots.shape[0], n), out_dtype)
     _call(run, _lib.combine_rows, a, _ptr(X), _ptr(slots), _ptr(weights), _ptr(out))
@@ -333,7 +369,7 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
         raise ValueError("dout must be (tokens, N)")
     a = _combine_args(X, slots, weights, _TYPES.get(X.dtype, 0), _matrix(dout, "dout"))
     _numbers(rows, "rows", X.shape[0])
-    run = _run(stream, dout, X, slots, weights, rows)
+    run = _Here(stream, dout, X, slots, weights, rows)
     dX = _new(run, X, X.shape, None)
     dw = None if weights is None else _new(run, weights, weights.shape, None)
     _call(run, _lib.combine_rows_backward, a, X.shape[1], _ptr(dout), _ptr(X), _ptr(slots),
@@ -342,7 +378,7 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
 
 
 def _adapters_args(x, W, A, B, offsets, rows, scale, out: int, algo: str, ldd: int):
-    code = _dtype("x, W, A and B", x, W, A, B)
+    code = _code("x, W, A and B", x, W, A, B)
     ldx, ldw = _matrix(x, "x"), _matrix(W, "W")
     lda, a_group = _matrices(A, "A")
     ldb, b_group = _matrices(B, "B")
@@ -393,7 +429,7 @@ def gemm_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Te
         out_dtype = D.dtype
     a = _adapters_args(x, W, A, B, offsets, rows, scale, _type(out_dtype, x.dtype, "D"), algo,
                        n if D is None else _matrix(D, "D"))
-    run = _run(stream, x, W, A, B, offsets, rows, scale, D)
+    run = _Here(stream, x, W, A, B, offsets, rows, scale, D)
     if D is None:
         D = _new(run, x, (m, n), out_dtype)
     ptrs = (_ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(offsets), _ptr(rows), _ptr(scale), _ptr(D))

@@ -656,16 +656,20 @@ __device__ __forceinline__ void by_rows(const Spot& spot, Place at, F f) {
   }
 }
 
-// D = A B[g]^T (PT false) or dA = dD B[g] (PT true)
+// D = A B[g]^T (PT false) or dA = dD B[g] (PT true): workgroup `id`'s part
 template <class T, class O, class S, bool PT>
-__global__ void __launch_bounds__(S::Full::T, 1) grouped_rows(const GroupedParams p) {
+__device__ __forceinline__ void rows_part(const GroupedParams& p, char* smem, int id) {
   using C = typename S::Full;
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
-  const GroupSpot x = group_spot<S::kParts>(p, blockIdx.x, C::BM);
+  const GroupSpot x = group_spot<S::kParts>(p, id, C::BM);
   if (x.spot.parts == 0) return;
   by_rows<S>(x.spot, x.at, [&](auto c, const Place& at) {
     rows_tile<T, O, decltype(c), PT>(p, smem, at, x.spot.tn * C::BN);
   });
+}
+template <class T, class O, class S>
+__global__ void __launch_bounds__(S::Full::T, 1) grouped_rows(const GroupedParams p) {
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+  rows_part<T, O, S, false>(p, smem, blockIdx.x);
 }
 
 template <class C, bool GATHER>
@@ -704,29 +708,41 @@ __device__ __forceinline__ void weights_tile(const GroupedParams& p, char* smem,
                           acc, w, lane);
 }
 
-// dB[g] = sum over the group's places of dD^T A
-template <class T, class O, class S, bool GATHER>
-__global__ void __launch_bounds__(S::Full::T, 1) grouped_weights(const GroupedParams p) {
-  using C = typename S::Full;
-  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+// dB[g] = sum over the group's places of dD^T A: workgroup `id`'s part
+template <class T, class O, class W, bool GATHER>
+__device__ __forceinline__ void weights_part(const GroupedParams& p, char* smem, int id) {
+  using C = typename W::Full;
   // slots: tiles of one group's rows times groups
   const int per = p.slots / p.groups;
   // (each group's tiles to all XCDs: with a run of the whole launch to each,
   // groups of 492 to 1800 places took 203 us where equal ones take 146)
-  const Spot x =
-      spot_of<S::kParts>(blockIdx.x, p.slots, p.tiles_n, min(p.band, per), per * p.tiles_n);
+  const Spot x = spot_of<W::kParts>(id, p.slots, p.tiles_n, min(p.band, per), per * p.tiles_n);
   if (x.parts == 0) return;
   const int g = x.tm / per;
   const int m0 = (x.tm - g * per) * C::BM, n0 = x.tn * C::BN;
-  if constexpr (S::kParts > 1) {
+  if constexpr (W::kParts > 1) {
     if (x.parts == 4)
-      return weights_tile<T, O, typename S::Corner, GATHER>(
-          p, smem, g, m0 + (x.part >> 1) * S::Corner::BM, n0 + (x.part & 1) * S::Corner::BN);
+      return weights_tile<T, O, typename W::Corner, GATHER>(
+          p, smem, g, m0 + (x.part >> 1) * W::Corner::BM, n0 + (x.part & 1) * W::Corner::BN);
     if (x.parts == 2)
-      return weights_tile<T, O, typename S::Half, GATHER>(p, smem, g, m0 + x.part * S::Half::BM,
+      return weights_tile<T, O, typename W::Half, GATHER>(p, smem, g, m0 + x.part * W::Half::BM,
                                                           n0);
   }
   weights_tile<T, O, C, GATHER>(p, smem, g, m0, n0);
+}
+
+// Both gradients in one launch: the first `first` workgroups are dA's, the
+// others dB's.
+template <class T, class O, class S, class W, bool GATHER>
+__global__ void __launch_bounds__(S::Full::T, 1) grouped_backward(const GroupedParams da,
+                                                                  const GroupedParams db,
+                                                                  int first) {
+  static_assert((int)S::Full::T == (int)W::Full::T && S::kLds >= W::kLds, "one workgroup for both");
+  __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
+  if ((int)blockIdx.x < first)
+    rows_part<T, T, S, true>(da, smem, blockIdx.x);
+  else
+    weights_part<T, O, W, GATHER>(db, smem, blockIdx.x - first);
 }
 
 // ------------------------------------------------------------- few rows
@@ -737,7 +753,7 @@ __global__ void __launch_bounds__(S::Full::T, 1) grouped_weights(const GroupedPa
 // added through LDS in the order of the waves.
 constexpr int kFewWaves = 8;
 // sub-steps a time: two of those are in registers beside the sums
-constexpr int few_depth(int rm, int rn) { return rm + rn > 6 ? 2 : 4; }
+constexpr int few_depth(int rm, int rn) { return rm + rn > 3 ? 2 : 4; }
 
 template <int RM, int RN>
 struct FewTile {

@@ -24,10 +24,11 @@ bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool half_type(int32_t t) { return t == MFL_F16 || t == MFL_BF16; }
 
-int launch(const KernelRef& k, int64_t blocks, void* params, void* stream) {
+int launch(const KernelRef& k, int64_t blocks, void* params, void* stream, void* more = nullptr,
+           void* rest = nullptr) {
   if (blocks == 0) return MFL_OK;
   if (blocks > kMaxBlocks) return MFL_E_TOO_LARGE;
-  void* args[] = {params};
+  void* args[] = {params, more, rest};   // (a kernel takes as many as it has)
   const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
                                        (hipStream_t)stream);
   return e == hipSuccess ? MFL_OK : MFL_E_LAUNCH;
@@ -126,6 +127,7 @@ void place(GroupedParams& p, const Choice& c) {
   p.band = c.algo == kFew ? 0 : c.algo == kTile256 ? 4 : 8;
 }
 
+// Both gradients, in one launch: the kernel, and each one's tiles.
 struct Backward {
   Choice da, db;
 };
@@ -133,14 +135,10 @@ Backward choose_backward(const mfl_grouped_t& f, bool gathered) {
   const bool bf16 = f.dtype == MFL_BF16, f32 = f.out == MFL_F32;
   const int64_t mean = ceil_div(f.places, f.groups);
   Backward r;
-  const int a = f.algo ? f.algo : square_tile(mean, f.places, f.k);
-  r.da = with(input_grad_kernel(bf16, a), a, f, f.k);
-  const int b = f.algo ? f.algo
-                : f.groups * ceil_div(f.n, 256) * ceil_div(f.k, 256) >= 192 ? kTile256 : kTile128;
-  r.db.algo = b;
-  r.db.kernel = weight_grad_kernel(bf16, f32, b, gathered);
-  r.db.slots = f.groups * ceil_div(f.n, r.db.kernel.bm);
-  r.db.tiles_n = ceil_div(f.k, r.db.kernel.bn);
+  const int algo = f.algo ? f.algo : square_tile(mean, f.places, f.k);
+  const KernelRef k = backward_kernel(bf16, f32, algo, gathered);
+  r.da = with(k, algo, f, f.k);
+  r.db = {algo, k, f.groups * ceil_div(f.n, k.bm), ceil_div(f.k, k.bn)};
   return r;
 }
 
@@ -159,8 +157,7 @@ int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, c
     if ((dA && dA == x) || (dB && dB == x)) return MFL_E_ALIAS;
   if (dA && dA == dB) return MFL_E_ALIAS;
   const Backward r = choose_backward(f, rows != nullptr);
-  if (r.da.blocks() > kMaxBlocks || r.db.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
-  return MFL_OK;
+  return r.da.blocks() + r.db.blocks() > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
 }
 
 int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const void* A,
@@ -398,39 +395,38 @@ int gemm_tn_grouped_backward(const mfl_grouped_grad_t* a, const void* dD, const 
   if (rc) return rc;
   const mfl_grouped_t& f = a->f;
   const Backward r = choose_backward(f, rows != nullptr);
-  GroupedParams p{};
-  p.offsets = offsets;
-  p.groups = (int)f.groups;
-  p.places = (int)f.places;
-  if (dA && f.places > 0) {
-    GroupedParams x = p;
-    x.p = B;
-    x.q = dD;
-    x.d = dA;
-    x.n = (int)f.k;
-    x.k = (int)f.n;
-    x.ldp = (int)f.ldb;
-    x.ldq = (int)f.ldd;
-    x.ldd = (int)a->ldda;
-    x.p_group = f.b_group;
-    place(x, r.da);
-    rc = launch(r.da.kernel, r.da.blocks(), &x, stream);
-    if (rc) return rc;
-  }
-  if (!dB) return MFL_OK;
-  p.p = A;
-  p.q = dD;
-  p.d = dB;
-  p.rows = rows;
-  p.m = (int)f.n;
-  p.n = (int)f.k;
-  p.ldp = (int)f.lda;
-  p.ldq = (int)f.ldd;
-  p.ldd = (int)a->lddb;
-  p.p_rows = (int)f.a_rows;
-  p.d_group = a->db_group;
-  place(p, r.db);
-  return launch(r.db.kernel, r.db.blocks(), &p, stream);
+  GroupedParams x{};           // dA
+  x.p = B;
+  x.q = dD;
+  x.d = dA;
+  x.offsets = offsets;
+  x.groups = (int)f.groups;
+  x.places = (int)f.places;
+  x.n = (int)f.k;
+  x.k = (int)f.n;
+  x.ldp = (int)f.ldb;
+  x.ldq = (int)f.ldd;
+  x.ldd = (int)a->ldda;
+  x.p_group = f.b_group;
+  place(x, r.da);
+  GroupedParams y{};           // dB
+  y.p = A;
+  y.q = dD;
+  y.d = dB;
+  y.offsets = offsets;
+  y.rows = rows;
+  y.groups = (int)f.groups;
+  y.places = (int)f.places;
+  y.m = (int)f.n;
+  y.n = (int)f.k;
+  y.ldp = (int)f.lda;
+  y.ldq = (int)f.ldd;
+  y.ldd = (int)a->lddb;
+  y.p_rows = (int)f.a_rows;
+  y.d_group = a->db_group;
+  place(y, r.db);
+  int first = dA && f.places > 0 ? (int)r.da.blocks() : 0;
+  return launch(r.da.kernel, first + (dB ? r.db.blocks() : 0), &x, stream, &y, &first);
 }
 
 int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W, const void* A,
