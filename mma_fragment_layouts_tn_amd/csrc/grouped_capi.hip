@@ -101,16 +101,34 @@ Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
   return {algo, k, tile_slots(a.places, a.groups, k.bm), ceil_div(n, k.bn)};
 }
 
-// Square tile for groups of `mean` rows.
-int square_tile(int64_t mean, int64_t places, int64_t n) {
-  return mean >= 192 && ceil_div(places, 256) * ceil_div(n, 256) >= 192 ? kTile256 : kTile128;
+// Kernel for `places` rows of `groups` matrices of n x k.  The lengths are on
+// the device, so the rule goes by their mean.  Microseconds, bf16, half of the
+// groups a quarter of the places and half three quarters:
+//
+//   groups mean    n     k   FEW  128  256
+//        2    2  4096  4096   14   41   29   few tiles: FEW goes to all CUs, until
+//        2   64  2048  4096   25   43   31   its tiles read the weights too often
+//        8   64  2048  4096   73   46   33
+//       64    2  1024  2048   49   41   45   many tiles: no kernel for few rows
+//       64   64  1024  2048  162   59   59   is needed
+//        8   64  4096  4096  138   63   60   256 has more loads under way per
+//        8  128  4096  4096    -   72   61   workgroup, 128 two workgroups per
+//        8  256  4096  4096    -   87   93   CU if there are as many, and less
+//       32  256  1024  2048    -   38   53   left over at the groups' ends
+//        8  512  4096  4096    -  170  122
+//       32  512  1024  2048    -   69   62
+int choose_algo(int64_t places, int64_t groups, int64_t n, int64_t k, bool few) {
+  const int64_t mean = ceil_div(places, groups), held = places < groups ? places : groups;
+  if (few && mean * held * ceil_div(n, 256) <= 768) return kFew;
+  if (mean >= 512) return kTile256;
+  const int64_t whole = places / 128 + held / 2, slots = whole > held ? whole : held;
+  return slots * ceil_div(n, 128) >= 2 * kFill || k < 2048 ? kTile128 : kTile256;
 }
 
 Choice choose(const mfl_grouped_t& a) {
   const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
   const int64_t mean = ceil_div(a.places, a.groups);
-  int algo = a.algo;
-  if (algo == kAuto) algo = mean <= 64 ? kFew : square_tile(mean, a.places, a.n);
+  const int algo = a.algo ? a.algo : choose_algo(a.places, a.groups, a.n, a.k, true);
   if (algo != kFew) return with(rows_kernel(bf16, f32, algo), algo, a, a.n);
   const int rm = mean <= 10 ? 1 : mean <= 24 ? 2 : 4;
   const int64_t held = a.places < a.groups ? a.places : a.groups;
@@ -133,9 +151,8 @@ struct Backward {
 };
 Backward choose_backward(const mfl_grouped_t& f, bool gathered) {
   const bool bf16 = f.dtype == MFL_BF16, f32 = f.out == MFL_F32;
-  const int64_t mean = ceil_div(f.places, f.groups);
   Backward r;
-  const int algo = f.algo ? f.algo : square_tile(mean, f.places, f.k);
+  const int algo = f.algo ? f.algo : choose_algo(f.places, f.groups, f.k, f.n, false);
   const KernelRef k = backward_kernel(bf16, f32, algo, gathered);
   r.da = with(k, algo, f, f.k);
   r.db = {algo, k, f.groups * ceil_div(f.n, k.bm), ceil_div(f.k, k.bn)};
@@ -203,7 +220,7 @@ AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
   AdaptersPlan r{};
   const int64_t mean = ceil_div(a.places, a.groups);
   const int algo = a.algo ? a.algo : a.places <= 192 ? kFew
-                   : square_tile(a.places, a.places, a.n);
+                   : choose_algo(a.places, 1, a.n, a.k, false);
   r.all.algo = algo;
   r.down.algo = kFew;
   if (algo == kFew) {
