@@ -105,7 +105,7 @@ int gemm_tn_grouped_plan(const mfl_grouped_t* a, const void* A, const void* B,
  *                                                without places
  * Either may be NULL.  A row that several places share has a row of dA for
  * each of them; combine_rows adds them by token.  f.ldd is dD's stride; f.algo
- * is AUTO or a TILE. */
+ * is AUTO (else MFL_E_ALGO_CASE). */
 typedef struct {
   mfl_grouped_t f;
   int64_t ldda, lddb, db_group;

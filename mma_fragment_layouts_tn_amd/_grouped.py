@@ -286,8 +286,7 @@ def gemm_grouped_plan(A, B, offsets, *, rows=None, out_dtype=None, algo="auto") 
 
 def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                           offsets: torch.Tensor, *, rows: Optional[torch.Tensor] = None,
-                          dB_dtype: Optional[torch.dtype] = None, algo: str = "auto",
-                          stream=None):
+                          dB_dtype: Optional[torch.dtype] = None, stream=None):
     """(dA, dB) of sum(D * dD) for gemm_grouped()'s arguments.
 
     dA (places, K) has a row per place, 0 for those of no group; where rows
@@ -300,7 +299,7 @@ def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
         raise TypeError("dD must have A's dtype")
     if B.dim() != 3 or dD.shape != (places, B.shape[1]):
         raise ValueError("dD must be (places, N)")
-    f = _grouped_args(A, B, offsets, rows, out, algo, places, _matrix(dD, "dD"))
+    f = _grouped_args(A, B, offsets, rows, out, "auto", places, _matrix(dD, "dD"))
     k, n = B.shape[2], B.shape[1]
     a = GroupedGradArgs(f, k, k, n * k)
     run = _Here(stream, dD, A, B, offsets, rows)

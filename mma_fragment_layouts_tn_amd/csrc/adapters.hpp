@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_first(const Adapte
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int id = blockIdx.x - p.down_blocks, split = id % p.splits;
   const int slot = id / p.splits % p.g.slots, n0 = id / p.splits / p.g.slots * F::BN;
-  const Place at{0, slot * F::BM, min(p.g.places - slot * F::BM, F::BM)};
+  const Place at{0, slot * F::BM, min(p.g.places - slot * F::BM, F::BM), false};
   const int from = split * p.part_k;
   few_tile<T, RM, RN>(p.g, at, n0, (const T*)p.g.p, from, min(from + p.part_k, p.g.k), sums, w,
                       lane);
@@ -237,7 +237,7 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const GroupedParams& g = p.g;
   RowsSource<C, false> src;
-  src.init(g, Place{0, first, count}, n0, (const T*)g.p, w, lane);
+  src.init(g, Place{0, first, count, false}, n0, (const T*)g.p, w, lane);
   // the groups of the wave's places, 64 a time (asked for ahead of the product)
   const int m0 = first + (w % C::WM) * WROWS, nw = n0 + (w / C::WM) * 64;
   int own[H];
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(S::Full::T, 1) adapters_rows(const AdapterPara
   __shared__ __attribute__((aligned(1024))) char smem[S::kLds];
   const Spot s = spot_of<S::kParts>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.band, INT_MAX);
   if (s.parts == 0) return;
-  const Place at{0, s.tm * C::BM, min(p.g.places - s.tm * C::BM, C::BM)};
+  const Place at{0, s.tm * C::BM, min(p.g.places - s.tm * C::BM, C::BM), false};
   by_rows<S>(s, at, [&](auto c, const Place& x) {
     adapters_tile<T, O, decltype(c)>(p, smem, x.first, x.count, s.tn * C::BN);
   });

@@ -418,6 +418,7 @@ struct GatheredColumns : ColumnLoads<R, N> {
 // ---------------------------------------------------------- rows of groups
 struct Place {
   int group, first, count;    // the tile's first place, its places
+  bool small;                 // the group's matrix is read by two tiles at most
 };
 
 // Workgroups go to the 8 XCDs in turn; renumbered, each XCD has a run of
@@ -474,6 +475,7 @@ __device__ __forceinline__ Spot spot_of(int id, int tiles_m, int tiles_n, int ba
 // idle and the others run a second round: 793 TFLOP/s where it gives 1,270.)
 // For more groups, group g takes the numbers from start(g) / bm + g on, as
 // attention's tiles of sequences, some of them empty.
+constexpr int kSmall = 256;
 struct GroupSpot {
   Spot spot;
   Place at;
@@ -489,7 +491,7 @@ __device__ __forceinline__ GroupSpot group_spot(const GroupedParams& p, int id, 
     const int g = att::find_sequence(p.groups + 1, r.spot.tm, first);
     const int a = uniform(held(g)), b = uniform(g < p.groups ? held(g + 1) : p.places);
     const int t = r.spot.tm - (a / bm + g);
-    r.at = Place{g, a + t * bm, t < 0 ? 0 : min(max(b - a, 0) - t * bm, bm)};
+    r.at = Place{g, a + t * bm, t < 0 ? 0 : min(max(b - a, 0) - t * bm, bm), b - a <= kSmall};
     if (r.at.count <= 0) r.spot.parts = 0;
     return r;
   }
@@ -525,8 +527,9 @@ __device__ __forceinline__ GroupSpot group_spot(const GroupedParams& p, int id, 
     if (!m) continue;
     const int l = 63 - __builtin_clzll(m);
     const int t = r.spot.tm - __builtin_amdgcn_readlane(before[b], l);
-    r.at = Place{64 * b + l, __builtin_amdgcn_readlane(start[b], l) + t * bm,
-                 min(__builtin_amdgcn_readlane(len[b], l) - t * bm, bm)};
+    const int n = __builtin_amdgcn_readlane(len[b], l);
+    r.at = Place{64 * b + l, __builtin_amdgcn_readlane(start[b], l) + t * bm, min(n - t * bm, bm),
+                 n <= kSmall};
   }
   return r;
 }
@@ -545,25 +548,104 @@ struct Out {
   }
 };
 
-// D's columns of a lane: atom j's four from column(j) on.
+// Columns of a lane's accumulators: atom j's four from column_of(j) on.
 template <bool PERM>
 __device__ __forceinline__ int column_of(int lane, int j) {
   return PERM ? 16 * (lane >> 4) + 4 * j : 16 * j + 4 * (lane >> 4);
 }
 
-// the wave's rows, row_of(m) for row m of the tile (null: none), columns < width
+// Exchanges between two lanes of which one bit differs: afterwards a lane with
+// the bit clear has both lanes' a, one with the bit set both lanes' b, in the
+// order of the lanes.
+template <int BIT>
+__device__ __forceinline__ void exchange(unsigned& a, unsigned& b, int lane) {
+  if constexpr (BIT == 5 || BIT == 4) {
+    const auto r = BIT == 5 ? __builtin_amdgcn_permlane32_swap(a, b, false, false)
+                            : __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+  } else {
+    static_assert(BIT == 3 || BIT == 2, "lane bits 2 to 5");
+    const bool set = lane >> BIT & 1;
+    const int send = (int)(set ? a : b);
+    const unsigned got = BIT == 3 ? __builtin_amdgcn_mov_dpp(send, 0x128, 0xf, 0xf, false)   // row_ror:8
+                                  : __builtin_amdgcn_ds_swizzle(send, 0x101f);                // xor 4
+    a = set ? got : a;
+    b = set ? b : got;
+  }
+}
+
+// The wave's rows, row_of(m) for row m of the tile (null: none), columns <
+// width.  An accumulator tuple is four columns of a row: stored as they are, a
+// row's 128-byte lines are written a quarter at a time, and the L2s put them
+// together.  Exchanges between lanes make 16 columns per lane (which P's order
+// in LDS does for tiles that have it) and then, of 16 rows by 64 columns, whole
+// rows per store, 8 lanes a line, which need not stay in the L2s.  D, dA and dB
+// of 8192 places, 8 groups of 4096 x 2048: 447 us by quarters (510 if those are
+// non-temporal), 419 by lines, 401 if non-temporal; D of 16384 places, 2048 x
+// 4096, 260 and 251.
 template <class O, class C, bool PERM, class RowOf>
 __device__ __forceinline__ void store_rows(const floatx4 (&acc)[C::RM][C::RN], int col0, int width,
                                            int w, int lane, RowOf row_of) {
-  const int wm = w % C::WM, wn = w / C::WM;
+  constexpr int NW = sizeof(O);          // dwords of four values (2 or 4 bytes each)
+  const int m0 = (w % C::WM) * (16 * C::RM), n0 = col0 + (w / C::WM) * 64 + 16 * (lane >> 4);
 #pragma unroll
   for (int i = 0; i < C::RM; ++i) {
-    O* row = row_of(wm * (C::BM / C::WM) + 16 * i + (lane & 15));
-    if (!row) continue;
+    unsigned u[4][NW];                   // columns 4 x of the lane's 16
 #pragma unroll
-    for (int j = 0; j < C::RN; ++j) {
-      const int n = col0 + wn * 64 + column_of<PERM>(lane, j);
-      if (n < width) Out<O>::store4(row + n, acc[i][j]);
+    for (int x = 0; x < 4; ++x) {
+      if constexpr (NW == 4) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float f = acc[i][x][v];
+          u[x][v] = __float_as_uint(f);
+        }
+      } else {
+        typedef O vec4 __attribute__((ext_vector_type(4)));
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        const floatx4 f = acc[i][x];
+        const u32x2 p = __builtin_bit_cast(u32x2, vec4{(O)f[0], (O)f[1], (O)f[2], (O)f[3]});
+        u[x][0] = p[0];
+        u[x][1] = p[1];
+      }
+    }
+    if constexpr (!PERM) {
+#pragma unroll
+      for (int v = 0; v < NW; ++v) {
+        exchange<5>(u[0][v], u[2][v], lane);
+        exchange<5>(u[1][v], u[3][v], lane);
+        exchange<4>(u[0][v], u[1][v], lane);
+        exchange<4>(u[2][v], u[3][v], lane);
+      }
+    }
+    // pieces of 16 bytes: bits of the row for bits of the piece
+    u32x4_t piece[NW];
+    if constexpr (NW == 4) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        exchange<3>(u[0][v], u[2][v], lane);
+        exchange<3>(u[1][v], u[3][v], lane);
+        exchange<2>(u[0][v], u[1][v], lane);
+        exchange<2>(u[2][v], u[3][v], lane);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) piece[x] = u32x4_t{u[x][0], u[x][1], u[x][2], u[x][3]};
+    } else {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        exchange<3>(u[0][v], u[2][v], lane);
+        exchange<3>(u[1][v], u[3][v], lane);
+      }
+      piece[0] = u32x4_t{u[0][0], u[0][1], u[1][0], u[1][1]};
+      piece[1] = u32x4_t{u[2][0], u[2][1], u[3][0], u[3][1]};
+    }
+    constexpr int ROWS = 16 / NW, COLS = 16 / NW;    // rows of a store, columns of a piece
+    const int n = n0 + COLS * ((lane & 15) / ROWS);
+    if (n >= width) continue;
+#pragma unroll
+    for (int x = 0; x < NW; ++x) {
+      O* row = row_of(m0 + 16 * i + ROWS * x + (lane & 15) % ROWS);
+      if (row) __builtin_nontemporal_store(piece[x], (u32x4_t*)(row + n));
     }
   }
 }
@@ -589,6 +671,16 @@ struct RowsSource {
   static constexpr int kAhead = 0;    // loads of ahead()
   RowLoads<C::NQ> q;
   typename std::conditional<PT, PlainColumns<C::BN, C::NP>, RowLoads<C::NP>>::type p;
+  // The step that the contraction begins with (it goes round), the same for
+  // tiles of the same weights.  Weights that few tiles read come straight from
+  // memory, and where their rows lie a power of two apart, workgroups in step
+  // would all ask the same channels: 64 groups of 8 rows, 1024 x 2048, 67 us in
+  // step, 55 so, 48 with rows of 2112.
+  int begin = 0, steps = 0;
+  __device__ __forceinline__ void start(int id, int k) {
+    steps = (k + 63) / 64;
+    begin = id % steps;
+  }
   // the tile's places against columns n0 .. of the matrix P
   template <class T>
   __device__ __forceinline__ void init(const GroupedParams& a, const Place& at, int n0, const T* P,
@@ -612,6 +704,10 @@ struct RowsSource {
   }
   __device__ __forceinline__ void ahead(int) {}
   __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
+    if (kt < steps) {
+      kt += begin;
+      kt = kt < steps ? kt : kt - steps;
+    }
     if (i < C::NP)
       p.issue(kt, i, to);
     else
@@ -631,6 +727,7 @@ __device__ __forceinline__ void rows_tile(const GroupedParams& p, char* smem, co
   }
   RowsSource<C, PT> src;
   src.init(p, at, n0, (const T*)p.p + at.group * p.p_group, w, lane);
+  if (!PT && at.small) src.start(at.group * p.tiles_n + n0 / C::BN, p.k);
   floatx4 acc[C::RM][C::RN];
   product<T, C, PT, false>((lds_c)smem, (p.k + 63) / 64, src, acc, w, lane);
   store_tile<O, C, !PT>(D, p.ldd, at.count, n0, p.n, acc, w, lane);
@@ -767,12 +864,14 @@ __device__ __forceinline__ att::Vec8<__bf16> as16(const u32x4_t& u, __bf16) {
   return __builtin_bit_cast(att::Vec8<__bf16>, u);
 }
 
-// The contraction from `from` to k.  q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
+// The contraction from `from` to k (begun at another place by tiles of other
+// weights, as RowsSource::start, by tiles of the same weights at the same).  q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
 // sums[(i RN + j) * 64 + lane] holds the four values of atom (i, j).
 template <class T, int RM, int RN>
 __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const unsigned (&q_off)[RM],
                                             __amdgpu_buffer_rsrc_t rp, const unsigned (&p_off)[RN],
-                                            int from, int k, floatx4* sums, int w, int lane) {
+                                            int from, int k, int begin, floatx4* sums, int w,
+                                            int lane) {
   constexpr int U = few_depth(RM, RN), W = kFewWaves;
   floatx4 acc[RM][RN];
 #pragma unroll
@@ -805,19 +904,25 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
         for (int j = 0; j < RN; ++j)
           acc[i][j] = Elem<T>::mma16(as16(x.p[u][j], T()), as16(x.q[u][i], T()), acc[i][j]);
   };
-  // two parts in turn, so that one is on its way while the other is used
+  // The waves take the pieces of 32 U in turn, from piece `begin` on and round;
+  // two at a time, so that one is on its way while the other is used.
   Part a, b;
-  const int step = 32 * U * W;
-  int k0 = from + 32 * U * w;
-  if (k0 < k) {
-    load(a, k0);
-    for (; k0 + step < k; k0 += 2 * step) {
-      load(b, k0 + step);
+  const int pieces = (k - from + 32 * U - 1) / (32 * U);
+  const int first = begin % max(pieces, 1);
+  auto place = [&](int v) {
+    const int c = v + first;
+    return from + 32 * U * (c < pieces ? c : c - pieces);
+  };
+  int v = w;
+  if (v < pieces) {
+    load(a, place(v));
+    for (; v + W < pieces; v += 2 * W) {
+      load(b, place(v + W));
       use(a);
-      if (k0 + 2 * step < k) load(a, k0 + 2 * step);
+      if (v + 2 * W < pieces) load(a, place(v + 2 * W));
       use(b);
     }
-    if (k0 < k) use(a);
+    if (v < pieces) use(a);
   }
 #pragma unroll
   for (int i = 0; i < RM; ++i)
@@ -856,7 +961,8 @@ __device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at
     p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + c : kOutside;
   few_product<T, RM, RN>(
       buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
-      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, from, k, sums, w, lane);
+      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, from, k,
+      n0 / (16 * RN) + 3 * at.group, sums, w, lane);
 }
 
 // D = A B[g]^T, groups of few rows

@@ -102,27 +102,29 @@ Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
 }
 
 // Kernel for `places` rows of `groups` matrices of n x k.  The lengths are on
-// the device, so the rule goes by their mean.  Microseconds, bf16, half of the
-// groups a quarter of the places and half three quarters:
+// the device, so the rule goes by their mean.  Microseconds, bf16, weights from
+// memory (not the caches), half of the groups a quarter of the places and half
+// three quarters:
 //
 //   groups mean    n     k   FEW  128  256
-//        2    2  4096  4096   14   41   29   few tiles: FEW goes to all CUs, until
-//        2   64  2048  4096   25   43   31   its tiles read the weights too often
-//        8   64  2048  4096   73   46   33
-//       64    2  1024  2048   49   41   45   many tiles: no kernel for few rows
-//       64   64  1024  2048  162   59   59   is needed
-//        8   64  4096  4096  138   63   60   256 has more loads under way per
-//        8  128  4096  4096    -   72   61   workgroup, 128 two workgroups per
-//        8  256  4096  4096    -   87   93   CU if there are as many, and less
-//       32  256  1024  2048    -   38   53   left over at the groups' ends
-//        8  512  4096  4096    -  170  122
-//       32  512  1024  2048    -   69   62
+//        2   16  4096  4096   20   59   46   FEW goes to more CUs, as long as its
+//        2  128  2048  4096   30   60   50   small tiles do not read the weights
+//        8   16  2048  4096   37   61   50   and rows too often
+//        8   16  4096  4096   70   65   55
+//       64    4  1024  2048   52   51   45
+//        8   64  4096  4096    -   75   73   256 has more loads under way per
+//       64   64  1024  2048    -   67   59   workgroup
+//        8  256  4096  4096    -   94  108   128 leaves less over at the groups'
+//       32  256  1024  2048    -   56   59   ends, if it fills the chip twice
+//        8  512  4096  4096    -  172  128
+//       32  512  1024  2048    -   92   76
 int choose_algo(int64_t places, int64_t groups, int64_t n, int64_t k, bool few) {
-  const int64_t mean = ceil_div(places, groups), held = places < groups ? places : groups;
-  if (few && mean * held * ceil_div(n, 256) <= 768) return kFew;
+  const int64_t mean = ceil_div(places, groups), held = places < groups ? places : groups,
+                tiles = held * ceil_div(n, 256);
+  if (few && tiles < kFill && mean * tiles <= (tiles <= 32 ? 2048 : 1024)) return kFew;
   if (mean >= 512) return kTile256;
-  const int64_t whole = places / 128 + held / 2, slots = whole > held ? whole : held;
-  return slots * ceil_div(n, 128) >= 2 * kFill || k < 2048 ? kTile128 : kTile256;
+  const bool fills = (places / 128 + held / 2) * ceil_div(n, 128) >= 2 * kFill;
+  return k < 1024 || (mean > 128 && fills) ? kTile128 : kTile256;
 }
 
 Choice choose(const mfl_grouped_t& a) {
@@ -145,17 +147,18 @@ void place(GroupedParams& p, const Choice& c) {
   p.band = c.algo == kFew ? 0 : c.algo == kTile256 ? 4 : 8;
 }
 
-// Both gradients, in one launch: the kernel, and each one's tiles.
+// Both gradients, in one launch: the kernel, and each one's tiles.  (Tiles of
+// 128 x 128 are no faster anywhere: 16 groups of 42 rows, 1024 x 512, 16 us
+// either way, 8 of 1024, 4096 x 2048, 321 and 269.)
 struct Backward {
   Choice da, db;
 };
 Backward choose_backward(const mfl_grouped_t& f, bool gathered) {
   const bool bf16 = f.dtype == MFL_BF16, f32 = f.out == MFL_F32;
   Backward r;
-  const int algo = f.algo ? f.algo : choose_algo(f.places, f.groups, f.k, f.n, false);
-  const KernelRef k = backward_kernel(bf16, f32, algo, gathered);
-  r.da = with(k, algo, f, f.k);
-  r.db = {algo, k, f.groups * ceil_div(f.n, k.bm), ceil_div(f.k, k.bn)};
+  const KernelRef k = backward_kernel(bf16, f32, gathered);
+  r.da = with(k, kTile256, f, f.k);
+  r.db = {kTile256, k, f.groups * ceil_div(f.n, k.bm), ceil_div(f.k, k.bn)};
   return r;
 }
 
@@ -164,7 +167,7 @@ int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, c
   const mfl_grouped_t& f = a.f;
   int rc = check_grouped(f, A, B, offsets, rows, dD);
   if (rc) return rc;
-  if (f.algo == MFL_GROUPED_FEW) return MFL_E_ALGO_CASE;
+  if (f.algo != MFL_GROUPED_AUTO) return MFL_E_ALGO_CASE;
   if ((rc = check_stride(a.ldda, f.k)) || (rc = check_stride(a.lddb, f.k)) ||
       (rc = check_group_stride(a.db_group, f.n, a.lddb, f.k, f.groups, true)))
     return rc;

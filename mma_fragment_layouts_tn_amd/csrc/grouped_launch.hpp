@@ -75,7 +75,7 @@ struct KernelRef {
 enum Algo { kAuto, kFew, kTile128, kTile256 };
 KernelRef rows_kernel(bool bf16, bool f32, int algo);                   // D
 KernelRef few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
-KernelRef backward_kernel(bool bf16, bool f32, int algo, bool gathered);   // dA and dB
+KernelRef backward_kernel(bool bf16, bool f32, bool gathered);   // dA and dB
 KernelRef down_kernel(bool bf16, int row_blocks, int column_blocks);
 KernelRef down_rows_kernel(bool bf16);
 KernelRef adapters_first_kernel(bool bf16, int row_blocks);

@@ -152,20 +152,18 @@ def test_few_shapes(rows):
         Case("f16", [rows, 2 * rows, 0], n, 520, gather=True).check_forward(algo="few")
 
 
-@pytest.mark.parametrize("algo", ["tile128", "tile256"])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("lens", LENS, ids=str)
-def test_gradient_lengths(lens, gather, algo):
-    Case("bf16", lens, 136, 200, gather=gather).check_backward(algo=algo)
+def test_gradient_lengths(lens, gather):
+    Case("bf16", lens, 136, 200, gather=gather).check_backward()
 
 
-@pytest.mark.parametrize("algo", ["tile128", "tile256"])
 @pytest.mark.parametrize("n,k", [(8, 8), (16, 64), (264, 128), (248, 72), (512, 1000)])
 @pytest.mark.parametrize("kind,db", [("f16", "f16"), ("f16", "f32"), ("bf16", "bf16"),
                                      ("bf16", "f32")])
 @pytest.mark.parametrize("gather", [False, True])
-def test_gradient_sizes(kind, db, n, k, gather, algo):
-    Case(kind, [40, 3, 70, 0, 130], n, k, gather=gather).check_backward(db, algo=algo)
+def test_gradient_sizes(kind, db, n, k, gather):
+    Case(kind, [40, 3, 70, 0, 130], n, k, gather=gather).check_backward(db)
 
 
 @pytest.mark.parametrize("gather", [False, True])
@@ -187,8 +185,8 @@ def test_places_of_no_group(algo):
     assert got is D and bool((D[c.used:] == 7).all())
     want, tol = G.product(f64(c.A), f64(c.B), c.offsets.numpy(), None, "bf16")
     within("D", D[:c.used], want[:c.used], tol[:c.used])
-    if algo != "few":
-        c.check_backward(algo=algo)
+    if algo == "few":
+        c.check_backward()
 
 
 @pytest.mark.parametrize("algo", ["few", "tile128", "tile256"])
@@ -196,8 +194,8 @@ def test_rows_from_outside_are_zeros(algo):
     c = Case("f16", [30, 40], 64, 96, gather=True)
     c.rows[::3] = torch.tensor([-1, c.A.shape[0], 2 ** 31 - 1, -2 ** 31]).repeat(20)[:24].int()
     c.check_forward(algo=algo)
-    if algo != "few":
-        c.check_backward(algo=algo)
+    if algo == "few":
+        c.check_backward()
 
 
 @pytest.mark.parametrize("algo", ["few", "tile128", "tile256"])
@@ -210,10 +208,9 @@ def test_groups_are_apart(algo):
     D = c.forward(algo=algo)
     keep = torch.cat([torch.arange(17), torch.arange(47, 117)])
     assert torch.equal(D[keep], clean[keep])
-    if algo != "few":
+    if algo == "few":
         c.dD[17:47] = float("inf")
-        dA, dB = mfl.gemm_grouped_backward(c.dD.cuda(), c.A.cuda(), c.B.cuda(), c.offsets.cuda(),
-                                           algo=algo)
+        dA, dB = mfl.gemm_grouped_backward(c.dD.cuda(), c.A.cuda(), c.B.cuda(), c.offsets.cuda())
         assert bool(torch.isfinite(dA[keep]).all())
         assert bool(torch.isfinite(dB[0]).all()) and bool(torch.isfinite(dB[2]).all())
 
