@@ -186,16 +186,42 @@ def _code(names: str, first: torch.Tensor, *others) -> int:
 
 
 def _grouped_args(A, B, offsets, rows, out: int, algo: str, places: int, ldd: int):
-    code = _code("A and B", A, B)
-    lda = _matrix(A, "A")
-    ldb, b_group = _matrices(B, "B")
+    # (a call for few rows is as long as this takes: one look at what is usual,
+    # the helpers for the rest)
+    sa, sb, dt = A.stride(), B.stride(), A.dtype
+    code = _DTYPES.get(dt)
+    if code is None or B.dtype is not dt or len(sa) != 2 or len(sb) != 3 or sa[1] != 1 or \
+            sb[2] != 1:
+        code = _code("A and B", A, B)
+        _matrix(A, "A")
+        _matrices(B, "B")
+    m, ka = A.shape
     groups, n, k = B.shape
-    if A.shape[1] != k:
+    if ka != k:
         raise ValueError("A and B disagree on K")
-    _numbers(offsets, "offsets", groups + 1)
-    _numbers(rows, "rows")
-    return GroupedArgs(code, out, GROUPED_ALGOS[algo], groups, places, A.shape[0], n, k, lda, ldb,
-                       b_group, ldd)
+    if offsets.dtype is not _int32 or offsets.numel() != groups + 1 or offsets.dim() != 1 or \
+            not offsets.is_contiguous():
+        _numbers(offsets, "offsets", groups + 1)
+    if rows is not None and (rows.dtype is not _int32 or rows.dim() != 1 or
+                             not rows.is_contiguous()):
+        _numbers(rows, "rows")
+    return GroupedArgs(code, out, GROUPED_ALGOS[algo], groups, places, m, n, k,
+                       sa[0] if m > 1 else k, sb[1] if n > 1 else k, sb[0] if groups > 1 else 0,
+                       ldd)
+
+
+def _dense(t: torch.Tensor, run: _Here) -> torch.Tensor:
+    """t, or where its rows do not follow each other whole (a sum's gradient,
+    expanded) a contiguous copy, made on the stream that reads it."""
+    if t.dim() != 2 or t.numel() == 0:
+        return t
+    s, (r, c) = t.stride(), t.shape
+    if s[1] == 1 and (r < 2 or s[0] >= c):
+        return t
+    if run.other is None:
+        return t.contiguous()
+    with torch.cuda.stream(run.other):
+        return t.contiguous()
 
 
 # ------------------------------------------------------------------ functions
@@ -226,10 +252,11 @@ def group_rows(ids: torch.Tensor, groups: int, *, stream=None):
     if groups < 1:
         raise ValueError("there must be a group")
     run = _Here(stream, ids)
-    # (one allocation: it takes longer than the kernels for a few choices)
+    # (one allocation: each takes a third of the time of the kernel for a few
+    # choices)
     n = ids.numel()
-    rows, offsets, slots = run.empty((2 * n + groups + 1,), torch.int32).split_with_sizes(
-        (n, groups + 1, n))
+    rows, offsets, slots = torch.unsafe_split_with_sizes(
+        _new(run, ids, (2 * n + groups + 1,), _int32), (n, groups + 1, n))
     if ids.dim() == 2:
         slots = slots.view(ids.shape)
     ptrs = _ptr(ids), _ptr(rows), _ptr(offsets), _ptr(slots)
@@ -292,19 +319,21 @@ def gemm_grouped_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
     dA (places, K) has a row per place, 0 for those of no group; where rows
     gathers, combine_rows(dA, slots) adds the rows of each token.  dB has B's
     shape and type, or float32 with dB_dtype; 0 for groups without places.
-    The same arguments give the same bits."""
+    An expanded or transposed dD is copied first.  The same arguments give the
+    same bits."""
     places = A.shape[0] if rows is None else rows.shape[0]
     out = _type(dB_dtype, A.dtype, "dB")
     if dD.dtype != A.dtype:
         raise TypeError("dD must have A's dtype")
     if B.dim() != 3 or dD.shape != (places, B.shape[1]):
         raise ValueError("dD must be (places, N)")
+    run = _Here(stream, dD, A, B, offsets, rows)
+    dD = _dense(dD, run)
     f = _grouped_args(A, B, offsets, rows, out, "auto", places, _matrix(dD, "dD"))
     k, n = B.shape[2], B.shape[1]
     a = GroupedGradArgs(f, k, k, n * k)
-    run = _Here(stream, dD, A, B, offsets, rows)
     dA = _new(run, A, (places, k), None)
-    dB = _new(run, B, B.shape, dB_dtype)
+    dB = run.like(B) if dB_dtype is None else _new(run, B, B.shape, dB_dtype)
     _call(run, _lib.gemm_tn_grouped_backward, a, _ptr(dD), _ptr(A), _ptr(B), _ptr(offsets),
           _ptr(rows), _ptr(dA), _ptr(dB))
     return dA, dB
@@ -361,16 +390,17 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
     rows (places,) int32: each place's token, as group_rows gives it with
     slots.  dX has X's shape; a place that no choice of its token leads to has
     gradient 0, and so has the weight of a choice without a place.  dweights is
-    None without weights."""
+    None without weights.  An expanded or transposed dout is copied first."""
     if dout.dtype != X.dtype:
         raise TypeError("dout must have X's dtype")
     if X.dim() != 2 or dout.shape != (slots.shape[0], X.shape[1]):
         raise ValueError("dout must be (tokens, N)")
+    run = _Here(stream, dout, X, slots, weights, rows)
+    dout = _dense(dout, run)
     a = _combine_args(X, slots, weights, _TYPES.get(X.dtype, 0), _matrix(dout, "dout"))
     _numbers(rows, "rows", X.shape[0])
-    run = _Here(stream, dout, X, slots, weights, rows)
-    dX = _new(run, X, X.shape, None)
-    dw = None if weights is None else _new(run, weights, weights.shape, None)
+    dX = run.like(X)
+    dw = None if weights is None else run.like(weights)
     _call(run, _lib.combine_rows_backward, a, X.shape[1], _ptr(dout), _ptr(X), _ptr(slots),
           _ptr(rows), _ptr(weights), _ptr(dX), _ptr(dw))
     return dX, dw
@@ -378,26 +408,34 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
 
 def _adapters_args(x, W, A, B, offsets, rows, scale, out: int, algo: str, ldd: int):
     code = _code("x, W, A and B", x, W, A, B)
-    ldx, ldw = _matrix(x, "x"), _matrix(W, "W")
-    lda, a_group = _matrices(A, "A")
-    ldb, b_group = _matrices(B, "B")
+    sx, sw, sa, sb = x.stride(), W.stride(), A.stride(), B.stride()
+    if len(sx) != 2 or len(sw) != 2 or len(sa) != 3 or len(sb) != 3 or \
+            not sx[1] == sw[1] == sa[2] == sb[2] == 1:
+        _matrix(x, "x")
+        _matrix(W, "W")
+        _matrices(A, "A")
+        _matrices(B, "B")
     (m, k), (n, kw), (groups, rank, ka) = x.shape, W.shape, A.shape
     if kw != k or ka != k:
         raise ValueError("x, W and A disagree on K")
     if B.shape != (groups, n, rank):
         raise ValueError("W, A and B disagree on the adapters, N or the rank")
     _numbers(offsets, "offsets", groups + 1)
-    _numbers(rows, "rows")
-    if rows is not None and rows.shape[0] > m:
-        raise ValueError("rows holds each row at most once")
+    places = m
+    if rows is not None:
+        _numbers(rows, "rows")
+        places = rows.shape[0]
+        if places > m:
+            raise ValueError("rows holds each row at most once")
     if scale is not None:
-        if scale.dtype != torch.float32:
+        if scale.dtype is not _float32:
             raise TypeError("scale must be float32")
-        if scale.shape != (groups,) or (groups > 1 and scale.stride(0) != 1):
+        if scale.dim() != 1 or scale.numel() != groups or not scale.is_contiguous():
             raise ValueError("scale must hold one factor per adapter, contiguous")
-    return AdaptersArgs(code, out, GROUPED_ALGOS[algo], groups,
-                        m if rows is None else rows.shape[0], m, n, k, rank, ldx, ldw, lda,
-                        a_group, ldb, b_group, ldd)
+    return AdaptersArgs(code, out, GROUPED_ALGOS[algo], groups, places, m, n, k, rank,
+                        sx[0] if m > 1 else k, sw[0] if n > 1 else k, sa[1] if rank > 1 else k,
+                        sa[0] if groups > 1 else 0, sb[1] if n > 1 else rank,
+                        sb[0] if groups > 1 else 0, ldd)
 
 
 def gemm_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Tensor,

@@ -77,8 +77,17 @@ int check_grouped(const mfl_grouped_t& a, const void* A, const void* B, const in
   if (rows && a.a_rows * a.lda > kMaxGather) return MFL_E_TOO_LARGE;
   if (!aligned(A) || !aligned(B) || !aligned(D) || !aligned4(offsets) || !aligned4(rows))
     return MFL_E_MISALIGNED;
-  if (D && (D == A || D == B)) return MFL_E_ALIAS;
   return MFL_OK;
+}
+bool is_one_of(const void* p, std::initializer_list<const void*> others) {
+  for (const void* x : others)
+    if (p && p == x) return true;
+  return false;
+}
+int check_forward(const mfl_grouped_t& a, const void* A, const void* B, const int32_t* offsets,
+                  const int32_t* rows, const void* D) {
+  const int rc = check_grouped(a, A, B, offsets, rows, D);
+  return rc ? rc : is_one_of(D, {A, B, offsets, rows}) ? MFL_E_ALIAS : MFL_OK;
 }
 
 // `bm`-place tiles over the groups and what is behind them, at most; the
@@ -172,10 +181,8 @@ int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, c
       (rc = check_group_stride(a.db_group, f.n, a.lddb, f.k, f.groups, true)))
     return rc;
   if (!aligned(dA) || !aligned(dB)) return MFL_E_MISALIGNED;
-  const void* in[3] = {dD, A, B};
-  for (const void* x : in)
-    if ((dA && dA == x) || (dB && dB == x)) return MFL_E_ALIAS;
-  if (dA && dA == dB) return MFL_E_ALIAS;
+  if (is_one_of(dA, {dD, A, B, offsets, rows, dB}) || is_one_of(dB, {dD, A, B, offsets, rows}))
+    return MFL_E_ALIAS;
   const Backward r = choose_backward(f, rows != nullptr);
   return r.da.blocks() + r.db.blocks() > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
 }
@@ -205,8 +212,7 @@ int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const 
   if (!aligned(x) || !aligned(W) || !aligned(A) || !aligned(B) || !aligned(D) ||
       !aligned4(offsets) || !aligned4(rows) || !aligned4(scale))
     return MFL_E_MISALIGNED;
-  if (D && (D == x || D == W || D == A || D == B)) return MFL_E_ALIAS;
-  return MFL_OK;
+  return is_one_of(D, {x, W, A, B, offsets, rows, scale}) ? MFL_E_ALIAS : MFL_OK;
 }
 
 // The shared product is on tiles of places whatever their group; the down
@@ -284,9 +290,10 @@ int check_sort(const mfl_group_rows_t& a, const void* ids, const int32_t* rows,
   if ((uintptr_t)ids % (a.ids_type == MFL_I64 ? 8 : 4) || !aligned4(rows) || !aligned4(offsets) ||
       !aligned4(slots))
     return MFL_E_MISALIGNED;
-  if (rows && (rows == ids || rows == offsets || rows == slots)) return MFL_E_ALIAS;
-  if (slots && (slots == ids || slots == offsets)) return MFL_E_ALIAS;
-  return offsets == ids ? MFL_E_ALIAS : MFL_OK;
+  return is_one_of(rows, {ids, offsets, slots}) || is_one_of(slots, {ids, offsets}) ||
+                 is_one_of(offsets, {ids})
+             ? MFL_E_ALIAS
+             : MFL_OK;
 }
 
 int check_combine(const mfl_combine_t& a, const void* X, const int32_t* slots,
@@ -304,7 +311,6 @@ int check_combine(const mfl_combine_t& a, const void* X, const int32_t* slots,
   if ((rc = check_stride(a.ldx, a.n)) || (rc = check_stride(a.ldo, a.n))) return rc;
   if (!aligned(X) || !aligned(out) || !aligned4(slots) || !aligned4(weights))
     return MFL_E_MISALIGNED;
-  if (out && out == X) return MFL_E_ALIAS;
   return ceil_div(a.tokens * (a.n / 8), 256) > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
 }
 
@@ -365,7 +371,7 @@ int gemm_tn_grouped_plan(const mfl_grouped_t* a, const void* A, const void* B,
                          const int32_t* offsets, const int32_t* rows, const void* D,
                          int32_t* algo) {
   if (!a) return MFL_E_NULL_POINTER;
-  const int rc = check_grouped(*a, A, B, offsets, rows, D);
+  const int rc = check_forward(*a, A, B, offsets, rows, D);
   if (rc) return rc;
   const Choice c = choose(*a);
   if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
@@ -376,7 +382,7 @@ int gemm_tn_grouped_plan(const mfl_grouped_t* a, const void* A, const void* B,
 int gemm_tn_grouped(const mfl_grouped_t* a, const void* A, const void* B, const int32_t* offsets,
                     const int32_t* rows, void* D, void* stream) {
   if (!a) return MFL_E_NULL_POINTER;
-  const int rc = check_grouped(*a, A, B, offsets, rows, D);
+  const int rc = check_forward(*a, A, B, offsets, rows, D);
   if (rc) return rc;
   const Choice c = choose(*a);
   if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
@@ -524,6 +530,7 @@ int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,
   if (!a) return MFL_E_NULL_POINTER;
   const int rc = check_combine(*a, X, slots, weights, out);
   if (rc) return rc;
+  if (is_one_of(out, {X, slots, weights})) return MFL_E_ALIAS;
   CombineRows p = combine_params(*a, X, slots, weights);
   p.out = out;
   return launch(combine_kernel(a->dtype == MFL_BF16, a->out == MFL_F32),
@@ -542,8 +549,9 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
   rc = check_stride(lddx, a->n);
   if (rc) return rc;
   if (!aligned(dX) || !aligned4(rows) || !aligned4(dw)) return MFL_E_MISALIGNED;
-  if (dX && (dX == X || dX == dout)) return MFL_E_ALIAS;
-  if (dw && dw == weights) return MFL_E_ALIAS;
+  if (is_one_of(dX, {X, dout, slots, rows, weights, dw}) ||
+      is_one_of(dw, {X, dout, slots, rows, weights}))
+    return MFL_E_ALIAS;
   CombineRows p = combine_params(*a, X, slots, weights);
   p.dout = dout;
   p.rows = rows;
