@@ -387,23 +387,25 @@ struct PlainColumns : ColumnLoads<R, N> {
 template <int R, int N>
 struct GatheredColumns : ColumnLoads<R, N> {
   using Base = ColumnLoads<R, N>;
-  __amdgpu_buffer_rsrc_t r, list;
+  __amdgpu_buffer_rsrc_t r;
+  const int* index;
   int ld, total, count;
   int next[N];       // indices of the step whose loads are issued next
-  __device__ __forceinline__ void init(const void* b, const int* index, int n, int ld_, int total_,
+  __device__ __forceinline__ void init(const void* b, const int* index_, int n, int ld_, int total_,
                                        int col0, int width, int w, int lane) {
     Base::init(col0, width, w, lane);
     r = buffer(b, kWhole);
-    list = buffer(index, 4 * min(n, 1 << 28));
+    index = index_;
     ld = ld_;
     total = total_;
     count = n;
   }
   __device__ __forceinline__ void ahead(int kt) {
+    const int left = min(max(count - 64 * kt, 0), 64);
+    const __amdgpu_buffer_rsrc_t list = buffer(index + 64 * (int64_t)kt, 4 * left);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      next[i] = __builtin_amdgcn_raw_buffer_load_b32(
-          list, 4 * (64 * kt + this->row0 + Base::RUN * i), 0, 0);
+      next[i] = __builtin_amdgcn_raw_buffer_load_b32(list, 4 * (this->row0 + Base::RUN * i), 0, 0);
   }
   __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
     const int row = next[i];

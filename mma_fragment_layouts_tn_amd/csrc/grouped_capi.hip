@@ -17,17 +17,19 @@ constexpr int64_t kMaxCount = (int64_t)INT_MAX - (1 << 16);
 constexpr int64_t kMaxExtent = (int64_t)1 << 21;     // n, k, strides between rows
 constexpr int64_t kMaxGroupStride = (int64_t)1 << 42;
 constexpr int64_t kMaxGather = ((int64_t)1 << 30) - 1;   // elements a gathered operand spans
-constexpr int64_t kMaxBlocks = ((int64_t)1 << 24) - 1;
 
 bool aligned(const void* p) { return (uintptr_t)p % 16 == 0; }
 bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool half_type(int32_t t) { return t == MFL_F16 || t == MFL_BF16; }
 
+// a launch has fewer than 2^32 threads
+bool fits(const KernelRef& k, int64_t blocks) { return blocks < ((int64_t)1 << 32) / k.threads; }
+
 int launch(const KernelRef& k, int64_t blocks, void* params, void* stream, void* more = nullptr,
            void* rest = nullptr) {
   if (blocks == 0) return MFL_OK;
-  if (blocks > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (!fits(k, blocks)) return MFL_E_TOO_LARGE;
   void* args[] = {params, more, rest};   // (a kernel takes as many as it has)
   const hipError_t e = hipLaunchKernel(k.fn, dim3((unsigned)blocks), dim3(k.threads), args, 0,
                                        (hipStream_t)stream);
@@ -184,7 +186,7 @@ int check_backward(const mfl_grouped_grad_t& a, const void* dD, const void* A, c
   if (is_one_of(dA, {dD, A, B, offsets, rows, dB}) || is_one_of(dB, {dD, A, B, offsets, rows}))
     return MFL_E_ALIAS;
   const Backward r = choose_backward(f, rows != nullptr);
-  return r.da.blocks() + r.db.blocks() > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
+  return fits(r.da.kernel, r.da.blocks() + r.db.blocks()) ? MFL_OK : MFL_E_TOO_LARGE;
 }
 
 int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const void* A,
@@ -296,6 +298,13 @@ int check_sort(const mfl_group_rows_t& a, const void* ids, const int32_t* rows,
              : MFL_OK;
 }
 
+// a thread per eight columns of a token; a wave per place or choice
+int64_t sum_blocks(const mfl_combine_t& a) { return ceil_div(a.tokens * (a.n / 8), 256); }
+int64_t grad_blocks(const mfl_combine_t& a) {
+  const int64_t choices = a.tokens * a.top;
+  return ceil_div(a.x_rows > choices ? a.x_rows : choices, 4);
+}
+
 int check_combine(const mfl_combine_t& a, const void* X, const int32_t* slots,
                   const float* weights, const void* out) {
   if (a.tokens < 0 || a.top < 0 || a.n < 0 || a.x_rows < 0) return MFL_E_NEGATIVE_DIM;
@@ -311,7 +320,7 @@ int check_combine(const mfl_combine_t& a, const void* X, const int32_t* slots,
   if ((rc = check_stride(a.ldx, a.n)) || (rc = check_stride(a.ldo, a.n))) return rc;
   if (!aligned(X) || !aligned(out) || !aligned4(slots) || !aligned4(weights))
     return MFL_E_MISALIGNED;
-  return ceil_div(a.tokens * (a.n / 8), 256) > kMaxBlocks ? MFL_E_TOO_LARGE : MFL_OK;
+  return fits(combine_kernel(false, false), sum_blocks(a)) ? MFL_OK : MFL_E_TOO_LARGE;
 }
 
 CombineRows combine_params(const mfl_combine_t& a, const void* X, const int32_t* slots,
@@ -374,7 +383,7 @@ int gemm_tn_grouped_plan(const mfl_grouped_t* a, const void* A, const void* B,
   const int rc = check_forward(*a, A, B, offsets, rows, D);
   if (rc) return rc;
   const Choice c = choose(*a);
-  if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (!fits(c.kernel, c.blocks())) return MFL_E_TOO_LARGE;
   if (algo) *algo = c.algo;
   return MFL_OK;
 }
@@ -385,7 +394,7 @@ int gemm_tn_grouped(const mfl_grouped_t* a, const void* A, const void* B, const 
   const int rc = check_forward(*a, A, B, offsets, rows, D);
   if (rc) return rc;
   const Choice c = choose(*a);
-  if (c.blocks() > kMaxBlocks) return MFL_E_TOO_LARGE;
+  if (!fits(c.kernel, c.blocks())) return MFL_E_TOO_LARGE;
   if (a->places == 0) return MFL_OK;
   GroupedParams p{};
   p.p = B;
@@ -463,7 +472,8 @@ int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W,
   const int rc = check_adapters(*a, x, W, A, B, offsets, rows, scale, D);
   if (rc) return rc;
   const AdaptersPlan r = plan_adapters(*a);
-  if (r.down.blocks() > kMaxBlocks || first_blocks(r) > kMaxBlocks || r.join_blocks > kMaxBlocks)
+  if (!fits(r.down.kernel, r.down.blocks()) || !fits(r.all.kernel, first_blocks(r)) ||
+      !fits(adapters_join_kernel(false, false), r.join_blocks))
     return MFL_E_TOO_LARGE;
   if (algo) *algo = r.all.algo;
   if (workspace_bytes) *workspace_bytes = r.bytes;
@@ -534,7 +544,7 @@ int combine_rows(const mfl_combine_t* a, const void* X, const int32_t* slots,
   CombineRows p = combine_params(*a, X, slots, weights);
   p.out = out;
   return launch(combine_kernel(a->dtype == MFL_BF16, a->out == MFL_F32),
-                ceil_div(a->tokens * (a->n / 8), 256), &p, stream);
+                sum_blocks(*a), &p, stream);
 }
 
 int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout, const void* X,
@@ -544,6 +554,7 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
   int rc = check_combine(*a, X, slots, weights, dout);
   if (rc) return rc;
   if (a->out != a->dtype) return MFL_E_UNSUPPORTED;
+  if (!fits(combine_grad_kernel(false), grad_blocks(*a))) return MFL_E_TOO_LARGE;
   if (a->x_rows > 0 && (!rows || !dX)) return MFL_E_NULL_POINTER;
   if (dw && !weights) return MFL_E_UNSUPPORTED;
   rc = check_stride(lddx, a->n);
@@ -558,8 +569,7 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
   p.dx = dX;
   p.dw = dw;
   p.lddx = lddx;
-  const int64_t choices = a->tokens * a->top, waves = a->x_rows > choices ? a->x_rows : choices;
-  return launch(combine_grad_kernel(a->dtype == MFL_BF16), ceil_div(waves, 4), &p, stream);
+  return launch(combine_grad_kernel(a->dtype == MFL_BF16), grad_blocks(*a), &p, stream);
 }
 
 }  // extern "C"
