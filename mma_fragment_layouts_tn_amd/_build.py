@@ -107,8 +107,9 @@ def _blocks(lines):
 
 # sources whose kernels tie accumulators to other instructions by hand: every
 # matrix instruction is taken for one of them
-TIED_SOURCES = {"attention_dkv.hip", "grouped_rows.hip", "grouped_backward.hip",
-                "adapters_rows.hip"}
+TIED_SOURCES = {"attention_dkv.hip"}
+# the same of the 16x16x32 instructions of both types
+TIED_GROUPED = {"grouped_rows.hip", "grouped_backward.hip", "adapters_rows.hip"}
 
 
 def check_mfma_fences(asm_text: str, where: str, tied=None, prefix=None) -> int:
@@ -181,7 +182,8 @@ def check_mfma_fences(asm_text: str, where: str, tied=None, prefix=None) -> int:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
-    checked = src in CHECKED_SOURCES | TIED_SOURCES
+    tied = src in TIED_SOURCES | TIED_GROUPED
+    checked = tied or src in CHECKED_SOURCES
     extra = ["-save-temps=obj"] if checked else []   # keeps the device assembly in OBJDIR
     cmd = [HIPCC, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -192,7 +194,7 @@ def _compile(src: str) -> str:
         asm = os.path.join(OBJDIR, f"{stem}-hip-amdgcn-amd-amdhsa-gfx950.s")
         with open(asm) as f:
             text = f.read()
-        how = dict(tied=True, prefix="v_mfma_") if src in TIED_SOURCES else {}
+        how = dict(tied=True, prefix="v_mfma_") if tied else {}
         if check_mfma_fences(text, src, **how) == 0:
             raise RuntimeError(f"{src}: no kernel issues a matrix instruction")
     return obj
