@@ -157,7 +157,8 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
  * they are.
  *
  * Kernels as above: FEW adds the low-rank terms row by row, the TILEs by runs
- * of one group.  The workspace: 4 bytes per place, places x rank numbers of 4
+ * of one group.  Small problems of a rank up to 64 are one launch by FEW and need
+ * no workspace (0 bytes, NULL will do).  For others: 4 bytes per place, places x rank numbers of 4
  * bytes (6 for TILE with an fp32 D), up to 32 for alignment, and with FEW
  * places x n numbers of 4 bytes for each of its parts of k, which are at most
  * one for 256 of k and about 256 / (tiles of 64 columns). */

@@ -67,9 +67,9 @@ def declare(lib: ctypes.CDLL) -> None:
     lib.combine_rows_backward.argtypes = [P(CombineArgs), _i64] + [_vp] * 8
     lib.gemm_tn_adapters.argtypes = [P(AdaptersArgs)] + [_vp] * 9 + [_i64, _vp]
     lib.gemm_tn_adapters_plan.argtypes = [P(AdaptersArgs)] + [_vp] * 8 + [P(_i32), P(_i64)]
-    for n in ("gemm_tn_adapters", "gemm_tn_adapters_plan", "group_rows", "group_rows_plan", "gemm_tn_grouped", "gemm_tn_grouped_plan",
+    for n in ("group_rows", "group_rows_plan", "gemm_tn_grouped", "gemm_tn_grouped_plan",
               "gemm_tn_grouped_backward", "gemm_tn_grouped_backward_plan", "combine_rows",
-              "combine_rows_backward"):
+              "combine_rows_backward", "gemm_tn_adapters", "gemm_tn_adapters_plan"):
         getattr(lib, n).restype = ctypes.c_int
 
 
@@ -407,8 +407,10 @@ def combine_rows_backward(dout: torch.Tensor, X: torch.Tensor, slots: torch.Tens
 
 
 def _adapters_args(x, W, A, B, offsets, rows, scale, out: int, algo: str, ldd: int):
-    code = _code("x, W, A and B", x, W, A, B)
-    sx, sw, sa, sb = x.stride(), W.stride(), A.stride(), B.stride()
+    sx, sw, sa, sb, dt = x.stride(), W.stride(), A.stride(), B.stride(), x.dtype
+    code = _DTYPES.get(dt)
+    if code is None or not dt is W.dtype is A.dtype is B.dtype:
+        code = _code("x, W, A and B", x, W, A, B)
     if len(sx) != 2 or len(sw) != 2 or len(sa) != 3 or len(sb) != 3 or \
             not sx[1] == sw[1] == sa[2] == sb[2] == 1:
         _matrix(x, "x")
@@ -420,10 +422,13 @@ def _adapters_args(x, W, A, B, offsets, rows, scale, out: int, algo: str, ldd: i
         raise ValueError("x, W and A disagree on K")
     if B.shape != (groups, n, rank):
         raise ValueError("W, A and B disagree on the adapters, N or the rank")
-    _numbers(offsets, "offsets", groups + 1)
+    if offsets.dtype is not _int32 or offsets.numel() != groups + 1 or offsets.dim() != 1 or \
+            not offsets.is_contiguous():
+        _numbers(offsets, "offsets", groups + 1)
     places = m
     if rows is not None:
-        _numbers(rows, "rows")
+        if rows.dtype is not _int32 or rows.dim() != 1 or not rows.is_contiguous():
+            _numbers(rows, "rows")
         places = rows.shape[0]
         if places > m:
             raise ValueError("rows holds each row at most once")

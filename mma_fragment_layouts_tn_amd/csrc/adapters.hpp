@@ -3,12 +3,13 @@
 //   D(r, n) = sum_k x(r, k) W(n, k) + s_g sum_j h(r, j) B(g, n, j)
 //   h(r, j) = sum_k x(r, k) A(g, j, k)             r = rows[place], place in group g
 //
-// Two launches.  The first forms s_g h for every place (few columns: the
-// kernel for few rows, by group).  The second is the shared product on tiles
-// of places whatever their group, so that W is read for all of them together,
-// and adds the low-rank terms of the tile's groups to its sums before they
-// are rounded.  A group's term reaches the rows of its own places alone, so
-// infinities in one adapter stay with its requests.
+// Small problems take one launch (adapters_one), others two.  The first forms
+// s_g h for every place (few columns: the kernel for few rows, by group).  The
+// second is the shared product on tiles of places whatever their group, so
+// that W is read for all of them together, and adds the low-rank terms of the
+// tile's groups to its sums before they are rounded.  A group's term reaches
+// the rows of its own places alone, so infinities in one adapter stay with its
+// requests.
 //
 // s_g h is kept to fp32's accuracy: as fp32 values where the second kernel
 // multiplies them out itself (few rows), and as two 16-bit numbers (three
@@ -153,6 +154,85 @@ __global__ void __launch_bounds__(kJoinThreads) adapters_join(const AdapterParam
     y += low;
   }
   Out<O>::store4((O*)p.g.d + (int64_t)row * p.g.ldd + n, y);
+}
+
+// Small problems, one launch: a tile of 16 places of one group (or of none) by
+// 32 columns forms its own h beside the shared product, as RA atoms more of
+// the same contraction, and adds the low-rank term a result per thread.  h is
+// formed again for every 32 columns; what it saves is a launch, the workspace
+// and the wait between the two: 48 rows of 256, rank 16, to 256 columns 4.5 us
+// where two launches take 9.1.  What bounds it is the latency of one pass over
+// the contraction.  B's row is asked for ahead of the product.
+template <int RA>
+struct OneTile {
+  static constexpr int RN = 2, BM = 16, BN = 16 * RN, T = 64 * kFewWaves;
+  static_assert(BM * BN == T, "a result per thread");
+};
+template <class T, class O, int RA>
+__global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_one(const AdapterParams p) {
+  using F = OneTile<RA>;
+  constexpr int RN = F::RN, NB = 2 * RA;
+  __shared__ floatx4 sums[kFewWaves * (RN + RA) * 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  const GroupSpot spot = group_spot<1>(p.g, blockIdx.x, F::BM);
+  if (spot.spot.parts == 0) return;
+  const Place at = spot.at;
+  const int n0 = spot.spot.tn * F::BN;
+  const bool has = at.group < p.g.groups;
+  const int group = has ? at.group : 0;
+  // the thread's result
+  const int m = tid / F::BN, nn = tid % F::BN, n = n0 + nn;
+  const bool mine = m < at.count && n < p.g.n;
+  const int row = mine ? row_at(p.g, at.first + m) : -1;
+  const float scale = p.scale ? p.scale[group] : 1.0f;
+  u32x4_t b[NB];
+  const __amdgpu_buffer_rsrc_t rb =
+      buffer((const T*)p.up + group * p.up_group + (int64_t)n0 * p.ldup, kWhole);
+#pragma unroll
+  for (int c = 0; c < NB; ++c)
+    b[c] = __builtin_amdgcn_raw_buffer_load_b128(
+        rb, has && mine && 8 * c < p.rank ? 2u * (nn * p.ldup + 8 * c) : kOutside, 0, 0);
+
+  const int r = lane & 15;
+  const unsigned c16 = 16u * (lane >> 4);
+  unsigned q_off[1], p_off[RN + RA];
+  few_rows<T, 1>(p.g, at, lane, q_off);
+#pragma unroll
+  for (int j = 0; j < RN; ++j)
+    p_off[j] = n0 + 16 * j + r < p.g.n ? 2u * (16 * j + r) * p.g.ldp + c16 : kOutside;
+#pragma unroll
+  for (int j = 0; j < RA; ++j)
+    p_off[RN + j] =
+        has && 16 * j + r < p.rank ? 2u * (16 * j + r) * p.down.ldp + c16 : kOutside;
+  const __amdgpu_buffer_rsrc_t rw = buffer((const T*)p.g.p + (int64_t)n0 * p.g.ldp, kWhole),
+                               ra = buffer((const T*)p.down.p + group * p.down.p_group, kWhole);
+  few_product<T, 1, RN + RA>(
+      few_base<T>(p.g, at), q_off,
+      [&](int j, bool in, int off) {
+        const unsigned x = in ? p_off[j] : kOutside;
+        return j < RN ? __builtin_amdgcn_raw_buffer_load_b128(rw, x, off, 0)
+                      : __builtin_amdgcn_raw_buffer_load_b128(ra, x, off, 0);
+      },
+      0, p.g.k, spot.spot.tn + 3 * at.group, sums, w, lane);
+  __syncthreads();
+  if (row < 0) return;
+  // value j of the place's columns from atom `atom` on
+  auto value = [&](int atom, int j) {
+    return ((const float*)sums)[((atom + j / 16) * 64 + m + 16 * (j % 16 / 4)) * 4 + j % 4];
+  };
+  float y = value(0, nn), low = 0.0f;
+  if (has) {
+#pragma unroll
+    for (int c = 0; c < NB; ++c) {
+      if (8 * c >= p.rank) break;
+      const Vec8<T> bv = as16(b[c], T());
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        low = __builtin_fmaf(scale * value(RN, 8 * c + e), (float)bv[e], low);
+    }
+    y += low;
+  }
+  ((O*)p.g.d)[(int64_t)row * p.g.ldd + n] = (O)y;
 }
 
 // what adapters_rows leaves out: the pairs of B's numbers of which one is not

@@ -867,13 +867,14 @@ __device__ __forceinline__ att::Vec8<__bf16> as16(const u32x4_t& u, __bf16) {
 }
 
 // The contraction from `from` to k (begun at another place by tiles of other
-// weights, as RowsSource::start, by tiles of the same weights at the same).  q_off, p_off: byte offsets of the lane's rows (kOutside: zeros).  After it
+// weights, as RowsSource::start, by tiles of the same weights at the same).
+// q_off: byte offsets of the lane's rows (kOutside: zeros); load_p(j, in, off):
+// its 16 bytes of atom j's row at off, zeros without `in`.  After it
 // sums[(i RN + j) * 64 + lane] holds the four values of atom (i, j).
-template <class T, int RM, int RN>
+template <class T, int RM, int RN, class LoadP>
 __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const unsigned (&q_off)[RM],
-                                            __amdgpu_buffer_rsrc_t rp, const unsigned (&p_off)[RN],
-                                            int from, int k, int begin, floatx4* sums, int w,
-                                            int lane) {
+                                            LoadP load_p, int from, int k, int begin,
+                                            floatx4* sums, int w, int lane) {
   constexpr int U = few_depth(RM, RN), W = kFewWaves;
   floatx4 acc[RM][RN];
 #pragma unroll
@@ -889,8 +890,7 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
       const bool in = k0 + 32 * u + 8 * (lane >> 4) < k;
 #pragma unroll
       for (int j = 0; j < RN; ++j)
-        x.p[u][j] = __builtin_amdgcn_raw_buffer_load_b128(
-            rp, in ? p_off[j] : kOutside, 2 * k0 + 64 * u, 0);
+        x.p[u][j] = load_p(j, in, 2 * k0 + 64 * u);
 #pragma unroll
       for (int i = 0; i < RM; ++i)
         x.q[u][i] = __builtin_amdgcn_raw_buffer_load_b128(
@@ -939,6 +939,30 @@ __device__ __forceinline__ void few_product(__amdgpu_buffer_rsrc_t rq, const uns
   }
 }
 
+// byte offsets of the lane's rows of Q
+template <class T, int RM>
+__device__ __forceinline__ void few_rows(const GroupedParams& p, const Place& at, int lane,
+                                         unsigned (&off)[RM]) {
+  const unsigned c = 16u * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
+    const int row = 16 * i + (lane & 15);
+    if (p.rows) {
+      const int a = p.rows[at.first + min(row, at.count - 1)];
+      off[i] = row < at.count && (unsigned)a < (unsigned)p.q_rows
+                   ? 2u * (unsigned)a * p.ldq + c : kOutside;
+    } else {
+      off[i] = row < at.count ? 2u * row * p.ldq + c : kOutside;
+    }
+  }
+}
+// Q of a tile, as few_rows counts it
+template <class T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t few_base(const GroupedParams& p,
+                                                           const Place& at) {
+  return buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole);
+}
+
 // the tile's places against columns n0 .. of the matrix P
 template <class T, int RM, int RN>
 __device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at, int n0,
@@ -947,24 +971,17 @@ __device__ __forceinline__ void few_tile(const GroupedParams& p, const Place& at
   const int r = lane & 15;
   const unsigned c = 16u * (lane >> 4);
   unsigned q_off[RM], p_off[RN];
-#pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    const int row = 16 * i + r;
-    if (p.rows) {
-      const int a = p.rows[at.first + min(row, at.count - 1)];
-      q_off[i] = row < at.count && (unsigned)a < (unsigned)p.q_rows
-                     ? 2u * (unsigned)a * p.ldq + c : kOutside;
-    } else {
-      q_off[i] = row < at.count ? 2u * row * p.ldq + c : kOutside;
-    }
-  }
+  few_rows<T, RM>(p, at, lane, q_off);
 #pragma unroll
   for (int j = 0; j < RN; ++j)
     p_off[j] = n0 + 16 * j + r < p.n ? 2u * (16 * j + r) * p.ldp + c : kOutside;
+  const __amdgpu_buffer_rsrc_t rp = buffer(P + (int64_t)n0 * p.ldp, kWhole);
   few_product<T, RM, RN>(
-      buffer((const T*)p.q + (p.rows ? 0 : (int64_t)at.first * p.ldq), kWhole), q_off,
-      buffer(P + (int64_t)n0 * p.ldp, kWhole), p_off, from, k,
-      n0 / (16 * RN) + 3 * at.group, sums, w, lane);
+      few_base<T>(p, at), q_off,
+      [&](int j, bool in, int off) {
+        return __builtin_amdgcn_raw_buffer_load_b128(rp, in ? p_off[j] : kOutside, off, 0);
+      },
+      from, k, n0 / (16 * RN) + 3 * at.group, sums, w, lane);
 }
 
 // D = A B[g]^T, groups of few rows

@@ -221,17 +221,44 @@ int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const 
 // projection on tiles of one group.
 struct AdaptersPlan {
   Choice down, all;
+  bool one;                    // one launch, no workspace
   int pieces;                  // 0: h in fp32
   int64_t splits, part_k;      // FEW: parts of the contraction
   int64_t h_at, part_at, bytes;
   int64_t join_blocks;
 };
+// Whether the problem is small enough for one launch, and its tiles.  Each of
+// its workgroups reads 16 rows of x, 32 of W and A's; a contraction longer than
+// that allows is better shared by workgroups, and beyond some 64 MB in all the
+// reading takes longer than a second launch.  Microseconds, bf16, rank 16,
+// weights from memory:
+//
+//   rows  adapters    n     k   one  two launches
+//      1         1   64    64   3.7   5.5
+//     48         8  256   256   4.5   9.1
+//   1000         8  256   256   8.7  17.7
+//     48         8 1024  1024   7.7  10.8
+//     48        64 1024  1024    23    11    (214 MB)
+//      8         1 1024  4096    17    16    (a contraction of 4096)
+//     48         1 4096  4096    33    22
+bool one_launch(const mfl_adapters_t& a, Choice* c) {
+  if (a.rank > 64) return false;
+  const int ra = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
+  const KernelRef k = adapters_one_kernel(a.dtype == MFL_BF16, a.out == MFL_F32, ra);
+  *c = {kFew, k, tile_slots(a.places, a.groups, k.bm), ceil_div(a.n, k.bn)};
+  const int64_t rows = k.bm + k.bn + 16 * ra, tiles = c->blocks();
+  return rows * a.k <= 64 * 2048 && tiles <= 1024 && tiles * rows * a.k * 2 <= (64 << 20);
+}
 AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
   const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
   AdaptersPlan r{};
   const int64_t mean = ceil_div(a.places, a.groups);
   const int algo = a.algo ? a.algo : a.places <= 192 ? kFew
                    : choose_algo(a.places, 1, a.n, a.k, false);
+  if ((algo == kFew || !a.algo) && one_launch(a, &r.all)) {
+    r.one = true;
+    return r;
+  }
   r.all.algo = algo;
   r.down.algo = kFew;
   if (algo == kFew) {
@@ -472,8 +499,8 @@ int gemm_tn_adapters_plan(const mfl_adapters_t* a, const void* x, const void* W,
   const int rc = check_adapters(*a, x, W, A, B, offsets, rows, scale, D);
   if (rc) return rc;
   const AdaptersPlan r = plan_adapters(*a);
-  if (!fits(r.down.kernel, r.down.blocks()) || !fits(r.all.kernel, first_blocks(r)) ||
-      !fits(adapters_join_kernel(false, false), r.join_blocks))
+  if (!r.one && (!fits(r.down.kernel, r.down.blocks()) || !fits(r.all.kernel, first_blocks(r)) ||
+                 !fits(adapters_join_kernel(false, false), r.join_blocks)))
     return MFL_E_TOO_LARGE;
   if (algo) *algo = r.all.algo;
   if (workspace_bytes) *workspace_bytes = r.bytes;
@@ -488,7 +515,8 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   int rc = gemm_tn_adapters_plan(a, x, W, A, B, offsets, rows, scale, D, nullptr, &need);
   if (rc) return rc;
   if (a->places == 0) return MFL_OK;
-  if (!workspace || !aligned(workspace) || workspace_bytes < need) return MFL_E_WORKSPACE;
+  if (need > 0 && (!workspace || !aligned(workspace) || workspace_bytes < need))
+    return MFL_E_WORKSPACE;
   const AdaptersPlan r = plan_adapters(*a);
   AdapterParams p{};
   p.g.q = x;
@@ -504,7 +532,6 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   p.down.n = (int)a->rank;
   p.down.ldp = (int)a->lda;
   p.down.p_group = a->a_group;
-  place(p.down, r.down);
   p.g.p = W;
   p.g.d = D;
   p.g.n = (int)a->n;
@@ -513,15 +540,17 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   place(p.g, r.all);
   p.up = B;
   p.scale = scale;
+  p.up_group = a->b_group;
+  p.rank = (int)a->rank;
+  p.ldup = (int)a->ldb;
+  if (r.one) return launch(r.all.kernel, r.all.blocks(), &p, stream);
+  place(p.down, r.down);
   p.owner = (int*)workspace;
   if (r.pieces)
     p.hp = (char*)workspace + r.h_at;
   else
     p.h = (float*)((char*)workspace + r.h_at);
   p.part = (float*)((char*)workspace + r.part_at);
-  p.up_group = a->b_group;
-  p.rank = (int)a->rank;
-  p.ldup = (int)a->ldb;
   p.pieces = r.pieces;
   if (r.all.algo == kFew) {
     p.down_blocks = (int)r.down.blocks();

@@ -209,7 +209,7 @@ def adapters(ptrs=None, **kw):
     rc = B._lib.gemm_tn_adapters_plan(c, *p.values(), al, n)
     if rc:
         assert B._lib.gemm_tn_adapters(c, *p.values(), 9 * P, 1 << 40, None) == rc
-    elif a["places"]:
+    elif a["places"] and n.value:
         for ws, size in ((None, 1 << 40), (9 * P, n.value - 1), (9 * P + 8, n.value)):
             assert B._lib.gemm_tn_adapters(c, *p.values(), ws, size, None) == WS
     return rc, al.value, n.value
@@ -250,6 +250,9 @@ def test_adapters_plans():
                         parts = (n - least) // part
                         assert 1 <= parts <= 16 and n - least - parts * part <= 32
     assert adapters(places=0, ptrs=dict(x=0, D=0))[0] == 0
+    # small problems need none, unless their rank is large or tiles are asked for
+    assert adapters()[1:] == (1, 0) and adapters(algo=1)[1:] == (1, 0)
+    assert adapters(rank=72, ldb=72)[2] > 0 and adapters(algo=2)[2] > 0
 
 
 # ------------------------------------------------------- the Python functions
@@ -328,6 +331,7 @@ def test_python_adapters_refuses(kw, err):
 
 def test_plans_need_no_gpu():
     assert mfl.gemm_grouped_plan(half(6, 16), half(2, 8, 16), OFF) == "few"
-    algo, need = mfl.gemm_adapters_plan(half(6, 16), half(8, 16), half(2, 8, 16), half(2, 8, 8),
-                                        OFF)
-    assert algo == "few" and need > 0
+    for rank in (8, 72):
+        algo, need = mfl.gemm_adapters_plan(half(6, 16), half(8, 16), half(2, rank, 16),
+                                            half(2, 8, rank), OFF)
+        assert algo == "few" and (need > 0) == (rank > 64)
