@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(S::Full::T, 1) adapters_rows(const AdapterPara
   const Spot s = spot_of<S::kParts>(blockIdx.x, p.g.slots, p.g.tiles_n, p.g.band, INT_MAX);
   if (s.parts == 0) return;
   const Place at{0, s.tm * C::BM, min(p.g.places - s.tm * C::BM, C::BM), false};
-  by_rows<S>(s, at, [&](auto c, const Place& x) {
-    adapters_tile<T, O, decltype(c)>(p, smem, x.first, x.count, s.tn * C::BN);
+  by_rows<S>(s, at, s.tn * C::BN, p.g.n, [&](auto c, const Place& x, int n0) {
+    adapters_tile<T, O, decltype(c)>(p, smem, x.first, x.count, n0);
   });
 }
 

@@ -85,10 +85,10 @@ struct Tile {
 };
 
 // Tiles of 256 x 256 by 8 waves of 128 x 64, two per SIMD, one workgroup per
-// CU.  The tiles of a launch's last, incomplete round are cut in two or four,
-// one part to a workgroup, as long as those find room in the round (kParts),
-// and a tile of few rows is computed as the smaller one: 68 tiles by 8 are 2
-// rounds and a quarter, not 3.
+// CU.  The tiles of a launch's last, incomplete round are cut in up to kParts,
+// one part to a workgroup, as long as those find room in the round, and a tile
+// of few rows is computed as the smaller one: 68 tiles by 8 are 2 rounds and a
+// little, not 3 (by_rows).
 //
 // A smaller tile's step is over before the loads of the next have come (a
 // quarter's: 0.7 us a step with two stages, where its instructions take 0.25),
@@ -97,7 +97,10 @@ struct Tiles256 {
   using Full = Tile<256, 256, 2, 4>;
   using Half = Tile<128, 256, 2, 4, 3>;
   using Quarter = Tile<64, 256, 2, 4, 4>;
-  static constexpr int kParts = 4, kLds = Quarter::LDS;
+  using Corner = Tile<128, 128, 4, 2, 5>;
+  using Eighth = Tile<64, 128, 4, 2, 6>;
+  static constexpr int kParts = 8, kLds = Quarter::LDS;
+  static_assert(kLds >= Corner::LDS && kLds >= Eighth::LDS, "one size for all");
 };
 // the same where both operands are transposed
 struct Weights256 {
@@ -448,7 +451,7 @@ __device__ __forceinline__ Spot spot_of(int id, int tiles_m, int tiles_n, int ba
   int whole = n, parts = 1;
   if constexpr (PARTS > 1) {
     const int rest = n % kFill;
-    parts = rest == 0 ? 1 : rest * 4 <= kFill && PARTS >= 4 ? 4 : rest * 2 <= kFill ? 2 : 1;
+    while (rest > 0 && parts < PARTS && rest * parts * 2 <= kFill) parts *= 2;
     if (parts > 1) whole = n - rest;
   }
   int lin, part = 0;
@@ -735,23 +738,34 @@ __device__ __forceinline__ void rows_tile(const GroupedParams& p, char* smem, co
   store_tile<O, C, !PT>(D, p.ldd, at.count, n0, p.n, acc, w, lane);
 }
 
-// a part of a tile's rows; f with the tile that fits them
+// A part of a tile of places against columns n0 ..; f with the tile that fits
+// it.  The rows there are, to 64, 128 or 256, and 256 columns are halved in
+// turn, so that a part reads as little as it can for its results.  What a part
+// has under way is what LDS holds, and few parts are bound by the latency of
+// it: 2 groups of 150 places, 2048 x 4096, cut by rows alone 46 us, so 29; both
+// gradients of 666 places, 16 groups of 1024 x 512, 20 and 17.
 template <class S, class F>
-__device__ __forceinline__ void by_rows(const Spot& spot, Place at, F f) {
-  using C = typename S::Full;
+__device__ __forceinline__ void by_rows(const Spot& spot, Place at, int n0, int width, F f) {
   if constexpr (S::kParts == 1) {
-    f(C(), at);
+    f(typename S::Full(), at, n0);
   } else {
-    const int rows = C::BM / spot.parts;
-    at.first += spot.part * rows;
-    at.count = min(at.count - spot.part * rows, rows);
-    if (at.count <= 0) return;
-    if (at.count <= S::Quarter::BM)
-      f(typename S::Quarter(), at);
-    else if (at.count <= S::Half::BM)
-      f(typename S::Half(), at);
+    int rows = at.count <= 64 ? 64 : at.count <= 128 ? 128 : 256, cols = 256;
+    if (spot.parts > 1) rows == 256 ? rows = 128 : cols = 128;
+    if (spot.parts > 2) cols == 256 ? cols = 128 : rows = 64;
+    if (spot.parts > 4) rows = 64;
+    const int across = 256 / cols, m = spot.part / across * rows;
+    n0 += spot.part % across * cols;
+    at.first += m;
+    at.count = min(at.count - m, rows);
+    if (at.count <= 0 || n0 >= width) return;
+    if (cols == 128)
+      at.count <= 64 ? f(typename S::Eighth(), at, n0) : f(typename S::Corner(), at, n0);
+    else if (at.count <= 64)
+      f(typename S::Quarter(), at, n0);
+    else if (at.count <= 128)
+      f(typename S::Half(), at, n0);
     else
-      f(C(), at);
+      f(typename S::Full(), at, n0);
   }
 }
 
@@ -761,8 +775,8 @@ __device__ __forceinline__ void rows_part(const GroupedParams& p, char* smem, in
   using C = typename S::Full;
   const GroupSpot x = group_spot<S::kParts>(p, id, C::BM);
   if (x.spot.parts == 0) return;
-  by_rows<S>(x.spot, x.at, [&](auto c, const Place& at) {
-    rows_tile<T, O, decltype(c), PT>(p, smem, at, x.spot.tn * C::BN);
+  by_rows<S>(x.spot, x.at, x.spot.tn * C::BN, p.n, [&](auto c, const Place& at, int n0) {
+    rows_tile<T, O, decltype(c), PT>(p, smem, at, n0);
   });
 }
 template <class T, class O, class S>

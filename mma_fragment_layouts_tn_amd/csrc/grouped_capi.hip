@@ -114,28 +114,30 @@ Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
 
 // Kernel for `places` rows of `groups` matrices of n x k.  The lengths are on
 // the device, so the rule goes by their mean.  Microseconds, bf16, weights from
-// memory (not the caches), half of the groups a quarter of the places and half
-// three quarters:
+// memory (not the caches), half of the groups half of the mean and half three
+// halves of it:
 //
 //   groups mean    n     k   FEW  128  256
-//        2   16  4096  4096   20   59   46   FEW goes to more CUs, as long as its
-//        2  128  2048  4096   30   60   50   small tiles do not read the weights
-//        8   16  2048  4096   37   61   50   and rows too often
-//        8   16  4096  4096   70   65   55
-//       64    4  1024  2048   52   51   45
-//        8   64  4096  4096    -   75   73   256 has more loads under way per
-//       64   64  1024  2048    -   67   59   workgroup
-//        8  256  4096  4096    -   94  108   128 leaves less over at the groups'
-//       32  256  1024  2048    -   56   59   ends, if it fills the chip twice
-//        8  512  4096  4096    -  172  128
-//       32  512  1024  2048    -   92   76
+//        2   16  4096  4096   19   54   26   FEW shares a contraction between
+//        8  100   256   256   5.3  6.6  6.5  waves, as long as its small tiles do
+//       32   16   256  1024   7.7   14  9.9  not read weights and rows too often
+//        8   48  1024  1024   16    14   10
+//       32   16  1024  1024   21    20   17
+//        8   48  1024   256   8.8  7.2  6.9  256 has more loads under way, and cuts
+//        8   48  1024  4096   44    59   28  what is left of a round
+//       32  400  1024  1024    -    46   38
+//        8   48  4096   256   24   8.4  9.5  128 has two workgroups per CU, which
+//       32  200  1024   256   59    10   14  counts where a tile is a few steps,
+//        8  200  4096  4096    -    86   96  and where a little over half of one
+//       32  200  1024  4096    -    95  111  round of 256's tiles cannot be cut
 int choose_algo(int64_t places, int64_t groups, int64_t n, int64_t k, bool few) {
   const int64_t mean = ceil_div(places, groups), held = places < groups ? places : groups,
-                tiles = held * ceil_div(n, 256);
-  if (few && tiles < kFill && mean * tiles <= (tiles <= 32 ? 2048 : 1024)) return kFew;
-  if (mean >= 512) return kTile256;
-  const bool fills = (places / 128 + held / 2) * ceil_div(n, 128) >= 2 * kFill;
-  return k < 1024 || (mean > 128 && fills) ? kTile128 : kTile256;
+                across = ceil_div(n, 256), tiles = held * across;
+  const bool narrow = tiles <= 16 && (k <= 512 || mean <= 64);
+  if (few && tiles <= 64 && mean * tiles <= (narrow ? 2048 : 768)) return kFew;
+  const int64_t round = (places / 256 + held / 2) * across;     // 256's tiles, about
+  if (mean > 128 && round > kFill / 2 && round <= kFill * 5 / 8) return kTile128;
+  return k < 512 && mean < 512 ? kTile128 : kTile256;
 }
 
 Choice choose(const mfl_grouped_t& a) {
