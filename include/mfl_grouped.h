@@ -24,9 +24,10 @@
  * Addressing (elements): A(r, k) = A[r lda + k], B(g, n, k) = B[g b_group +
  * n ldb + k], D(i, n) = D[i ldd + n].  n, k and every stride are multiples of
  * 8 and every matrix is 16-byte aligned (else MFL_E_MISALIGNED); strides reach
- * past a row (MFL_E_LEADING_DIM); n, k and the strides between rows are at
- * most 2^21, and where rows are gathered A (x) spans less than 2 GiB
- * (MFL_E_TOO_LARGE).  At most 4096 groups.
+ * past a row (MFL_E_LEADING_DIM); n, k and the rank are at least 8 (0 is
+ * MFL_E_UNSUPPORTED), they and the strides between rows at most 2^21, and
+ * where rows are gathered A (x) spans less than 2 GiB (MFL_E_TOO_LARGE).  At
+ * most 4096 groups.
  *
  * Values of one group's rows and of its matrix never reach another group's
  * results, whatever they are.

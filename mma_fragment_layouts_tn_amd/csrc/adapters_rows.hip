@@ -20,7 +20,8 @@ KernelRef by_tile(int algo) {
 
 KernelRef down_rows_kernel(bool bf16) {
   using C = DownTile;
-  return {bf16 ? (const void*)adapters_down_rows<__bf16> : (const void*)adapters_down_rows<_Float16>,
+  return {bf16 ? (const void*)adapters_down_rows<__bf16>
+               : (const void*)adapters_down_rows<_Float16>,
           kDownParts * C::T, C::BM, C::BN};
 }
 KernelRef adapters_kernel(bool bf16, bool f32, int algo) {

