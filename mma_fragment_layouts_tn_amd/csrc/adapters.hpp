@@ -157,21 +157,22 @@ __global__ void __launch_bounds__(kJoinThreads) adapters_join(const AdapterParam
 }
 
 // Small problems, one launch: a tile of 16 places of one group (or of none) by
-// 32 columns forms its own h beside the shared product, as RA atoms more of
+// 16 RN columns forms its own h beside the shared product, as RA atoms more of
 // the same contraction, and adds the low-rank term a result per thread.  h is
-// formed again for every 32 columns; what it saves is a launch, the workspace
-// and the wait between the two: 48 rows of 256, rank 16, to 256 columns 4.5 us
-// where two launches take 9.1.  What bounds it is the latency of one pass over
-// the contraction.  B's row is asked for ahead of the product.
-template <int RA>
+// formed again for every tile; what it saves is a launch, the workspace and the
+// wait between the two: 48 rows of 256, rank 16, to 256 columns 4.5 us where
+// two launches take 9.1, one row of 4096 to 4096 columns (RN = 1) 14 and 17.
+// What bounds it is the latency of one pass over the contraction.  B's row is
+// asked for ahead of the product.
+template <int RN>
 struct OneTile {
-  static constexpr int RN = 2, BM = 16, BN = 16 * RN, T = 64 * kFewWaves;
-  static_assert(BM * BN == T, "a result per thread");
+  static constexpr int BM = 16, BN = 16 * RN, T = 64 * kFewWaves;
+  static_assert(BM * BN <= T, "a result per thread");
 };
-template <class T, class O, int RA>
+template <class T, class O, int RN, int RA>
 __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_one(const AdapterParams p) {
-  using F = OneTile<RA>;
-  constexpr int RN = F::RN, NB = 2 * RA;
+  using F = OneTile<RN>;
+  constexpr int NB = 2 * RA;
   __shared__ floatx4 sums[kFewWaves * (RN + RA) * 64];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const GroupSpot spot = group_spot<1>(p.g, blockIdx.x, F::BM);
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_one(const AdapterP
   const int group = has ? at.group : 0;
   // the thread's result
   const int m = tid / F::BN, nn = tid % F::BN, n = n0 + nn;
-  const bool mine = m < at.count && n < p.g.n;
+  const bool mine = m < at.count && n < p.g.n;      // (at most 16 rows)
   const int row = mine ? row_at(p.g, at.first + m) : -1;
   const float scale = p.scale ? p.scale[group] : 1.0f;
   u32x4_t b[NB];

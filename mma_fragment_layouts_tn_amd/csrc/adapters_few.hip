@@ -26,19 +26,23 @@ template <class T>
 KernelRef first_by_size(int rm) {
   return rm == 4 ? first<T, 4>() : rm == 2 ? first<T, 2>() : first<T, 1>();
 }
-template <class T, class O>
+template <class T, class O, int RN>
 KernelRef one_by_rank(int ra) {
-  const void* f = ra == 4   ? (const void*)adapters_one<T, O, 4>
-                  : ra == 2 ? (const void*)adapters_one<T, O, 2>
-                            : (const void*)adapters_one<T, O, 1>;
-  using F = OneTile<1>;
+  const void* f = ra == 4   ? (const void*)adapters_one<T, O, RN, 4>
+                  : ra == 2 ? (const void*)adapters_one<T, O, RN, 2>
+                            : (const void*)adapters_one<T, O, RN, 1>;
+  using F = OneTile<RN>;
   return {f, F::T, F::BM, F::BN};
+}
+template <class T, class O>
+KernelRef one(int rn, int ra) {
+  return rn == 1 ? one_by_rank<T, O, 1>(ra) : one_by_rank<T, O, 2>(ra);
 }
 }  // namespace
 
-KernelRef adapters_one_kernel(bool bf16, bool f32, int ra) {
-  return f32 ? bf16 ? one_by_rank<__bf16, float>(ra) : one_by_rank<_Float16, float>(ra)
-         : bf16 ? one_by_rank<__bf16, __bf16>(ra) : one_by_rank<_Float16, _Float16>(ra);
+KernelRef adapters_one_kernel(bool bf16, bool f32, int rn, int ra) {
+  return f32 ? bf16 ? one<__bf16, float>(rn, ra) : one<_Float16, float>(rn, ra)
+         : bf16 ? one<__bf16, __bf16>(rn, ra) : one<_Float16, _Float16>(rn, ra);
 }
 KernelRef down_kernel(bool bf16, int rm, int rn) {
   return bf16 ? down_by_size<__bf16>(rm, rn) : down_by_size<_Float16>(rm, rn);

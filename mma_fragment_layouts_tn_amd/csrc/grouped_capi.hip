@@ -230,26 +230,33 @@ struct AdaptersPlan {
   int64_t join_blocks;
 };
 // Whether the problem is small enough for one launch, and its tiles.  Each of
-// its workgroups reads 16 rows of x, 32 of W and A's; a contraction longer than
-// that allows is better shared by workgroups, and beyond some 64 MB in all the
-// reading takes longer than a second launch.  Microseconds, bf16, rank 16,
-// weights from memory:
+// its workgroups reads 16 rows of x, 32 or 16 of W and A's; a contraction
+// longer than that allows is better shared by workgroups, and beyond some 64 MB
+// in all, or a workgroup per CU where they are long, the reading takes longer
+// than a second launch.  Microseconds, bf16, weights from memory:
 //
-//   rows  adapters    n     k   one  two launches
-//      1         1   64    64   3.7   5.5
-//     48         8  256   256   4.5   9.1
-//   1000         8  256   256   8.7  17.7
-//     48         8 1024  1024   7.7  10.8
-//     48        64 1024  1024    23    11    (214 MB)
-//      8         1 1024  4096    17    16    (a contraction of 4096)
-//     48         1 4096  4096    33    22
+//   rows  adapters  rank    n     k    32    16  two launches
+//      1         1    16   64    64   3.7         5.5
+//     48         8    16  256   256   4.5         9.1
+//   1000         8    16  256   256   8.7        17.7
+//     48         8    16 1024  1024   7.7        10.8
+//     48        64    16 1024  1024    23          11    (214 MB)
+//      1         1    16 4096  4096    18    14    17
+//     48         8    16  256  4096          13    15
+//     16         8    16 1024  4096          21    15    (512 workgroups)
+//      1         1    64 4096  4096    32    27    22
 bool one_launch(const mfl_adapters_t& a, Choice* c) {
   if (a.rank > 64) return false;
   const int ra = a.rank <= 16 ? 1 : a.rank <= 32 ? 2 : 4;
-  const KernelRef k = adapters_one_kernel(a.dtype == MFL_BF16, a.out == MFL_F32, ra);
-  *c = {kFew, k, tile_slots(a.places, a.groups, k.bm), ceil_div(a.n, k.bn)};
-  const int64_t rows = k.bm + k.bn + 16 * ra, tiles = c->blocks();
-  return rows * a.k <= 64 * 2048 && tiles <= 1024 && tiles * rows * a.k * 2 <= (64 << 20);
+  for (int rn = 2; rn; --rn) {
+    const KernelRef k = adapters_one_kernel(a.dtype == MFL_BF16, a.out == MFL_F32, rn, ra);
+    *c = {kFew, k, tile_slots(a.places, a.groups, k.bm), ceil_div(a.n, k.bn)};
+    const int64_t each = (k.bm + k.bn + 16 * ra) * a.k, tiles = c->blocks();
+    if (rn == 2 ? each <= 64 * 2048 && tiles <= 1024 && tiles * each <= (32 << 20)
+                : each <= 48 * 4096 && tiles <= kFill)
+      return true;
+  }
+  return false;
 }
 AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
   const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;

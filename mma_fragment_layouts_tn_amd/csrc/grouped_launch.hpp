@@ -78,7 +78,7 @@ KernelRef few_kernel(bool bf16, bool f32, int row_blocks, int column_blocks);
 KernelRef backward_kernel(bool bf16, bool f32, bool gathered);   // dA and dB
 KernelRef down_kernel(bool bf16, int row_blocks, int column_blocks);
 KernelRef down_rows_kernel(bool bf16);
-KernelRef adapters_one_kernel(bool bf16, bool f32, int rank_blocks);
+KernelRef adapters_one_kernel(bool bf16, bool f32, int column_blocks, int rank_blocks);
 KernelRef adapters_first_kernel(bool bf16, int row_blocks);
 KernelRef adapters_join_kernel(bool bf16, bool f32);
 KernelRef adapters_kernel(bool bf16, bool f32, int algo);

@@ -36,6 +36,17 @@ def test_one_launch_sizes(n, k, kind):
     c.check("f32", scale=False, algo="few")
 
 
+@pytest.mark.parametrize("m,adapters,rank,n,k", [(1, 1, 16, 520, 4096), (1, 9, 8, 4096, 4096),
+                                                 (37, 3, 16, 40, 4000), (16, 1, 32, 72, 2056),
+                                                 (3, 2, 24, 8, 2560), (150, 1, 16, 200, 2736)])
+@pytest.mark.parametrize("kind,out", [("f16", "f32"), ("bf16", "bf16")])
+def test_one_launch_long(m, adapters, rank, n, k, kind, out):
+    """Sixteen columns a workgroup."""
+    c = Adapted(kind, m, adapters, rank, n, k)
+    assert launches(c, out) == 1
+    c.check(out, algo="few")
+
+
 def test_one_launch_many_adapters():
     """More groups than are numbered without gaps; most without a row."""
     c = Adapted("f16", 200, 300, 8, 32, 64)
@@ -46,7 +57,7 @@ def test_one_launch_many_adapters():
 @pytest.mark.parametrize("m", [1, 16, 31, 64, 65, 190])
 @pytest.mark.parametrize("mode", ["mixed", "runs", "none", "one"])
 def test_two_launches_rows(m, mode):
-    c = Adapted("bf16", m, 5, 16, 136, 2312, mode=mode)
+    c = Adapted("bf16", m, 5, 16, 136, 4168, mode=mode)
     assert launches(c) == 2
     c.check(algo="few")
 
@@ -60,7 +71,7 @@ def test_two_launches_sizes(rank, n, k, kind, out):
     c.check(out, scale=rank != 64, algo="few")
 
 
-@pytest.mark.parametrize("k", [264, 2312])
+@pytest.mark.parametrize("k", [264, 4168])
 def test_are_apart(k):
     """An adapter of infinities and NaN changes no other request's row, by one
     launch and by two."""
@@ -74,7 +85,7 @@ def test_are_apart(k):
     assert bool((~D[c.ids == 3].isfinite()).all()) and bool(D[c.ids == 2].isnan().all())
 
 
-@pytest.mark.parametrize("k", [264, 2312])
+@pytest.mark.parametrize("k", [264, 4168])
 def test_rows_of_infinities(k):
     """A request's own infinities stay in its row."""
     c = Adapted("bf16", 40, 3, 16, 72, k, seed=3)
@@ -85,7 +96,7 @@ def test_rows_of_infinities(k):
     assert torch.equal(D[rest], clean[rest]) and bool((~D[7].isfinite()).all())
 
 
-@pytest.mark.parametrize("k", [72, 2312])
+@pytest.mark.parametrize("k", [72, 4168])
 def test_listed_in_part_and_out_of_range(k):
     c = Adapted("bf16", 90, 3, 8, 64, k, seed=4)
     rows = torch.arange(0, 90, 2, dtype=torch.int32)

@@ -239,7 +239,7 @@ def test_adapters_plans():
             for out in (BF16, F32):
                 for algo in (0, 1, 2, 3):
                     rc, al, n = adapters(places=places, x_rows=places, rank=rank, ldb=rank, out=out,
-                                         algo=algo, k=4096, ldx=4096, ldw=4096, lda=4096, n=512,
+                                         algo=algo, k=4608, ldx=4608, ldw=4608, lda=4608, n=512,
                                          ldd=512)
                     assert rc == 0 and al == (algo or al) and al in (1, 2, 3)
                     least = 4 * places + places * rank * (6 if al > 1 and out == F32 else 4)
@@ -248,7 +248,7 @@ def test_adapters_plans():
                         assert least <= n <= least + 32
                     else:
                         parts = (n - least) // part
-                        assert 1 <= parts <= 16 and n - least - parts * part <= 32
+                        assert 1 <= parts <= 18 and n - least - parts * part <= 32
     assert adapters(places=0, ptrs=dict(x=0, D=0))[0] == 0
     # small problems need none, unless their rank is large or tiles are asked for
     assert adapters()[1:] == (1, 0) and adapters(algo=1)[1:] == (1, 0)
