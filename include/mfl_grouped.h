@@ -153,7 +153,8 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
  *
  * rows holds each row of x and D at most once, NULL: places are rows; rows of
  * D that no place leads to stay as they were.  s_g h is held to fp32's
- * accuracy (in fp16, beyond 65504 it becomes infinite), sums are fp32, D is
+ * accuracy (with fp16 operands the TILEs hold it as sums of fp16 numbers: in
+ * steps of 2^-24 at the least, and infinite beyond 65504), sums are fp32, D is
  * rounded once.  The values of an adapter reach its own rows alone, whatever
  * they are.
  *

@@ -118,7 +118,7 @@ Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
 // halves of it:
 //
 //   groups mean    n     k   FEW  128  256
-//        2   16  4096  4096   19   54   26   FEW shares a contraction between
+//        2   16  4096  4096   19   49   26   FEW shares a contraction between
 //        8  100   256   256   5.3  6.6  6.5  waves, as long as its small tiles do
 //       32   16   256  1024   7.7   14  9.9  not read weights and rows too often
 //        8   48  1024  1024   16    14   10
