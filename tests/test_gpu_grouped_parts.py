@@ -1,7 +1,8 @@
 """Every tile that a launch's last round may be cut into: a round that is
 nearly full keeps its tiles of 256 columns whole, emptier ones are cut in two,
 four and eight, along rows and columns, and a tile of few rows is the smaller
-one.  Groups of each height against widths that give each number of parts."""
+one.  Groups of each height against widths that give each number of parts; more
+groups than the kernels count; more choices than a walk of a wave."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +88,21 @@ def test_alignment_of_parts_with_strides():
         mfl.gemm_grouped(c.cuda(c.A), c.cuda(c.B), c.offsets.cuda(), rows=c.cuda(c.rows),
                          D=D[:, :n], algo="tile256")
         assert bool((D[:, n:] == 3).all()) and torch.equal(D[:, :n], c.forward(algo="tile256"))
+
+
+@pytest.mark.parametrize("tokens,top,groups", [(300001, 8, 64), (60001, 8, 1000), (1100000, 1, 256),
+                                               (131073, 2, 4096)])
+def test_more_choices_than_a_chunk_each(tokens, top, groups):
+    """Chunks grow beyond one walk of a wave: against a stable sort."""
+    gen = torch.Generator().manual_seed(tokens)
+    ids = torch.randint(-1, groups + 1, (tokens, top), generator=gen)
+    rows, offsets, slots = mfl.group_rows(ids.cuda(), groups)
+    torch.cuda.synchronize()
+    key = torch.where((ids < 0) | (ids >= groups), groups, ids).flatten()
+    order = torch.sort(key, stable=True).indices
+    place = torch.empty_like(order)
+    place[order] = torch.arange(len(order))
+    counts = torch.bincount(key, minlength=groups + 1)
+    assert torch.equal(rows.cpu().long(), order // top)
+    assert int(offsets[0]) == 0 and torch.equal(offsets[1:].cpu().long(), counts[:-1].cumsum(0))
+    assert torch.equal(slots.cpu().long().flatten(), torch.where(key < groups, place, -1))
