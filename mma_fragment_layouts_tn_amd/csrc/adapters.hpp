@@ -426,8 +426,10 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   };
   store_rows<O, C, true>(acc, n0, g.n, w, lane, row_of);
   if (!__any(bad)) return;
-  // (each lane reads what it stored: a sum with an infinity or NaN does not
-  // depend on the rounding of its finite part)
+  // Each lane adds to the results of its sums, which lanes of this wave have
+  // stored (a sum with an infinity or NaN does not depend on the rounding of its
+  // finite part).
+  __threadfence_block();
 #pragma unroll 1
   for (int x = 0; x < C::RM * RN; ++x) {
     const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of<true>(lane, x % RN);
