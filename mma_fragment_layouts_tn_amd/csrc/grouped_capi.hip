@@ -258,37 +258,61 @@ bool one_launch(const mfl_adapters_t& a, Choice* c) {
   }
   return false;
 }
+// FEW: tiles of the shared product (*all) and of the down projection, two
+// launches.
+Choice few_down(const mfl_adapters_t& a, Choice* all) {
+  const bool bf16 = a.dtype == MFL_BF16;
+  const KernelRef k = adapters_first_kernel(bf16, a.places <= 16 ? 1 : a.places <= 32 ? 2 : 4);
+  *all = {kFew, k, ceil_div(a.places, k.bm), ceil_div(a.n, k.bn)};
+  const KernelRef d = down_kernel(bf16, 1, 1);
+  return {kFew, d, tile_slots(a.places, a.groups, d.bm), ceil_div(a.rank, d.bn)};
+}
+// The kernel: FEW as long as both find room in one round, or nearly, and the
+// down projection of the requests does where each has an adapter of its own.
+// Microseconds, bf16, weights from memory; tiles of both:
+//
+//   rows  adapters  rank    n     k          FEW  TILE
+//    192         1    16 4096  4096  192+14   46    45
+//    300         4    16 1024  1024   80+23   16    21
+//    500         4    32 1024  1024  128+72   21    21
+//   1000         4    16  256  4096   64+67   25    39
+//   2000         4    16  256  4096  128+130  39    39
+//   1000         4    64  256  1024   64+268  25    25
+//     64        64    64 1024  4096   16+272  50    67
+//    128        64    64 4096  4096  128+292  72    67
+//   1000         4    64   64  4096   16+268  50    42
+int adapters_algo(const mfl_adapters_t& a) {
+  Choice all;
+  const int64_t down = few_down(a, &all).blocks(), tiles = all.blocks(), sum = tiles + down;
+  const bool few = sum <= kFill * 3 / 4 ||
+                   (a.places <= 192 && tiles <= kFill / 4 && sum <= kFill * 11 / 8);
+  return few ? kFew : choose_algo(a.places, 1, a.n, a.k, false);
+}
 AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
   const bool bf16 = a.dtype == MFL_BF16, f32 = a.out == MFL_F32;
   AdaptersPlan r{};
-  const int64_t mean = ceil_div(a.places, a.groups);
-  const int algo = a.algo ? a.algo : a.places <= 192 ? kFew
-                   : choose_algo(a.places, 1, a.n, a.k, false);
-  if ((algo == kFew || !a.algo) && one_launch(a, &r.all)) {
+  if (a.algo <= kFew && one_launch(a, &r.all)) {
     r.one = true;
     return r;
   }
-  r.all.algo = algo;
-  r.down.algo = kFew;
+  const int algo = a.algo ? a.algo : adapters_algo(a);
   if (algo == kFew) {
-    r.all.kernel = adapters_first_kernel(bf16, a.places <= 16 ? 1 : a.places <= 32 ? 2 : 4);
-    r.down.kernel = down_kernel(bf16, 1, 1);
+    r.down = few_down(a, &r.all);
   } else {
-    r.all.kernel = adapters_kernel(bf16, f32, algo);
-    r.down.kernel = mean > 24 ? down_rows_kernel(bf16)
-                              : down_kernel(bf16, mean <= 10 ? 1 : 2, a.rank <= 16 ? 1 : 2);
+    const int64_t mean = ceil_div(a.places, a.groups);
+    const KernelRef k = adapters_kernel(bf16, f32, algo),
+                    d = mean > 24 ? down_rows_kernel(bf16)
+                                  : down_kernel(bf16, mean <= 10 ? 1 : 2, a.rank <= 16 ? 1 : 2);
+    r.all = {algo, k, ceil_div(a.places, k.bm), ceil_div(a.n, k.bn)};
+    r.down = {kFew, d, tile_slots(a.places, a.groups, d.bm), ceil_div(a.rank, d.bn)};
     r.pieces = f32 ? 3 : 2;
   }
-  r.all.slots = ceil_div(a.places, r.all.kernel.bm);
-  r.all.tiles_n = ceil_div(a.n, r.all.kernel.bn);
-  r.down.slots = tile_slots(a.places, a.groups, r.down.kernel.bm);
-  r.down.tiles_n = ceil_div(a.rank, r.down.kernel.bn);
   r.h_at = ceil_div(4 * a.places, 16) * 16;
   r.part_at = r.h_at + ceil_div(a.places * a.rank * (r.pieces ? 2 * r.pieces : 4), 16) * 16;
   if (algo == kFew) {
     // one round of the chip (a workgroup per CU) with the down projection's,
     // 256 of the contraction each at least
-    const int64_t tiles = r.all.slots * r.all.tiles_n, most = ceil_div(a.k, 256),
+    const int64_t tiles = r.all.blocks(), most = ceil_div(a.k, 256),
                   free = kFill - r.down.blocks();
     r.splits = tiles > 0 && free > tiles ? free / tiles : 1;
     if (r.splits > most) r.splits = most;
