@@ -61,7 +61,7 @@ extern "C" {
  *   offsets[g] (groups + 1)  the first place of group g
  *   slots[c]   (count)       the place of choice c, -1 for no group
  * The workspace is 4 (groups + 1) bytes for every 4096 choices (1024 with more
- * than 256 groups), at most 256 times that; none up to as many. */
+ * than 256 groups), at most 256 times that; none up to 8192 (1024). */
 typedef struct {
   int32_t ids_type;
   int64_t count, top, groups;

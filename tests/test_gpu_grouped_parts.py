@@ -90,7 +90,8 @@ def test_alignment_of_parts_with_strides():
         assert bool((D[:, n:] == 3).all()) and torch.equal(D[:, :n], c.forward(algo="tile256"))
 
 
-@pytest.mark.parametrize("tokens,top,groups", [(300001, 8, 64), (60001, 8, 1000), (1100000, 1, 256),
+@pytest.mark.parametrize("tokens,top,groups", [(4093, 2, 64), (8192, 1, 256), (8193, 1, 3),
+                                               (300001, 8, 64), (60001, 8, 1000), (1100000, 1, 256),
                                                (131073, 2, 4096)])
 def test_more_choices_than_a_chunk_each(tokens, top, groups):
     """Chunks grow beyond one walk of a wave: against a stable sort."""

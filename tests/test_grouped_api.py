@@ -155,10 +155,11 @@ def test_group_rows_refuses():
 
 
 def test_group_rows_workspace_is_as_documented():
-    """None up to a chunk, 4 (groups + 1) bytes per chunk, 256 chunks at most."""
-    for groups, chunk in ((8, 4096), (256, 4096), (257, 1024), (4096, 1024)):
-        assert sort(count=chunk, top=1, groups=groups)[1] == 0
-        assert sort(count=chunk + 1, top=1, groups=groups)[1] == 2 * 4 * (groups + 1)
+    """None up to one workgroup's choices, 4 (groups + 1) bytes per chunk begun,
+    256 chunks at most."""
+    for groups, alone, chunks in ((8, 8192, 3), (256, 8192, 3), (257, 1024, 2), (4096, 1024, 2)):
+        assert sort(count=alone, top=1, groups=groups)[1] == 0
+        assert sort(count=alone + 1, top=1, groups=groups)[1] == chunks * 4 * (groups + 1)
         for count in (1 << 20, (1 << 20) + 1, 1 << 24, (1 << 31) - (1 << 16) - 1):
             assert 0 < sort(count=count, top=1, groups=groups)[1] <= 256 * 4 * (groups + 1)
 
