@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_row
     floatx4 h = acc[0][j];
 #pragma unroll
     for (int v = 1; v < kDownParts; ++v) h += sums[(((v - 1) * C::W + w) * C::RN + j) * 64 + lane];
-    const int n = n0 + column_of<true>(lane, j);
+    const int n = n0 + column_of(lane, j);
     if (n < p.rank) keep<T>(p, x.at.first + m, x.at.group, n, h);
   }
 }
@@ -432,7 +432,7 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   __threadfence_block();
 #pragma unroll 1
   for (int x = 0; x < C::RM * RN; ++x) {
-    const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of<true>(lane, x % RN);
+    const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of(lane, x % RN);
     O* row = row_of(m);
     if (!row || n >= g.n) continue;
     floatx4 y = rest<T>(p, first + m, n, NPC);

@@ -14,8 +14,8 @@ KernelRef down() {
 }
 template <class T>
 KernelRef down_by_size(int rm, int rn) {
-  if (rn == 1) return rm == 4 ? down<T, 4, 1>() : rm == 2 ? down<T, 2, 1>() : down<T, 1, 1>();
-  return rm == 4 ? down<T, 4, 2>() : rm == 2 ? down<T, 2, 2>() : down<T, 1, 2>();
+  if (rn == 1) return rm == 2 ? down<T, 2, 1>() : down<T, 1, 1>();
+  return rm == 2 ? down<T, 2, 2>() : down<T, 1, 2>();
 }
 template <class T, int RM>
 KernelRef first() {

@@ -553,11 +553,9 @@ struct Out {
   }
 };
 
-// Columns of a lane's accumulators: atom j's four from column_of(j) on.
-template <bool PERM>
-__device__ __forceinline__ int column_of(int lane, int j) {
-  return PERM ? 16 * (lane >> 4) + 4 * j : 16 * j + 4 * (lane >> 4);
-}
+// Columns of a lane's accumulators (P's order in LDS as perm64): atom j's four
+// from column_of(lane, j) on.
+__device__ __forceinline__ int column_of(int lane, int j) { return 16 * (lane >> 4) + 4 * j; }
 
 // Exchanges between two lanes of which one bit differs: afterwards a lane with
 // the bit clear has both lanes' a, one with the bit set both lanes' b, in the
