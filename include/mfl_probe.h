@@ -48,6 +48,12 @@ int mfl_probe_lds_tr16(const int32_t* lane_offsets, const uint16_t* lds_in, uint
  * -5 on a launch error. */
 int mfl_probe_xcc(int32_t nblocks, int32_t* out, void* stream);
 
+/* One wave, lane l holding own[l] (device, 64 numbers), writes the bits of the
+ * lanes that begin a run of equal numbers to out[0] (lanes 0 .. 31) and out[1],
+ * found as the adapters' kernels find the runs of rows of one adapter.  Returns
+ * 0, -4 for a NULL pointer, -5 on a launch error. */
+int mfl_probe_run_starts(const int32_t* own, uint32_t* out, void* stream);
+
 /* Register dump of an LDS kernel (test-only): the kernel of configuration
  * `algo` (mfl_algo value, 2..10) with fetch policies fetch_a /
  * fetch_b (0 direct-to-LDS, 1 registers, 2 M-contiguous A transposed in

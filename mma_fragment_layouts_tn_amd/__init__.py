@@ -137,6 +137,8 @@ def _load() -> ctypes.CDLL:
     lib.mfl_probe_lds_tr16.restype = ctypes.c_int
     lib.mfl_probe_xcc.argtypes = [i32, vp, vp]
     lib.mfl_probe_xcc.restype = ctypes.c_int
+    lib.mfl_probe_run_starts.argtypes = [vp] * 3
+    lib.mfl_probe_run_starts.restype = ctypes.c_int
     lib.mfl_probe_gemm_poisoned.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
                                             GemmDtypes, vp]
     lib.mfl_probe_gemm_poisoned.restype = ctypes.c_int
@@ -544,6 +546,21 @@ def probe_xcc(nblocks: int) -> torch.Tensor:
     rc = _lib.mfl_probe_xcc(nblocks, out.data_ptr(), torch.cuda.current_stream().cuda_stream)
     _check(rc)
     return out
+
+
+def probe_run_starts(own: torch.Tensor) -> int:
+    """Bit l is set where number l of 64 (int32, on the GPU) begins a run of
+    equal ones."""
+    if own.dtype != torch.int32 or own.shape != (64,) or not own.is_cuda or \
+            not own.is_contiguous():
+        raise ValueError("own must be 64 contiguous int32 on the device")
+    out = torch.empty(2, dtype=torch.int32, device=own.device)
+    with torch.cuda.device(own.device):
+        rc = _lib.mfl_probe_run_starts(own.data_ptr(), out.data_ptr(),
+                                       torch.cuda.current_stream().cuda_stream)
+    _check(rc)
+    low, high = out.tolist()
+    return (low & 0xffffffff) | (high & 0xffffffff) << 32
 
 
 # ------------------------------------------------------- microbenchmarks

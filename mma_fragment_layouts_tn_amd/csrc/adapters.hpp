@@ -89,6 +89,13 @@ __device__ __forceinline__ int owner_of(const AdapterParams& p, int place) {
   const int g = place < p.g.offsets[p.g.groups] ? p.owner[place] : -1;
   return (unsigned)g < (unsigned)p.g.groups ? g : -1;
 }
+// Lanes whose number differs from the lane's before them; the first is one.
+// (The exchange ahead of the condition: behind `lane == 0 ||` lane 0 would be
+// off, and what lane 1 reads from it undefined.)
+__device__ __forceinline__ unsigned long long run_starts(int own, int lane) {
+  const int before = __shfl_up(own, 1);
+  return __ballot(lane == 0 || own != before);
+}
 // row of x and D at a place, -1 where it is outside
 __device__ __forceinline__ int row_at(const GroupedParams& p, int place) {
   const int r = p.rows ? p.rows[place] : place;
@@ -403,7 +410,7 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
       } while (s.group < 0);
       return s;
     };
-    Step s = advance(Step{0, 0, -1, 0, __ballot(lane == 0 || own[h] != __shfl_up(own[h], 1))});
+    Step s = advance(Step{0, 0, -1, 0, run_starts(own[h], lane)});
     if constexpr (NPC == 2) {
       Operands x = load(s);
       while (s.group >= 0) {

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "../../include/mfl_probe.h"
+#include "adapters.hpp"
 
 namespace {
 
@@ -116,5 +117,18 @@ __global__ void __launch_bounds__(64) probe_xcc(int32_t* out) {
 extern "C" int mfl_probe_xcc(int32_t nblocks, int32_t* out, void* stream) {
   if (nblocks <= 0 || nblocks > 65536 || !out) return -4;
   hipLaunchKernelGGL(probe_xcc, dim3(nblocks), dim3(64), 0, (hipStream_t)stream, out);
+  return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+// The run starts among a wave's 64 numbers, as the adapters' kernels find them.
+__global__ void __launch_bounds__(64) probe_run_starts(const int32_t* own, uint32_t* out) {
+  const int lane = threadIdx.x;
+  const unsigned long long m = mfl::grp::run_starts(own[lane], lane);
+  if (lane < 2) out[lane] = (uint32_t)(m >> 32 * lane);
+}
+
+extern "C" int mfl_probe_run_starts(const int32_t* own, uint32_t* out, void* stream) {
+  if (!own || !out) return -4;
+  hipLaunchKernelGGL(probe_run_starts, dim3(1), dim3(64), 0, (hipStream_t)stream, own, out);
   return hipGetLastError() == hipSuccess ? 0 : -5;
 }
