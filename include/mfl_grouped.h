@@ -152,16 +152,16 @@ int combine_rows_backward(const mfl_combine_t* a, int64_t lddx, const void* dout
  * also MFL_F32.  rank is a multiple of 8.
  *
  * rows holds each row of x and D at most once, NULL: places are rows; rows of
- * D that no place leads to stay as they were.  s_g h is held to fp32's
- * accuracy (with fp16 operands the TILEs hold it as sums of fp16 numbers: in
- * steps of 2^-24 at the least, and infinite beyond 65504), sums are fp32, D is
- * rounded once.  The values of an adapter reach its own rows alone, whatever
- * they are.
+ * D that no place leads to stay as they were.  s_g h is held in fp32 (as a
+ * matrix operand in three numbers of the operands' type that add up to it, with
+ * fp16 to 2^-38 of the largest beside it), sums are fp32, D is rounded once.  The
+ * values of an adapter reach its own rows alone, whatever they are.
  *
  * Kernels as above: FEW adds the low-rank terms row by row, the TILEs by runs
  * of one group.  Small problems of a rank up to 64 are one launch by FEW and need
- * no workspace (0 bytes, NULL will do).  For others: 4 bytes per place, places x rank numbers of 4
- * bytes (6 for TILE with an fp32 D), up to 32 for alignment, and with FEW
+ * no workspace (0 bytes, NULL will do).  For others: 4 bytes per place, 4 bytes
+ * for each of places x rank numbers (6 are asked for by TILE with an fp32 D, which
+ * leaves 2 of them unused), up to 32 for alignment, and with FEW
  * places x n numbers of 4 bytes for each of its parts of k, which are at most
  * one for 256 of k and about 256 / (tiles of 64 columns). */
 typedef struct {

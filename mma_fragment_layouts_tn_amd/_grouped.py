@@ -460,9 +460,8 @@ def gemm_adapters(x: torch.Tensor, W: torch.Tensor, A: torch.Tensor, B: torch.Te
     gives them; without it places are rows.  scale: (adapters,) float32, 1
     without it.  D (M, N) is of x's type, or float32 with out_dtype; it is
     allocated when not given, and rows that no place leads to are not written.
-    An adapter's values reach its own rows alone.  x @ A[g].T, scaled, is kept
-    to float32's accuracy; for many rows of float16 it is infinite beyond 65504.
-    No autograd graph is recorded.  algo chooses the kernel."""
+    An adapter's values reach its own rows alone.  x @ A[g].T, scaled, is held
+    in float32.  No autograd graph is recorded.  algo chooses the kernel."""
     m, n = x.shape[0], W.shape[0]
     if D is not None:
         if D.shape != (m, n):

@@ -11,9 +11,8 @@
 // the rows of its own places alone, so infinities in one adapter stay with its
 // requests.
 //
-// s_g h is kept to fp32's accuracy: as fp32 values where the second kernel
-// multiplies them out itself (few rows), and as two 16-bit numbers (three
-// with fp32 results) that add up to it where they are a matrix operand.
+// s_g h is held in fp32.  Where it is a matrix operand (many rows) it is taken
+// apart there, into three numbers of the operands' type that add up to it.
 #pragma once
 
 #include "grouped.hpp"
@@ -29,35 +28,77 @@ __device__ __forceinline__ bool not_finite(unsigned u) {
 }
 __device__ __forceinline__ bool not_finite(float x) { return !(__builtin_fabsf(x) < INFINITY); }
 
-// 16-bit numbers that stand for an fp32 value.  Each leaves half a step, 2^-8
-// (bf16) or 2^-11 (fp16) of what it stands for: two 2^-16 or 2^-22, far below
-// a 16-bit result's own rounding, three 2^-24, an fp32 result's.
-template <class O>
-constexpr int pieces_of() {
-  return sizeof(O) == 4 ? 3 : 2;
+// An fp32 number as a sum of kPieces numbers of T, cut off, not rounded: 24
+// bits are three times bf16's 8, or twice fp16's 11 and two more.  bf16 has fp32's
+// range.  fp16's ends at 65504 and, downwards, in steps of 2^-24: numbers that
+// are taken apart together are scaled by a power of two (scale_of) that brings
+// the largest of them between 2^14 and 2^15, and those far below it are off by
+// 2^-38 of it at the most.  take(): the next number of each of eight.
+constexpr int kPieces = 3;
+template <class T>
+struct Pieces;
+template <>
+struct Pieces<__bf16> {
+  static constexpr bool kScaled = false;
+  static __device__ __forceinline__ Vec8<__bf16> take(float (&left)[8]) {
+    u32x4_t x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const unsigned a = __float_as_uint(left[2 * q]), b = __float_as_uint(left[2 * q + 1]);
+      x[q] = __builtin_amdgcn_perm(b, a, 0x07060302);
+      left[2 * q] -= __uint_as_float(a & 0xffff0000u);
+      left[2 * q + 1] -= __uint_as_float(b & 0xffff0000u);
+    }
+    return __builtin_bit_cast(Vec8<__bf16>, x);
+  }
+};
+template <>
+struct Pieces<_Float16> {
+  static constexpr bool kScaled = true;
+  // Exponent of the factor's inverse: over what the lanes of a row hold, l, l ^
+  // 16, l ^ 32 and l ^ 48.
+  static __device__ __forceinline__ int scale_of(const float (&x)[8]) {
+    float top = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = __builtin_fabsf(x[e]);
+      top = fmaxf(top, a < INFINITY ? a : 0.0f);
+    }
+    const att::Halves q = att::quarters(top);
+    top = att::both_max(fmaxf(q.lower, q.upper));
+    return (int)(__float_as_uint(top) >> 23) - 126 - 15;
+  }
+  static __device__ __forceinline__ Vec8<_Float16> take(float (&left)[8]) {
+    Vec8<_Float16> x;
+#pragma unroll
+    for (int q = 0; q < 8; q += 2) {
+      const auto y = __builtin_amdgcn_cvt_pkrtz(left[q], left[q + 1]);
+      x[q] = (_Float16)y[0];
+      x[q + 1] = (_Float16)y[1];
+      left[q] = __builtin_fmaf((float)x[q], -1.0f, left[q]);
+      left[q + 1] = __builtin_fmaf((float)x[q + 1], -1.0f, left[q + 1]);
+    }
+    return x;
+  }
+};
+
+// Mma's instruction with the sums in ordinary registers: the compiler keeps the
+// results of its own all in the one kind or all in the other.  settle() is what
+// follows the last.
+template <class T>
+__device__ __forceinline__ void mma_low(const Vec8<T>& p, const Vec8<T>& q, floatx4& c) {
+  if constexpr (std::is_same<T, __bf16>::value)
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(p), "v"(q));
+  else
+    asm volatile("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(p), "v"(q));
 }
 
 // Four values of s_g h of a place, columns n .. n + 3, and the place's group.
-template <class T>
 __device__ __forceinline__ void keep(const AdapterParams& p, int place, int group, int n,
                                      floatx4 h) {
   h *= p.scale ? p.scale[group] : 1.0f;
   if (n == 0) p.owner[place] = group;
-  if (p.h) {
-    *(floatx4*)(p.h + (int64_t)place * p.rank + n) = h;
-    return;
-  }
-  typedef T vec4 __attribute__((ext_vector_type(4)));
-  for (int c = 0; c < p.pieces; ++c) {
-    vec4 y;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      y[v] = (T)h[v];
-      const float z = (float)y[v];
-      h[v] = not_finite(z) ? 0.0f : h[v] - z;
-    }
-    *(vec4*)((T*)p.hp + ((int64_t)place * p.pieces + c) * p.rank + n) = y;
-  }
+  *(floatx4*)(p.h + (int64_t)place * p.rank + n) = h;
 }
 
 // h of a tile of one group's places, few rows
@@ -75,7 +116,7 @@ __device__ __forceinline__ void down_few(const AdapterParams& p, floatx4* sums, 
   for (int x = tid; x < RM * RN * 64; x += F::T) {
     const int l = x & 63, j = (x >> 6) % RN, i = (x >> 6) / RN;
     const int m = 16 * i + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
-    if (m < at.count && n < p.rank) keep<T>(p, at.first + m, at.group, n, sums[x]);
+    if (m < at.count && n < p.rank) keep(p, at.first + m, at.group, n, sums[x]);
   }
 }
 template <class T, int RM, int RN>
@@ -246,20 +287,17 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_one(const AdapterP
 // what adapters_rows leaves out: the pairs of B's numbers of which one is not
 // finite, for the place's columns n .. n + 3
 template <class T>
-__device__ __forceinline__ floatx4 rest(const AdapterParams& p, int place, int n, int pieces) {
+__device__ __forceinline__ floatx4 rest(const AdapterParams& p, int place, int n) {
   floatx4 low{0.0f, 0.0f, 0.0f, 0.0f};
   const int g = owner_of(p, place);
   if (g < 0) return low;
   const T* b = (const T*)p.up + g * p.up_group + (int64_t)n * p.ldup;
-  const T* h = (const T*)p.hp + (int64_t)place * pieces * p.rank;
+  const float* h = p.h + (int64_t)place * p.rank;
   for (int c = 0; c < p.rank; c += 2) {
-    float s[2] = {};
-    for (int x = pieces; x--;)
-      for (int e = 0; e < 2; ++e) s[e] += (float)h[x * p.rank + c + e];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const float b0 = (float)b[v * p.ldup + c], b1 = (float)b[v * p.ldup + c + 1];
-      if (not_finite(b0) || not_finite(b1)) low[v] += s[0] * b0 + s[1] * b1;
+      if (not_finite(b0) || not_finite(b1)) low[v] += h[c] * b0 + h[c + 1] * b1;
     }
   }
   return low;
@@ -307,20 +345,20 @@ __global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_row
 #pragma unroll
     for (int v = 1; v < kDownParts; ++v) h += sums[(((v - 1) * C::W + w) * C::RN + j) * 64 + lane];
     const int n = n0 + column_of(lane, j);
-    if (n < p.rank) keep<T>(p, x.at.first + m, x.at.group, n, h);
+    if (n < p.rank) keep(p, x.at.first + m, x.at.group, n, h);
   }
 }
 
 // Tiles through LDS.  The low-rank term of each run of places of one group is
-// a few matrix instructions more into the same sums, on fragments straight
-// from memory (a few KB that every workgroup of a row of tiles reads): rows
-// of other groups multiply B by zeros.  What is not finite in B is left out
-// there, so that it cannot reach them, and added to its own rows at the end.
+// a few matrix instructions more, on fragments straight from memory (a few KB
+// that every workgroup of a row of tiles reads): rows of other groups multiply B
+// by zeros, and 16 rows without one of the run are passed over.  bf16's add to
+// the tile's own sums; fp16's are scaled.  What is not finite in B is left out
+// there, so that it cannot reach other rows, and added to its own at the end.
 template <class T, class O, class C>
 __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem, int first,
                                               int count, int n0) {
-  constexpr int NPC = pieces_of<O>(), RN = C::RN, WROWS = 16 * C::RM, H = (C::RM + 3) / 4,
-                HM = C::RM < 4 ? C::RM : 4;
+  constexpr int RN = C::RN, WROWS = 16 * C::RM, H = (C::RM + 3) / 4, HM = C::RM < 4 ? C::RM : 4;
   static_assert(H * HM == C::RM, "runs are found 64 rows at a time");
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const GroupedParams& g = p.g;
@@ -337,13 +375,20 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   floatx4 acc[C::RM][RN];
   product<T, C, false, false>((lds_c)smem, (g.k + 63) / 64, src, acc, w, lane);
 
+  // s_g h is an operand in pieces.  Where they are scaled, per row and 32 columns
+  // of the rank, those columns' sums are registers of their own, scaled back when
+  // they are added.
+  constexpr bool SCALED = Pieces<T>::kScaled;
   const int r = lane & 15, c8 = 8 * (lane >> 4);
   bool bad = false;       // something in B that is not finite
-  tied<C>(acc);
-  // A run's operands for 32 columns of the rank: those of the next are on
-  // their way while one's are multiplied (where the registers hold two).
-  struct Operands {
-    u32x4_t b[RN], h[NPC][HM];
+  if (!SCALED) tied<C>(acc);
+  // For 32 columns of the rank of a run: B, and s_g h of 16 rows at a time.  The
+  // next ones are on their way while some are multiplied.
+  struct Columns {
+    u32x4_t x[RN];
+  };
+  struct Rows {
+    u32x4_t x[2];
   };
   struct Step {
     int a, b, group, c;   // places a .. b - 1 of 64, columns c ..; group < 0: none
@@ -352,48 +397,78 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     const int at = m0 + 64 * h;
-    const __amdgpu_buffer_rsrc_t rh =
-        buffer((const T*)p.hp + (int64_t)at * NPC * p.rank, kWhole);
-    auto load = [&](const Step& s) {
-      Operands x;
+    const __amdgpu_buffer_rsrc_t rh = buffer(p.h + (int64_t)at * p.rank, kWhole);
+    auto load_b = [&](const Step& s) {
+      Columns y;
       const __amdgpu_buffer_rsrc_t rb =
           buffer((const T*)p.up + max(s.group, 0) * p.up_group + (int64_t)nw * p.ldup, kWhole);
       const int c = s.group < 0 ? p.rank : s.c + c8;
 #pragma unroll
       for (int j = 0; j < RN; ++j) {
         const int n = 16 * (r >> 2) + 4 * j + (r & 3);
-        x.b[j] = __builtin_amdgcn_raw_buffer_load_b128(
+        y.x[j] = __builtin_amdgcn_raw_buffer_load_b128(
             rb, c < p.rank && nw + n < g.n ? 2u * (n * p.ldup + c) : kOutside, 0, 0);
       }
-#pragma unroll
-      for (int v = 0; v < NPC; ++v)
-#pragma unroll
-        for (int i = 0; i < HM; ++i) {
-          const int m = 16 * i + r;
-          x.h[v][i] = __builtin_amdgcn_raw_buffer_load_b128(
-              rh,
-              c < p.rank && m >= s.a && m < s.b ? 2u * ((m * NPC + v) * p.rank + c) : kOutside, 0,
-              0);
-        }
-      return x;
+      return y;
     };
-    auto use = [&](Operands& x) {
+    auto load_h = [&](const Step& s, int i) {
+      Rows y;
+      const int c = s.group < 0 ? p.rank : s.c + c8, m = 16 * i + r;
+      const unsigned x = c < p.rank && m >= s.a && m < s.b ? 4u * (m * p.rank + c) : kOutside;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        y.x[e] = __builtin_amdgcn_raw_buffer_load_b128(rh, x, 16 * e, 0);
+      return y;
+    };
+    auto finite = [&](Columns& y) {
 #pragma unroll
       for (int j = 0; j < RN; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const unsigned u = x.b[j][e];
+          const unsigned u = y.x[j][e];
           const bool z = not_finite<T>(u);
-          x.b[j][e] = z ? 0u : u;
+          y.x[j][e] = z ? 0u : u;
           bad |= z;
         }
+    };
+    auto use = [&](const Columns& b, const Rows& y, int i) {
+      float left[8];
 #pragma unroll
-      for (int v = 0; v < NPC; ++v)
+      for (int e = 0; e < 8; ++e) left[e] = __uint_as_float(y.x[e / 4][e % 4]);
+      floatx4 low[RN];
+      int ex = 0;
+      if constexpr (SCALED) {
+        ex = Pieces<T>::scale_of(left);
 #pragma unroll
-        for (int i = 0; i < HM; ++i)
+        for (int e = 0; e < 8; ++e) left[e] = __builtin_amdgcn_ldexpf(left[e], -ex);
 #pragma unroll
-          for (int j = 0; j < RN; ++j)
-            Mma<T>::run(as16(x.b[j], T()), as16(x.h[v][i], T()), acc[4 * h + i][j]);
+        for (int j = 0; j < RN; ++j) low[j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+#pragma unroll
+      for (int v = 0; v < kPieces; ++v) {
+        const Vec8<T> piece = Pieces<T>::take(left);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)      // (of an infinity nothing is left)
+          if (v == 0) left[e] = not_finite(left[e]) ? 0.0f : left[e];
+#pragma unroll
+        for (int j = 0; j < RN; ++j) {
+          if constexpr (SCALED)
+            mma_low<T>(as16(b.x[j], T()), piece, low[j]);
+          else
+            Mma<T>::run(as16(b.x[j], T()), piece, acc[4 * h + i][j]);
+        }
+      }
+      if constexpr (SCALED) {
+        att::settle();
+#pragma unroll
+        for (int j = 0; j < RN; ++j) {
+          asm volatile("" : "+v"(low[j]), "+a"(acc[4 * h + i][j]));
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[4 * h + i][j][v] += __builtin_amdgcn_ldexpf(low[j][v], ex);
+          asm volatile("" : "+a"(acc[4 * h + i][j]));     // (else all leave their AGPRs at once)
+        }
+      }
     };
     auto advance = [&](Step s) {
       if (s.group >= 0 && (s.c += 32) < p.rank) return s;
@@ -411,22 +486,23 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
       return s;
     };
     Step s = advance(Step{0, 0, -1, 0, run_starts(own[h], lane)});
-    if constexpr (NPC == 2) {
-      Operands x = load(s);
-      while (s.group >= 0) {
-        s = advance(s);
-        const Operands y = load(s);    // (of no step: nothing is read)
-        use(x);
-        x = y;
+    Columns b = load_b(s);
+    Rows y = load_h(s, 0);
+    while (s.group >= 0) {
+      const Step to = advance(s);
+      const Columns next = load_b(to);      // (of no step: nothing is read)
+      finite(b);
+#pragma unroll
+      for (int i = 0; i < HM; ++i) {
+        const Rows then = i + 1 < HM ? load_h(s, i + 1) : load_h(to, 0);
+        if (16 * i < s.b && 16 * i + 16 > s.a) use(b, y, i);
+        y = then;
       }
-    } else {
-      for (; s.group >= 0; s = advance(s)) {
-        Operands x = load(s);
-        use(x);
-      }
+      b = next;
+      s = to;
     }
   }
-  settled<C>(acc);
+  if (!SCALED) settled<C>(acc);
   auto row_of = [&](int m) {
     const int row = m < count ? row_at(g, first + m) : -1;
     return row < 0 ? nullptr : (O*)g.d + (int64_t)row * g.ldd;
@@ -442,7 +518,7 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
     const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of(lane, x % RN);
     O* row = row_of(m);
     if (!row || n >= g.n) continue;
-    floatx4 y = rest<T>(p, first + m, n, NPC);
+    floatx4 y = rest<T>(p, first + m, n);
 #pragma unroll
     for (int v = 0; v < 4; ++v) y[v] += (float)row[n + v];
     Out<O>::store4(row + n, y);

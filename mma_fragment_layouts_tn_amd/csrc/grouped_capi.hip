@@ -224,7 +224,6 @@ int check_adapters(const mfl_adapters_t& a, const void* x, const void* W, const 
 struct AdaptersPlan {
   Choice down, all;
   bool one;                    // one launch, no workspace
-  int pieces;                  // 0: h in fp32
   int64_t splits, part_k;      // FEW: parts of the contraction
   int64_t h_at, part_at, bytes;
   int64_t join_blocks;
@@ -305,10 +304,10 @@ AdaptersPlan plan_adapters(const mfl_adapters_t& a) {
                                   : down_kernel(bf16, mean <= 10 ? 1 : 2, a.rank <= 16 ? 1 : 2);
     r.all = {algo, k, ceil_div(a.places, k.bm), ceil_div(a.n, k.bn)};
     r.down = {kFew, d, tile_slots(a.places, a.groups, d.bm), ceil_div(a.rank, d.bn)};
-    r.pieces = f32 ? 3 : 2;
   }
   r.h_at = ceil_div(4 * a.places, 16) * 16;
-  r.part_at = r.h_at + ceil_div(a.places * a.rank * (r.pieces ? 2 * r.pieces : 4), 16) * 16;
+  // (h takes 4 bytes each; a TILE with an fp32 D is documented to take 6)
+  r.part_at = r.h_at + ceil_div(a.places * a.rank * (algo != kFew && f32 ? 6 : 4), 16) * 16;
   if (algo == kFew) {
     // one round of the chip (a workgroup per CU) with the down projection's,
     // 256 of the contraction each at least
@@ -583,12 +582,8 @@ int gemm_tn_adapters(const mfl_adapters_t* a, const void* x, const void* W, cons
   if (r.one) return launch(r.all.kernel, r.all.blocks(), &p, stream);
   place(p.down, r.down);
   p.owner = (int*)workspace;
-  if (r.pieces)
-    p.hp = (char*)workspace + r.h_at;
-  else
-    p.h = (float*)((char*)workspace + r.h_at);
+  p.h = (float*)((char*)workspace + r.h_at);
   p.part = (float*)((char*)workspace + r.part_at);
-  p.pieces = r.pieces;
   if (r.all.algo == kFew) {
     p.down_blocks = (int)r.down.blocks();
     p.splits = (int)r.splits;

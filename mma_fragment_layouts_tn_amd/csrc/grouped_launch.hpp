@@ -30,11 +30,10 @@ struct AdapterParams {
   const void* up;              // B
   const float* scale;          // of each group, or null: 1
   int* owner;                  // workspace: the group of each place that has one,
-  float* h;                    // scale h in fp32, places x rank,
-  void* hp;                    // or as 16-bit numbers, places x pieces x rank,
+  float* h;                    // scale h, places x rank,
   float* part;                 // sums over parts of the contraction, splits x places x n
   int64_t up_group;
-  int rank, ldup, pieces;
+  int rank, ldup;
   int down_blocks, splits, part_k;
 };
 

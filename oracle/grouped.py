@@ -118,9 +118,8 @@ def combine_gradients(dout, X, slots, rows, weights, kind):
 
 def adapters(x, W, A, B, offsets, rows, scale, kind):
     """D (NaN in rows that no place leads to) and its bound.  The low-rank
-    term's own factor is held in fp32 or as numbers of the inputs' type that add
-    up to it: each is off by half a step, 2^-8 of what is left (bf16), so two by
-    2^-16 and three (for fp32 results) by 2^-24."""
+    term's own factor is an fp32 sum, scaled and held in fp32; as an operand it
+    may be off by 2^-38 of the row's largest besides."""
     places = x.shape[0] if rows is None else len(rows)
     r = np.arange(places) if rows is None else np.asarray(rows)
     K, R = W.shape[1], A.shape[1]
@@ -128,7 +127,6 @@ def adapters(x, W, A, B, offsets, rows, scale, kind):
     group = np.full(places, -1)
     for g, (a, b) in enumerate(_spans(offsets, places)):
         group[a:b] = g
-    held = 2.0 ** -24 if kind == "f32" else 2.0 ** -16
     for i in range(places):
         if not 0 <= r[i] < x.shape[0]:
             continue
@@ -137,8 +135,9 @@ def adapters(x, W, A, B, offsets, rows, scale, kind):
         err = 2 * (K + R + 16) * F32 * mag
         if g >= 0:
             h = scale[g] * (A[g] @ v)
-            eh = 2 * (K + 8) * (F32 * abs(scale[g]) * (np.abs(A[g]) @ np.abs(v)) + LOW) + \
-                (held + 2 * F32) * np.abs(h) + 2.0 ** -25 * (kind != "bf16")
+            s = abs(scale[g])
+            eh = 2 * (K + 8) * (F32 * s * (np.abs(A[g]) @ np.abs(v)) + (1 + s) * LOW) + \
+                2 * F32 * np.abs(h) + 2.0 ** -38 * np.abs(h).max()
             want = want + B[g] @ h
             err = err + np.abs(B[g]) @ eh + 2 * (K + R + 16) * F32 * (np.abs(B[g]) @ np.abs(h))
         D[r[i]] = want
