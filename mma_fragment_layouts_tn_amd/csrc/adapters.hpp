@@ -55,15 +55,9 @@ struct Pieces<__bf16> {
 template <>
 struct Pieces<_Float16> {
   static constexpr bool kScaled = true;
-  // Exponent of the factor's inverse: over what the lanes of a row hold, l, l ^
-  // 16, l ^ 32 and l ^ 48.
-  static __device__ __forceinline__ int scale_of(const float (&x)[8]) {
-    float top = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = __builtin_fabsf(x[e]);
-      top = fmaxf(top, a < INFINITY ? a : 0.0f);
-    }
+  // Exponent of the factor's inverse, from the largest magnitude of each of a
+  // row's lanes, l, l ^ 16, l ^ 32 and l ^ 48.
+  static __device__ __forceinline__ int scale_of(float top) {
     const att::Halves q = att::quarters(top);
     top = att::both_max(fmaxf(q.lower, q.upper));
     return (int)(__float_as_uint(top) >> 23) - 126 - 15;
@@ -284,22 +278,21 @@ __global__ void __launch_bounds__(64 * kFewWaves, 1) adapters_one(const AdapterP
   ((O*)p.g.d)[(int64_t)row * p.g.ldd + n] = (O)y;
 }
 
-// what adapters_rows leaves out: the pairs of B's numbers of which one is not
-// finite, for the place's columns n .. n + 3
+// What adapters_rows leaves out: the products of which a factor is not finite,
+// for the place's columns n .. n + 3 (else -0, which changes no sum).
 template <class T>
 __device__ __forceinline__ floatx4 rest(const AdapterParams& p, int place, int n) {
-  floatx4 low{0.0f, 0.0f, 0.0f, 0.0f};
+  floatx4 low{-0.0f, -0.0f, -0.0f, -0.0f};
   const int g = owner_of(p, place);
   if (g < 0) return low;
   const T* b = (const T*)p.up + g * p.up_group + (int64_t)n * p.ldup;
   const float* h = p.h + (int64_t)place * p.rank;
-  for (int c = 0; c < p.rank; c += 2) {
+  for (int c = 0; c < p.rank; ++c)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const float b0 = (float)b[v * p.ldup + c], b1 = (float)b[v * p.ldup + c + 1];
-      if (not_finite(b0) || not_finite(b1)) low[v] += h[c] * b0 + h[c + 1] * b1;
+      const float x = h[c], y = (float)b[v * p.ldup + c];
+      if (not_finite(x) || not_finite(y)) low[v] += x * y;
     }
-  }
   return low;
 }
 
@@ -353,8 +346,9 @@ __global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_row
 // a few matrix instructions more, on fragments straight from memory (a few KB
 // that every workgroup of a row of tiles reads): rows of other groups multiply B
 // by zeros, and 16 rows without one of the run are passed over.  bf16's add to
-// the tile's own sums; fp16's are scaled.  What is not finite in B is left out
-// there, so that it cannot reach other rows, and added to its own at the end.
+// the tile's own sums; fp16's are scaled.  What is not finite in B, which must
+// not reach those other rows, or in s_g h, of whose infinities the pieces would
+// make NaN, is left out there and added to the sums of its own rows afterwards.
 template <class T, class O, class C>
 __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem, int first,
                                               int count, int n0) {
@@ -380,7 +374,7 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
   // they are added.
   constexpr bool SCALED = Pieces<T>::kScaled;
   const int r = lane & 15, c8 = 8 * (lane >> 4);
-  bool bad = false;       // something in B that is not finite
+  bool bad = false;       // something was left out
   if (!SCALED) tied<C>(acc);
   // For 32 columns of the rank of a run: B, and s_g h of 16 rows at a time.  The
   // next ones are on their way while some are multiplied.
@@ -433,12 +427,26 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
     };
     auto use = [&](const Columns& b, const Rows& y, int i) {
       float left[8];
+      unsigned top = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) left[e] = __uint_as_float(y.x[e / 4][e % 4]);
+      for (int e = 0; e < 8; ++e) {
+        const unsigned u = y.x[e / 4][e % 4];
+        left[e] = __uint_as_float(u);
+        top = max(top, u & 0x7fffffffu);
+      }
+      if (__any(top >= 0x7f800000u)) {
+        bad = true;
+        top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          left[e] = not_finite(left[e]) ? 0.0f : left[e];
+          top = max(top, __float_as_uint(left[e]) & 0x7fffffffu);
+        }
+      }
       floatx4 low[RN];
       int ex = 0;
       if constexpr (SCALED) {
-        ex = Pieces<T>::scale_of(left);
+        ex = Pieces<T>::scale_of(__uint_as_float(top));
 #pragma unroll
         for (int e = 0; e < 8; ++e) left[e] = __builtin_amdgcn_ldexpf(left[e], -ex);
 #pragma unroll
@@ -447,9 +455,6 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
 #pragma unroll
       for (int v = 0; v < kPieces; ++v) {
         const Vec8<T> piece = Pieces<T>::take(left);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)      // (of an infinity nothing is left)
-          if (v == 0) left[e] = not_finite(left[e]) ? 0.0f : left[e];
 #pragma unroll
         for (int j = 0; j < RN; ++j) {
           if constexpr (SCALED)
@@ -503,26 +508,25 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
     }
   }
   if (!SCALED) settled<C>(acc);
-  auto row_of = [&](int m) {
+  if (__any(bad))
+#pragma unroll 1
+    for (int x = 0; x < C::RM * RN; ++x) {
+      const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of(lane, x % RN);
+      floatx4 y{-0.0f, -0.0f, -0.0f, -0.0f};
+      if (m < count && n < g.n) y = rest<T>(p, first + m, n);
+#pragma unroll
+      for (int i = 0; i < C::RM; ++i)
+#pragma unroll
+        for (int j = 0; j < RN; ++j)
+        {
+          if (x == RN * i + j) acc[i][j] += y;
+          asm volatile("" : "+a"(acc[i][j]));
+        }
+    }
+  store_rows<O, C, true>(acc, n0, g.n, w, lane, [&](int m) {
     const int row = m < count ? row_at(g, first + m) : -1;
     return row < 0 ? nullptr : (O*)g.d + (int64_t)row * g.ldd;
-  };
-  store_rows<O, C, true>(acc, n0, g.n, w, lane, row_of);
-  if (!__any(bad)) return;
-  // Each lane adds to the results of its sums, which lanes of this wave have
-  // stored (a sum with an infinity or NaN does not depend on the rounding of its
-  // finite part).
-  __threadfence_block();
-#pragma unroll 1
-  for (int x = 0; x < C::RM * RN; ++x) {
-    const int m = m0 - first + 16 * (x / RN) + r, n = nw + column_of(lane, x % RN);
-    O* row = row_of(m);
-    if (!row || n >= g.n) continue;
-    floatx4 y = rest<T>(p, first + m, n);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) y[v] += (float)row[n + v];
-    Out<O>::store4(row + n, y);
-  }
+  });
 }
 
 template <class T, class O, class S>
