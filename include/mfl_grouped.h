@@ -14,8 +14,9 @@
  * them 0, growing: group g owns the places offsets[g] .. offsets[g + 1] - 1;
  * groups without places are allowed.  r_i is rows[i] (device memory), or i
  * where rows is NULL.  The kernels hold offsets inside [0, places] whatever
- * they are (of those that then do not grow the results are undefined); a row number outside A counts as a row of zeros.  Places behind
- * the last group belong to none.
+ * they are (of those that then do not grow the results are undefined); a row
+ * number outside A counts as a row of zeros.  Places behind the last group belong
+ * to none.
  *
  * Types.  A, B and their gradients' inputs are all MFL_F16 or all MFL_BF16;
  * D and dB are of that type or MFL_F32.  Products are summed in fp32 and

@@ -130,6 +130,10 @@ Choice with(KernelRef k, int algo, const mfl_grouped_t& a, int64_t n) {
 //       32  200  1024   256   59    10   14  counts where a tile is a few steps,
 //        8  200  4096  4096    -    86   96  and where a little over half of one
 //       32  200  1024  4096    -    95  111  round of 256's tiles cannot be cut
+//
+// The rule gives two of these rows to the slower kernel: 8 of 48 by 1024 x 256 to
+// 128, for 0.3 us, and the last to 256 (`round` is 164 there, beyond 5/8 of the
+// 256; on another device 106 us, 99 by 128).
 int choose_algo(int64_t places, int64_t groups, int64_t n, int64_t k, bool few) {
   const int64_t mean = ceil_div(places, groups), held = places < groups ? places : groups,
                 across = ceil_div(n, 256), tiles = held * across;

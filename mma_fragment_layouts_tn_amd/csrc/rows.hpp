@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(64 * W) group_place(const SortParams p) {
 }
 
 // ---------------------------------------------------------- combine_rows
-typedef unsigned u32x4_r __attribute__((ext_vector_type(4)));
 template <class T>
 struct Eight {
   typedef T vec __attribute__((ext_vector_type(8)));
