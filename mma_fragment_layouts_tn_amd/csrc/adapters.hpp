@@ -349,6 +349,10 @@ __global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_row
 // the tile's own sums; fp16's are scaled.  What is not finite in B, which must
 // not reach those other rows, or in s_g h, of whose infinities the pieces would
 // make NaN, is left out there and added to the sums of its own rows afterwards.
+// 5,001 rows of 4096 x 4096, fp16, with the down projection: 147 us without an
+// adapter, 167 with 8 of rank 16, 186 of rank 64.  (Three numbers of s_g h, the
+// scales and the sums cost less than it did to store numbers and form each run
+// twice: 182 -> 172 for rank 64 in bf16, the same run's 162 for rank 16.)
 template <class T, class O, class C>
 __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem, int first,
                                               int count, int n0) {
@@ -492,17 +496,20 @@ __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem
     };
     Step s = advance(Step{0, 0, -1, 0, run_starts(own[h], lane)});
     Columns b = load_b(s);
-    Rows y = load_h(s, 0);
+    Rows y = load_h(s, s.a / 16);
     while (s.group >= 0) {
       const Step to = advance(s);
       const Columns next = load_b(to);      // (of no step: nothing is read)
+      const Rows ahead = load_h(to, to.a / 16);
       finite(b);
 #pragma unroll
-      for (int i = 0; i < HM; ++i) {
-        const Rows then = i + 1 < HM ? load_h(s, i + 1) : load_h(to, 0);
-        if (16 * i < s.b && 16 * i + 16 > s.a) use(b, y, i);
-        y = then;
-      }
+      for (int i = 0; i < HM; ++i)
+        if (16 * i < s.b && 16 * i + 16 > s.a) {
+          const Rows then = load_h(s, i + 1);
+          use(b, y, i);
+          y = then;
+        }
+      y = ahead;
       b = next;
       s = to;
     }
