@@ -272,18 +272,21 @@ Choice few_down(const mfl_adapters_t& a, Choice* all) {
 }
 // The kernel: FEW as long as both find room in one round, or nearly, and the
 // down projection of the requests does where each has an adapter of its own.
-// Microseconds, bf16, weights from memory; tiles of both:
+// Microseconds, bf16, x and weights from memory; tiles of both:
 //
 //   rows  adapters  rank    n     k          FEW  TILE
-//    192         1    16 4096  4096  192+14   46    45
-//    300         4    16 1024  1024   80+23   16    21
-//    500         4    32 1024  1024  128+72   21    21
-//   1000         4    16  256  4096   64+67   25    39
-//   2000         4    16  256  4096  128+130  39    39
-//   1000         4    64  256  1024   64+268  25    25
-//     64        64    64 1024  4096   16+272  50    67
-//    128        64    64 4096  4096  128+292  72    67
-//   1000         4    64   64  4096   16+268  50    42
+//    192         1    16 4096  4096  192+14   46    48
+//    300         4    16 1024  1024   80+23   15    19
+//    500         4    32 1024  1024  128+72   20    20
+//   1000         4    16  256  4096   64+67   26    46
+//   2000         4    16  256  4096  128+130  40    45
+//   1000         4    64  256  1024   64+268  25    23
+//     64        64    64 1024  4096   16+272  52    72
+//    128        64    64 4096  4096  128+292  74    69
+//   1000         4    64   64  4096   16+268  51    47
+//
+// (The first and the fifth row go to TILE, a few workgroups beyond the rule; with
+// x in the caches that is the faster one there, 45 and 39.)
 int adapters_algo(const mfl_adapters_t& a) {
   Choice all;
   const int64_t down = few_down(a, &all).blocks(), tiles = all.blocks(), sum = tiles + down;
