@@ -350,9 +350,8 @@ __global__ void __launch_bounds__(kDownParts * DownTile::T, 1) adapters_down_row
 // not reach those other rows, or in s_g h, of whose infinities the pieces would
 // make NaN, is left out there and added to the sums of its own rows afterwards.
 // 5,001 rows of 4096 x 4096, fp16, with the down projection: 147 us without an
-// adapter, 167 with 8 of rank 16, 186 of rank 64.  (Three numbers of s_g h, the
-// scales and the sums cost less than it did to store numbers and form each run
-// twice: 182 -> 172 for rank 64 in bf16, the same run's 162 for rank 16.)
+// adapter, 167 with 8 of rank 16, 186 of rank 64.  (s_g h as two 16-bit numbers,
+// stored and read back, takes as long: bf16, rank 64, 172 us and 171.)
 template <class T, class O, class C>
 __device__ __forceinline__ void adapters_tile(const AdapterParams& p, char* smem, int first,
                                               int count, int n0) {
